@@ -30,12 +30,20 @@ BEAM_OK, BEAM_ERR_NULL, BEAM_ERR_CONFIG, BEAM_ERR_SHAPE = 0, 1, 2, 3
 BEAM_ERR_DTYPE, BEAM_ERR_ALIGN, BEAM_ERR_WORKSPACE, BEAM_ERR_HIP = 4, 5, 6, 7
 BEAM_F32, BEAM_BF16, BEAM_FP8_E4M3, BEAM_MXFP4, BEAM_E8M0 = 0, 1, 2, 3, 4
 BEAM_LAYOUT_ROW_MAJOR, BEAM_LAYOUT_PACKED = 0, 1
+BEAM_QUANT_NONE, BEAM_QUANT_ROW, BEAM_QUANT_BLOCK = 0, 1, 2
+BEAM_SCORE_SIGMOID, BEAM_SCORE_SOFTMAX = 0, 1
+BEAM_GROUP_TOP2, BEAM_GROUP_MAX = 0, 1
+BEAM_X_E4M3_ROW, BEAM_X_E4M3_BLOCK, BEAM_X_MXFP4 = 0, 1, 2
 
 EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route", "beam_moe_forward",
             "beam_moe_forward_residual", "beam_moe_status_string", "beam_moe_profile_begin",
             "beam_moe_profile_end", "beam_moe_pack_weights", "beam_moe_backward_workspace_bytes",
             "beam_moe_backward", "beam_moe_pack_weights_transposed", "beam_moe_update_bias",
-            "beam_moe_forward_shard", "beam_moe_forward_noalloc")
+            "beam_moe_forward_shard", "beam_moe_forward_noalloc", "beam_moe_add_rms_norm",
+            "beam_moe_add_rms_norm_backward_workspace_bytes", "beam_moe_add_rms_norm_backward",
+            "beam_moe_gate", "beam_moe_gate_backward", "beam_moe_mx4_quantize",
+            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear_workspace_bytes",
+            "beam_moe_mx4_linear")
 
 # Scratch size of beam_moe_forward_noalloc (BEAM_MOE_NOALLOC_MAX_BYTES in the header)
 NOALLOC_MAX_BYTES = 64 << 20
@@ -76,6 +84,40 @@ class BeamMoeGrads(ctypes.Structure):
         ("d_w_gate", ctypes.c_void_p),
         ("d_w_up", ctypes.c_void_p),
         ("d_w_down", ctypes.c_void_p),
+    ]
+
+
+class BeamMoeNorm(ctypes.Structure):
+    _fields_ = [
+        ("hidden", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32),
+        ("keep", ctypes.c_float),
+        ("add", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("quant", ctypes.c_int32),
+    ]
+
+
+class BeamMoeGateConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_experts", ctypes.c_int32),
+        ("n_group", ctypes.c_int32),
+        ("topk_group", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("z_dtype", ctypes.c_int32),
+        ("routed_scaling_factor", ctypes.c_float),
+    ]
+
+
+class BeamMoeLinear(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("x_format", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
     ]
 
 
@@ -132,6 +174,24 @@ def lib():
         L.beam_moe_pack_weights_transposed.restype = ctypes.c_int
         L.beam_moe_update_bias.argtypes = [vp, vp, i32, ctypes.c_float, vp]
         L.beam_moe_update_bias.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        normp, gatep = ctypes.POINTER(BeamMoeNorm), ctypes.POINTER(BeamMoeGateConfig)
+        linp = ctypes.POINTER(BeamMoeLinear)
+        L.beam_moe_add_rms_norm.argtypes = [normp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.beam_moe_add_rms_norm_backward_workspace_bytes.argtypes = [normp, i32]
+        L.beam_moe_add_rms_norm_backward_workspace_bytes.restype = sz
+        L.beam_moe_add_rms_norm_backward.argtypes = [normp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                     sz, vp]
+        L.beam_moe_gate.argtypes = [gatep, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.beam_moe_gate_backward.argtypes = [gatep, i32, vp, vp, vp, vp, vp]
+        L.beam_moe_mx4_quantize.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp]
+        L.beam_moe_mx4_dequantize.argtypes = [vp, vp, i64, i32, i32, vp, vp]
+        L.beam_moe_mx4_linear_workspace_bytes.argtypes = [linp, i32]
+        L.beam_moe_mx4_linear_workspace_bytes.restype = sz
+        L.beam_moe_mx4_linear.argtypes = [linp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        for name in ("add_rms_norm", "add_rms_norm_backward", "gate", "gate_backward",
+                     "mx4_quantize", "mx4_dequantize", "mx4_linear"):
+            getattr(L, "beam_moe_" + name).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -501,6 +561,269 @@ def update_bias(expert_bias, expert_counts, gamma, stream=None):
     if st != BEAM_OK:
         raise BeamMoeError(st, "beam_moe_update_bias")
     return expert_bias
+
+
+class _Here:
+    """The context of a call on the current device and stream: nothing to switch."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE_CTX = _Here()
+
+
+def _on(device, stream):
+    """The context in which a call allocates and launches: ``stream``, else the
+    current stream of the tensors' device (made current if another device is)."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}, expected a GPU")
+    if stream is None:
+        return _HERE_CTX if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _launch(where, device, fn, *args):
+    """Calls the library on the current stream of ``device``."""
+    st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != BEAM_OK:
+        raise BeamMoeError(st, where)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def add_rms_norm(x, norm_weight, *, stream_in=None, keep=1.0, add=1.0, norm_eps=1e-6, quant=None,
+                 return_y=True, stream_out=None, stream=None):
+    """The residual's addition and the RMS norm of the sum, in one pass:
+    s = keep * stream_in + add * x (add * x without ``stream_in``), y = s /
+    sqrt(mean(s^2) + norm_eps) * norm_weight, from the unrounded s.
+
+    x and stream_in [T, H] bf16 or fp32, norm_weight [H] fp32. Returns dict(
+    stream_out: s in x's dtype (None without stream_in; ``stream_out`` may be
+    given, also x or stream_in itself), y: in x's dtype (None without
+    ``return_y``), q, q_scale: with ``quant`` the E4M3 codes of y and their
+    scales, "row": fp32 [T], amax / 448, or "block": E8M0 bytes [T, H / 32]
+    (uint8), for mx4_linear(); else None)."""
+    T, H = x.shape
+    dev = x.device
+    if quant not in _QUANTS:
+        raise ValueError(f"quant is {quant!r}, expected None, 'row' or 'block'")
+    _check(x, "x", (T, H), _FLOATS, dev)
+    _check(norm_weight, "norm_weight", (H,), _F32, dev)
+    for t, name in ((stream_in, "stream_in"), (stream_out, "stream_out")):
+        if t is not None:
+            _check(t, name, (T, H), (x.dtype,), dev)
+    cfg = BeamMoeNorm(H, _X_DTYPES[x.dtype], keep, add, norm_eps, _QUANTS[quant])
+    y = q = scale = None
+    with _on(dev, stream):
+        if stream_out is None and stream_in is not None:
+            stream_out = torch.empty_like(x)
+        if return_y:
+            y = torch.empty_like(x)
+        if quant is not None:
+            q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
+            scale = (torch.empty(T, dtype=torch.float32, device=dev) if quant == "row" else
+                     torch.empty((T, H // 32), dtype=torch.uint8, device=dev))
+        _launch("beam_moe_add_rms_norm", dev, lib().beam_moe_add_rms_norm, ctypes.byref(cfg), T,
+                _p(x), _p(stream_in), _p(norm_weight), _p(stream_out), _p(y), _p(q), _p(scale))
+    return {"stream_out": stream_out, "y": y, "q": q, "q_scale": scale}
+
+
+def add_rms_norm_backward(dy, s, norm_weight, *, d_stream_out=None, keep=1.0, add=1.0,
+                          norm_eps=1e-6, stream_grad=True, weight_grad=True, workspace=None,
+                          stream=None):
+    """Gradients of add_rms_norm() from its stored sum ``s`` (stream_out; x
+    itself without stream_in and with add = 1), the gradient ``dy`` of y and,
+    where the sum is used further, ``d_stream_out`` of the sum. Returns dict(
+    dx, d_stream_in: [T, H] in dy's dtype (d_stream_in is None without
+    ``stream_grad``, and is dx itself where keep == add), d_norm_weight: [H]
+    fp32, None without ``weight_grad``)."""
+    T, H = dy.shape
+    dev = dy.device
+    _check(dy, "dy", (T, H), _FLOATS, dev)
+    _check(s, "s", (T, H), (dy.dtype,), dev)
+    _check(norm_weight, "norm_weight", (H,), _F32, dev)
+    if d_stream_out is not None:
+        _check(d_stream_out, "d_stream_out", (T, H), (dy.dtype,), dev)
+    cfg = BeamMoeNorm(H, _X_DTYPES[dy.dtype], keep, add, norm_eps, BEAM_QUANT_NONE)
+    d_in = dw = None
+    with _on(dev, stream):
+        dx = torch.empty_like(dy)
+        if stream_grad and keep != add:
+            d_in = torch.empty_like(dy)
+        if weight_grad:
+            # no rows: the sum over them is 0
+            dw = (torch.empty if T else torch.zeros)(H, dtype=torch.float32, device=dev)
+            need = int(lib().beam_moe_add_rms_norm_backward_workspace_bytes(ctypes.byref(cfg), T))
+            workspace = _scratch(workspace, need, dev)
+        else:
+            workspace = None
+        _launch("beam_moe_add_rms_norm_backward", dev, lib().beam_moe_add_rms_norm_backward,
+                ctypes.byref(cfg), T, _p(dy), _p(s), _p(norm_weight), _p(d_stream_out), _p(dx),
+                _p(d_in), _p(dw), _p(workspace), 0 if workspace is None else workspace.numel())
+    return {"dx": dx, "d_stream_in": dx if stream_grad and d_in is None else d_in,
+            "d_norm_weight": dw}
+
+
+def gate(logits, *, top_k, expert_bias=None, score="sigmoid", n_group=1, topk_group=1,
+         group_score="top2", renormalise=True, routed_scaling_factor=1.0, valid=None,
+         return_counts=False, stream=None):
+    """Routing of given logits [T, E] (bf16 or fp32, E <= 1024): scores by
+    ``score`` ("sigmoid" or "softmax" over all experts), keys = scores +
+    ``expert_bias`` [E] fp32, the ``topk_group`` of ``n_group`` groups with the
+    best ``group_score`` ("top2": the sum of the two largest keys, "max"), the
+    ``top_k`` largest keys inside them, weights = routed_scaling_factor * score
+    (over the chosen scores' sum with ``renormalise``). ``valid`` [T] bool marks
+    the tokens that are none of the padding. Returns dict(topk_idx [T, k] int32
+    (-1 for padding), topk_w [T, k] fp32, expert_counts [E] int32 or None)."""
+    T, E = logits.shape
+    dev = logits.device
+    cfg = _gate_config(logits, top_k, score, n_group, topk_group, group_score, renormalise,
+                       routed_scaling_factor)
+    if expert_bias is not None:
+        _check(expert_bias, "expert_bias", (E,), _F32, dev)
+    if valid is not None:
+        _check(valid, "valid", (T,), (torch.bool, torch.uint8), dev)
+    counts = None
+    with _on(dev, stream):
+        idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        if return_counts:
+            counts = (torch.empty if T else torch.zeros)(E, dtype=torch.int32, device=dev)
+        _launch("beam_moe_gate", dev, lib().beam_moe_gate, ctypes.byref(cfg), T, _p(logits),
+                _p(expert_bias), _p(valid), _p(idx), _p(w), _p(counts))
+    return {"topk_idx": idx, "topk_w": w, "expert_counts": counts}
+
+
+def gate_backward(d_topk_w, logits, topk_idx, *, score="sigmoid", renormalise=True,
+                  routed_scaling_factor=1.0, stream=None):
+    """Gradient of the logits [T, E] (in their dtype) from the gradient
+    ``d_topk_w`` [T, k] fp32 of gate()'s weights and its ``topk_idx`` (a slot
+    with an index outside [0, E), as padding has, is empty)."""
+    T, E = logits.shape
+    dev = logits.device
+    k = d_topk_w.shape[-1]
+    cfg = _gate_config(logits, k, score, 1, 1, "max", renormalise, routed_scaling_factor)
+    _check(d_topk_w, "d_topk_w", (T, k), _F32, dev)
+    _check(topk_idx, "topk_idx", (T, k), (torch.int32,), dev)
+    with _on(dev, stream):
+        dz = torch.empty_like(logits)
+        _launch("beam_moe_gate_backward", dev, lib().beam_moe_gate_backward, ctypes.byref(cfg), T,
+                _p(d_topk_w), _p(logits), _p(topk_idx), _p(dz))
+    return dz
+
+
+def _gate_config(logits, top_k, score, n_group, topk_group, group_score, renormalise, rsf):
+    if score not in _SCORES or group_score not in _GROUP_SCORES:
+        raise ValueError(f"score {score!r} / group_score {group_score!r}: expected one of "
+                         f"{tuple(_SCORES)} / {tuple(_GROUP_SCORES)}")
+    _check(logits, "logits", logits.shape, _FLOATS, logits.device)
+    return BeamMoeGateConfig(logits.shape[1], n_group, topk_group, top_k, _SCORES[score],
+                             _GROUP_SCORES[group_score], int(bool(renormalise)),
+                             _X_DTYPES[logits.dtype], rsf)
+
+
+def mx4_quantize(x, *, packed=False, stream=None):
+    """MXFP4 of rows x [..., C] (bf16 or fp32, C a multiple of 32): (codes
+    [..., C / 2], scales [..., C / 32]), uint8, row-major; what mx4_linear()
+    takes for weights or rows. With ``packed``, x [E, R, C] are expert weights
+    (R a multiple of 16, C of 512) and both come in the packed layout, as from
+    pack_weights() and pack_mx_scales(): forward(..., packed=True) takes them."""
+    dev = x.device
+    if x.dim() < 1 or (packed and x.dim() != 3):
+        raise ValueError("mx4_quantize needs rows [..., C], with packed [E, R, C]")
+    _check(x, "x", x.shape, _FLOATS, dev)
+    C = x.shape[-1]
+    if C == 0 or C % 32:
+        raise ValueError(f"x has rows of {C} values, expected a multiple of 32")
+    if packed and x.shape[1] % 16:
+        raise ValueError(f"x has {x.shape[1]} rows per expert, expected a multiple of 16")
+    with _on(dev, stream):
+        codes = torch.empty((*x.shape[:-1], C // 2), dtype=torch.uint8, device=dev)
+        scales = torch.empty((*x.shape[:-1], C // 32), dtype=torch.uint8, device=dev)
+        _launch("beam_moe_mx4_quantize", dev, lib().beam_moe_mx4_quantize, _p(x), x.numel() // C,
+                C, _X_DTYPES[x.dtype], BEAM_LAYOUT_PACKED if packed else BEAM_LAYOUT_ROW_MAJOR,
+                _p(codes), _p(scales))
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, *, dtype=torch.bfloat16, stream=None):
+    """The values [..., C] (bf16 or fp32, exact) of row-major MXFP4 codes
+    [..., C / 2] and scales [..., C / 32]."""
+    dev = codes.device
+    if dtype not in _X_DTYPES:
+        raise ValueError(f"dtype is {dtype}, expected one of {_FLOATS}")
+    C = 2 * codes.shape[-1]
+    if C == 0 or C % 32:
+        raise ValueError(f"codes have rows of {C} values, expected a multiple of 32")
+    _check(codes, "codes", codes.shape, _U8, dev)
+    _check(scales, "scales", (*codes.shape[:-1], C // 32), _U8, dev)
+    with _on(dev, stream):
+        out = torch.empty((*codes.shape[:-1], C), dtype=dtype, device=dev)
+        _launch("beam_moe_mx4_dequantize", dev, lib().beam_moe_mx4_dequantize, _p(codes),
+                _p(scales), out.numel() // C, C, _X_DTYPES[dtype], _p(out))
+    return out
+
+
+def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, workspace=None,
+               stream=None):
+    """x W^T with MXFP4 weights (row-major codes ``w`` [N, K / 2] and scales
+    ``w_scale`` [N, K / 32], as from mx4_quantize()). The token rows ``x`` are
+    E4M3 codes [T, K] (float8_e4m3fn) with ``x_scale`` fp32 [T] or E8M0 bytes
+    [T, K / 32], as from add_rms_norm(quant="row" / "block"), or MXFP4 codes
+    [T, K / 2] (uint8) with E8M0 bytes [T, K / 32]. Returns ``out`` [T, N]
+    (``out_dtype``, bf16 or fp32)."""
+    T = x.shape[0]
+    N, K = w.shape[0], 2 * w.shape[1]
+    dev = x.device
+    _check(w, "w", (N, K // 2), _U8, dev)
+    _check(w_scale, "w_scale", (N, K // 32), _U8, dev)
+    if x.dtype == torch.uint8:
+        fmt = BEAM_X_MXFP4
+        _check(x, "x", (T, K // 2), _U8, dev)
+    else:
+        fmt = BEAM_X_E4M3_ROW if x_scale.dtype == torch.float32 else BEAM_X_E4M3_BLOCK
+        _check(x, "x", (T, K), (torch.float8_e4m3fn, torch.uint8), dev)
+    if fmt == BEAM_X_E4M3_ROW:
+        _check(x_scale, "x_scale", (T,), _F32, dev)
+    else:
+        _check(x_scale, "x_scale", (T, K // 32), _U8, dev)
+    if out is not None:
+        out_dtype = out.dtype
+        _check(out, "out", (T, N), _FLOATS, dev)
+    if out_dtype not in _X_DTYPES:
+        raise ValueError(f"out_dtype is {out_dtype}, expected one of {_FLOATS}")
+    cfg = BeamMoeLinear(N, K, fmt, _X_DTYPES[out_dtype])
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, N), dtype=out_dtype, device=dev)
+        need = int(lib().beam_moe_mx4_linear_workspace_bytes(ctypes.byref(cfg), T))
+        workspace = _scratch(workspace, need, dev) if need else None
+        _launch("beam_moe_mx4_linear", dev, lib().beam_moe_mx4_linear, ctypes.byref(cfg), T, _p(x),
+                _p(x_scale), _p(w), _p(w_scale), _p(out), _p(workspace),
+                0 if workspace is None else workspace.numel())
+    return out
+
+
+def _scratch(workspace, need, device):
+    """The caller's workspace if it is large enough, else a new one."""
+    if workspace is None or workspace.numel() < need:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    _check(workspace, "workspace", workspace.shape, _U8, device)
+    return workspace
+
+
+_FLOATS, _F32, _U8 = tuple(_X_DTYPES), (torch.float32,), (torch.uint8,)
+_QUANTS = {None: BEAM_QUANT_NONE, "row": BEAM_QUANT_ROW, "block": BEAM_QUANT_BLOCK}
+_SCORES = {"sigmoid": BEAM_SCORE_SIGMOID, "softmax": BEAM_SCORE_SOFTMAX}
+_GROUP_SCORES = {"top2": BEAM_GROUP_TOP2, "max": BEAM_GROUP_MAX}
 
 
 def profile_begin(stages=STAGES):

@@ -1,0 +1,507 @@
+// RMS norm of the residual stream, with the stream's own update and an E4M3
+// output, and its gradient.
+//
+// Beam launch post ("Introducing Beam"), section "Residual Stream", and the
+// transformers model doc "Beam", section "Overview": every sublayer reads the
+// RMS norm of the stream (sandwich norm), the stream is depth scaled, and the
+// norm is computed in fp32 or better. Per row of H values:
+//   s = keep * stream_in + add * x        r = 1 / sqrt(mean(s^2) + eps)
+//   y = s r w
+// One pass over memory: a row stays in the registers of the threads that
+// loaded it from its load to its last use.
+#include "common.h"
+#include "operators.h"
+
+#include <algorithm>
+
+namespace beam {
+namespace {
+
+// ------------------------------------------------------------------ rows
+// A row is held by NT threads, V units of 8 values each. VEC (H a multiple of
+// 8, so every row is 16-byte aligned): unit j of thread i is the chunk
+// i + j NT, read and written 16 bytes at a time. Else: value u of unit j is
+// element i + (8 j + u) NT, one at a time, neighbours in neighbouring lanes.
+template <bool VEC>
+__device__ __forceinline__ int elem(int tid, int nt, int j, int u) {
+  return VEC ? (tid + j * nt) * 8 + u : tid + (j * 8 + u) * nt;
+}
+
+// 8 raw values of a row: bf16 pairs or fp32.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ float get(int u) const {
+    return (u & 1) ? __uint_as_float(v[u >> 1] & 0xffff0000u) : __uint_as_float(v[u >> 1] << 16);
+  }
+  __device__ __forceinline__ void set(int u, uint16_t b) {
+    if (u & 1)
+      v[u >> 1] |= (uint32_t)b << 16;
+    else
+      v[u >> 1] = b;
+  }
+  __device__ __forceinline__ void load(const uint16_t* p) { v = ld16(p); }
+};
+template <>
+struct Raw<float> {
+  u32x4 lo, hi;
+  __device__ __forceinline__ float get(int u) const {
+    return __uint_as_float(u < 4 ? lo[u & 3] : hi[u & 3]);
+  }
+  __device__ __forceinline__ void set(int u, float f) {
+    if (u < 4)
+      lo[u & 3] = __float_as_uint(f);
+    else
+      hi[u & 3] = __float_as_uint(f);
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    lo = ld16(p);
+    hi = ld16(p + 4);
+  }
+};
+
+// Unit j of the row at p; values past the row read as 0.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> load_unit(const T* p, int tid, int nt, int j, int H) {
+  Raw<T> r;
+  if constexpr (VEC) {
+    const int e = elem<true>(tid, nt, j, 0);
+    if (e < H) {
+      r.load(p + e);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) r.set(u, T(0));
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int e = elem<false>(tid, nt, j, u);
+      r.set(u, e < H ? p[e] : T(0));
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_unit(T* p, int tid, int nt, int j, int H, const float (&v)[8]) {
+  if constexpr (VEC) {
+    const int e = elem<true>(tid, nt, j, 0);
+    if (e >= H) return;
+    if constexpr (sizeof(T) == 2) {
+      st16(p + e, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                        pack_bf16x2(v[6], v[7])});
+    } else {
+      st16(p + e, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                        __float_as_uint(v[3])});
+      st16(p + e + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
+                            __float_as_uint(v[7])});
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int e = elem<false>(tid, nt, j, u);
+      if (e < H) store_value(p + e, v[u]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sums
+template <typename F>
+__device__ __forceinline__ F wave_sum(F v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+template <typename F>
+__device__ __forceinline__ F wave_amax(F v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    const F x = __shfl_xor(v, o);
+    v = x > v ? x : v;
+  }
+  return v;
+}
+
+// Sum / maximum over the row's waves, in every thread: wave results through
+// LDS in wave order (the same order for every thread and every run).
+template <bool MAX, typename F>
+__device__ __forceinline__ F row_reduce(F v, F* lds, int nwaves) {
+  v = MAX ? wave_amax(v) : wave_sum(v);
+  if (nwaves == 1) return v;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  F s = lds[0];
+  for (int i = 1; i < nwaves; ++i) s = MAX ? (lds[i] > s ? lds[i] : s) : s + lds[i];
+  return s;
+}
+
+// ------------------------------------------------------------------ E4M3
+// fp64 -> fp32 rounded to odd: the value cut after 24 bits, its last bit set
+// if anything was cut, so that a later rounding to few bits decides as from
+// the fp64 value itself. Below 2^-126 the result is 0 (far under half of the
+// smallest E4M3 value).
+__device__ __forceinline__ float round_to_odd(double d) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, d);
+  const uint32_t hi = (uint32_t)(b >> 32), lo = (uint32_t)b, mag = hi & 0x7fffffffu;
+  if (mag < (897u << 20)) return 0.0f;
+  const uint32_t sticky = (lo & 0x1fffffffu) ? 1u : 0u;
+  return __uint_as_float((hi & 0x80000000u) | ((mag - (896u << 20)) << 3) | (lo >> 29) | sticky);
+}
+
+// Eight values, each at most 448 in magnitude after the clamp, to E4M3 codes
+// (round to nearest even, one instruction per pair).
+__device__ __forceinline__ u32x2 e4m3x8(const float (&v)[8]) {
+  u32x2 out;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(v[4 * h + i], -448.0f), 448.0f);
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], w, true);
+    out[h] = (uint32_t)w;
+  }
+  return out;
+}
+
+// ------------------------------------------------------------------ forward
+// The 8-bit outputs are decided in fp64 (QUANT != 0): a code is the nearest
+// to the exact quotient, not to one with an fp32 rounding on either side of a
+// border. fp64 runs at the unpacked fp32 rate here and the kernel is bound by
+// memory. Without an 8-bit output everything is fp32.
+template <typename T, bool VEC, int V, int QUANT>
+__global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormArgs p, int nt) {
+  using F = typename std::conditional<QUANT != 0, double, float>::type;
+  __shared__ F lds[2][16];
+  const int nwaves = nt >> 6;
+  // rows of one wave: four of them in a workgroup
+  const int row = nt == 64 ? blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
+  if (row >= p.T) return;
+  const int tid = nt == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int H = p.H;
+  const size_t off = (size_t)row * H;
+
+  Raw<T> xr[V], sr[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    xr[j] = load_unit<T, VEC>((const T*)p.x + off, tid, nt, j, H);
+    if (p.stream_in) sr[j] = load_unit<T, VEC>((const T*)p.stream_in + off, tid, nt, j, H);
+  }
+  F s[V][8], sq = 0;
+  const F keep = p.keep, add = p.add;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      F h = add * (F)xr[j].get(u);
+      if (p.stream_in) h += keep * (F)sr[j].get(u);
+      s[j][u] = h;
+      sq += h * h;
+    }
+  if (p.stream_out) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = (float)s[j][u];
+      store_unit<VEC>((T*)p.stream_out + off, tid, nt, j, H, v);
+    }
+  }
+  sq = row_reduce<false>(sq, lds[0], nwaves);
+  F r;
+  if constexpr (QUANT)
+    r = 1.0 / sqrt(sq / H + (double)p.eps);
+  else
+    r = 1.0f / sqrtf(sq / H + p.eps);
+
+  // s becomes s w; y = r (s w)
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const Raw<float> w = load_unit<float, VEC>(p.w, tid, nt, j, H);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) s[j][u] *= (F)w.get(u);
+    if (p.y) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = (float)(s[j][u] * r);
+      store_unit<VEC>((T*)p.y + off, tid, nt, j, H, v);
+    }
+  }
+  if constexpr (QUANT == 1) {
+    // one scale per row, amax / 448; r is common to all of a row's values, so
+    // y 448 / amax|y| = (s w) 448 / amax|s w|
+    double m = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const double a = fabs(s[j][u]);
+        m = a > m ? a : m;
+      }
+    m = row_reduce<true>(m, lds[1], nwaves);
+    const double ym = m * r;
+    const bool zero = m == 0;
+    const double inv = zero ? 0.0 : 448.0 / m;
+    if (tid == 0) ((float*)p.q_scale)[row] = zero && ym == ym ? 1.0f : (float)(ym / 448.0);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = round_to_odd(s[j][u] * inv);
+      const u32x2 c = e4m3x8(v);
+      if constexpr (VEC) {
+        const int e = elem<true>(tid, nt, j, 0);
+        if (e < H) *reinterpret_cast<u32x2*>(p.q + off + e) = c;
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int e = elem<false>(tid, nt, j, u);
+          if (e < H) p.q[off + e] = (uint8_t)(c[u >> 2] >> (8 * (u & 3)));
+        }
+      }
+    }
+  }
+  if constexpr (QUANT == 2) {
+    // One E8M0 scale per 32 values (four neighbouring lanes): the power of two
+    // that brings the block's largest binade to E4M3's own, 2^8; values that
+    // still pass 448 become 448. The exponent of the maximum is the maximum of
+    // the exponents, so only the high words are compared.
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      double y[8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        y[u] = s[j][u] * r;
+        const uint32_t hi = (uint32_t)(__builtin_bit_cast(uint64_t, y[u]) >> 32) & 0x7fffffffu;
+        top = hi > top ? hi : top;
+      }
+      uint32_t o = __shfl_xor(top, 1);
+      top = o > top ? o : top;
+      o = __shfl_xor(top, 2);
+      top = o > top ? o : top;
+      const int be = (int)(top >> 20);  // biased exponent; 0x7ff: infinity or NaN in the block
+      const int e = min(max(be - 1023 - 8, -127), 127);
+      const double inv = __builtin_bit_cast(double, (uint64_t)(1023 - e) << 52);
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = round_to_odd(y[u] * inv);
+      u32x2 c = e4m3x8(v);
+      if (be == 0x7ff) c = u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
+      const int at = elem<true>(tid, nt, j, 0);
+      if (at < H) {
+        *reinterpret_cast<u32x2*>(p.q + off + at) = c;
+        if ((tid & 3) == 0)
+          ((uint8_t*)p.q_scale)[(size_t)row * (H / 32) + at / 32] =
+              be == 0x7ff ? (uint8_t)255 : (uint8_t)(e + 127);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ backward
+// With g = dy w and n = s r:
+//   ds = d_stream_out + r (g - n mean(g n)),  dx = add ds,  d_stream_in = keep ds,
+//   dw = sum over rows of dy n.
+// A workgroup walks the rows b, b + gridDim.x, ...; it keeps its partial dw in
+// registers over all of them and writes it once (norm_dw_kernel adds the
+// partials in order: no atomics).
+template <typename T, bool VEC, int V, bool DW>
+__global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
+  __shared__ float lds[2][2][16];  // double buffered over rows: one barrier per row
+  const int nwaves = nt >> 6;
+  const int per = nt == 64 ? (blockDim.x >> 6) : 1;  // rows side by side in the workgroup
+  const int tid = nt == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int first = nt == 64 ? blockIdx.x * per + (threadIdx.x >> 6) : blockIdx.x;
+  const int H = p.H;
+
+  Raw<float> w[V];
+  float dw[DW ? V : 1][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    w[j] = load_unit<float, VEC>(p.w, tid, nt, j, H);
+    if (DW)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) dw[DW ? j : 0][u] = 0.f;
+  }
+  int buf = 0;
+  for (int row = first; row < p.T; row += gridDim.x * per, buf ^= 1) {
+    const size_t off = (size_t)row * H;
+    Raw<T> s[V], dy[V], d[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      s[j] = load_unit<T, VEC>((const T*)p.s + off, tid, nt, j, H);
+      dy[j] = load_unit<T, VEC>((const T*)p.dy + off, tid, nt, j, H);
+      if (p.d_stream_out) d[j] = load_unit<T, VEC>((const T*)p.d_stream_out + off, tid, nt, j, H);
+    }
+    float sq = 0.f, gs = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float sv = s[j].get(u);
+        sq += sv * sv;
+        gs += dy[j].get(u) * w[j].get(u) * sv;
+      }
+    sq = wave_sum(sq);
+    gs = wave_sum(gs);
+    if (nwaves > 1) {
+      if ((threadIdx.x & 63) == 0) {
+        lds[buf][0][threadIdx.x >> 6] = sq;
+        lds[buf][1][threadIdx.x >> 6] = gs;
+      }
+      __syncthreads();
+      sq = lds[buf][0][0];
+      gs = lds[buf][1][0];
+      for (int i = 1; i < nwaves; ++i) {
+        sq += lds[buf][0][i];
+        gs += lds[buf][1][i];
+      }
+    }
+    const float r = 1.0f / sqrtf(sq / H + p.eps);
+    const float c = gs * r / H;  // mean(g n)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float a[8], b[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float n = s[j].get(u) * r, g = dy[j].get(u);
+        float ds = r * (g * w[j].get(u) - n * c);
+        if (p.d_stream_out) ds += d[j].get(u);
+        if (DW) dw[DW ? j : 0][u] += g * n;
+        a[u] = p.add * ds;
+        b[u] = p.keep * ds;
+      }
+      store_unit<VEC>((T*)p.dx + off, tid, nt, j, H, a);
+      if (p.d_stream_in) store_unit<VEC>((T*)p.d_stream_in + off, tid, nt, j, H, b);
+    }
+  }
+  if (DW) {
+    // rows side by side have partials of their own
+    float* out = p.part + (size_t)(nt == 64 ? first : (int)blockIdx.x) * H;
+#pragma unroll
+    for (int j = 0; j < V; ++j) store_unit<VEC>(out, tid, nt, j, H, dw[DW ? j : 0]);
+  }
+}
+
+// dw[c] = sum over the groups of part[group, c]: 64 columns per workgroup, its
+// 16 waves take every 16th group, their sums are added in wave order.
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int groups,
+                                                       int H, float* __restrict__ dw) {
+  __shared__ float lds[16][64];
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), wv = threadIdx.x >> 6;
+  float s = 0.f;
+  if (c < H)
+    for (int g = wv; g < groups; g += 16) s += part[(size_t)g * H + c];
+  lds[wv][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (wv == 0 && c < H) {
+    for (int i = 1; i < 16; ++i) s += lds[i][threadIdx.x];
+    dw[c] = s;
+  }
+}
+
+// ------------------------------------------------------------------ launch shape
+// Threads of a row and units of 8 values per thread: the fewest units (1, 2,
+// 4, 8) whose threads, a whole number of waves, are at most `most`.
+struct RowShape {
+  int nt, v;
+};
+RowShape row_shape(int H, int most) {
+  const int units = (H + 7) / 8;
+  int v = 1;
+  while (v < 8 && (units + v - 1) / v > most) v *= 2;
+  const int nt = ((units + v - 1) / v + 63) / 64 * 64;
+  return {nt, v};
+}
+
+template <typename T, bool VEC, int V>
+void norm_launch(const NormArgs& a, int quant, int nt, hipStream_t st) {
+  const int threads = nt == 64 ? 256 : nt;
+  const int grid = nt == 64 ? (a.T + 3) / 4 : a.T;
+  if (quant == 0)
+    add_rms_norm_kernel<T, VEC, V, 0><<<grid, threads, 0, st>>>(a, nt);
+  else if (quant == 1)
+    add_rms_norm_kernel<T, VEC, V, 1><<<grid, threads, 0, st>>>(a, nt);
+  else if constexpr (VEC)
+    add_rms_norm_kernel<T, true, V, 2><<<grid, threads, 0, st>>>(a, nt);
+}
+
+template <typename T, bool VEC>
+void norm_units(const NormArgs& a, int quant, RowShape rs, hipStream_t st) {
+  if (rs.v == 1)
+    norm_launch<T, VEC, 1>(a, quant, rs.nt, st);
+  else if (rs.v == 2)
+    norm_launch<T, VEC, 2>(a, quant, rs.nt, st);
+  else if (rs.v == 4)
+    norm_launch<T, VEC, 4>(a, quant, rs.nt, st);
+  else
+    norm_launch<T, VEC, 8>(a, quant, rs.nt, st);
+}
+
+template <typename T, bool VEC, int V>
+void bwd_launch(const NormBwdArgs& a, int nt, int grid, hipStream_t st) {
+  const int threads = nt == 64 ? 256 : nt;
+  if (a.part)
+    add_rms_norm_bwd_kernel<T, VEC, V, true><<<grid, threads, 0, st>>>(a, nt);
+  else
+    add_rms_norm_bwd_kernel<T, VEC, V, false><<<grid, threads, 0, st>>>(a, nt);
+}
+
+template <typename T, bool VEC>
+void bwd_units(const NormBwdArgs& a, RowShape rs, int grid, hipStream_t st) {
+  if (rs.v == 1)
+    bwd_launch<T, VEC, 1>(a, rs.nt, grid, st);
+  else if (rs.v == 2)
+    bwd_launch<T, VEC, 2>(a, rs.nt, grid, st);
+  else if (rs.v == 4)
+    bwd_launch<T, VEC, 4>(a, rs.nt, grid, st);
+  else
+    bwd_launch<T, VEC, 8>(a, rs.nt, grid, st);
+}
+
+constexpr int kNormThreads = 512;     // threads of a row before it takes more units
+constexpr int kNormBwdGroups = 1024;  // partial weight gradients
+
+}  // namespace
+
+hipError_t launch_add_rms_norm(const NormArgs& a, int f32, int quant, hipStream_t st) {
+  RowShape rs = row_shape(a.H, kNormThreads);
+  if (rs.nt > 1024) return hipErrorInvalidValue;
+  const bool vec = a.H % 8 == 0;
+  if (f32)
+    vec ? norm_units<float, true>(a, quant, rs, st) : norm_units<float, false>(a, quant, rs, st);
+  else
+    vec ? norm_units<uint16_t, true>(a, quant, rs, st) : norm_units<uint16_t, false>(a, quant, rs, st);
+  return hipGetLastError();
+}
+
+int norm_bwd_groups(int T, int H) {
+  const RowShape rs = row_shape(H, kNormThreads);
+  const int per = rs.nt == 64 ? 4 : 1;
+  return std::min((T + per - 1) / per, kNormBwdGroups / per) * per;
+}
+
+hipError_t launch_add_rms_norm_backward(const NormBwdArgs& a, int f32, hipStream_t st) {
+  RowShape rs = row_shape(a.H, kNormThreads);
+  if (rs.nt > 1024) return hipErrorInvalidValue;
+  const int per = rs.nt == 64 ? 4 : 1;
+  const int groups = norm_bwd_groups(a.T, a.H);
+  const int grid = a.part ? groups / per : (a.T + per - 1) / per;
+  const bool vec = a.H % 8 == 0;
+  if (f32)
+    vec ? bwd_units<float, true>(a, rs, grid, st) : bwd_units<float, false>(a, rs, grid, st);
+  else
+    vec ? bwd_units<uint16_t, true>(a, rs, grid, st) : bwd_units<uint16_t, false>(a, rs, grid, st);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.part) return e;
+  norm_dw_kernel<<<(a.H + 63) / 64, 1024, 0, st>>>(a.part, groups, a.H, a.dw);
+  return hipGetLastError();
+}
+
+}  // namespace beam

@@ -40,3 +40,5 @@ from . import e4m3  # noqa: F401
 from . import mxfp4  # noqa: F401
 from . import residual  # noqa: F401
 from . import backward  # noqa: F401
+from . import norm  # noqa: F401
+from . import gate  # noqa: F401

@@ -1,0 +1,295 @@
+"""GPU parity of MXFP4 quantisation, values and the dense product, against
+oracle.mxfp4 and float64 products of the exact values.
+
+Codes, scales and values are exact and have to be equal. In the product the
+matrix cores add a step's products in groups of 8 along the reduction: the
+terms of a group are aligned to its largest product and cut 13 bits below that
+product's leading bit (measured with single products: 2^10 + 2^-3 keeps the
+small term, 2^10 + 2^-4 drops it, in the same group of 8 only), and groups, steps
+and the running sum are added in fp32. So a group is less than 7 units of 2^-13
+of its largest product off: exactly 0 for E2M1 x E2M1, whose products are
+multiples of 2^-2 below 2^6, in blocks of one scale. The fp32 additions are K / 8
+groups, each at most one step (2^-23) of the sum of magnitudes off, if they went
+one after the other; splits of the reduction add fewer than 64 more. Then one
+rounding to the output type (bf16 2^-8, fp32 2^-24) and, with row scales, one
+for the scale (2^-24).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import group_limited_routing_amd as gl
+import oracle
+import workloads
+from parity import Guarded
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _dev():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    return torch.device("cuda:0")
+
+
+def _rand(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed))
+
+
+def _bytes(shape, seed, lo=0, hi=256):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randint(lo, hi, shape, generator=g, dtype=torch.int32).to(torch.uint8).to(_dev())
+
+
+def _oracle_quantize(x):
+    codes, scales = oracle.mxfp4.quantize_blocks(x.cpu().double().numpy())
+    return oracle.mxfp4.pack_nibbles(codes), scales
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,C", [(1, 32), (3, 64), (7, 96), (33, 160), (16, 512), (65, 5120)])
+def test_quantize_values(R, C, dtype):
+    x = (_rand((R, C), 61) * torch.exp(3 * _rand((R, 1), 62))).to(DT[dtype])
+    x[0, :32] = 0.0
+    codes, scales = gl.mx4_quantize(x.to(_dev()))
+    ref, sc = _oracle_quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), sc) and np.array_equal(codes.cpu().numpy(), ref)
+    for out in DT.values():
+        v = gl.mx4_dequantize(codes, scales, dtype=out)
+        assert v.dtype == out and np.array_equal(v.cpu().double().numpy(), oracle.mxfp4.dequantize(ref, sc))
+
+
+def test_quantize_borders():
+    """Every border between two codes, the values next to it on both sides, and
+    every power of two, with a 4 in the block to fix its scale at 1."""
+    m = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.9999995]
+    v = []
+    for a in m:
+        a = np.float32(a)
+        v += [a, np.nextafter(a, np.float32(0)), np.nextafter(a, np.float32(8))]
+    v = [min(a, np.float32(7.9999995)) for a in v] + [2.0 ** -i for i in range(1, 31)]
+    v = np.array(v + [-a for a in v] + [-0.0], dtype=np.float32)
+    x = np.zeros((len(v) // 31 + 1, 32), dtype=np.float32)
+    x[:, 0] = 4.0
+    for i, a in enumerate(v):
+        x[i // 31, 1 + i % 31] = a
+    x = np.concatenate([np.ldexp(x, e).astype(np.float32) for e in (-100, -3, 0, 1, 60, 120)])
+    x = torch.from_numpy(x)
+    codes, scales = gl.mx4_quantize(x.to(_dev()))
+    ref, sc = _oracle_quantize(x)
+    assert np.array_equal(scales.cpu().numpy(), sc) and np.array_equal(codes.cpu().numpy(), ref)
+
+
+def test_quantize_range_ends():
+    """Blocks at the ends of fp32's range: subnormals take the smallest scale,
+    the largest finite number a scale below the top; infinities and NaN."""
+    x = torch.zeros((8, 32))
+    tiny = 2.0 ** -149
+    x[0, 3] = tiny
+    x[1] = torch.arange(32) * 2.0 ** -131
+    x[2, 0], x[2, 1] = 2.0 ** -126, -(2.0 ** -127)
+    x[3] = torch.finfo(torch.float32).max
+    x[4, 5] = float("inf")
+    x[5, 6] = float("nan")
+    x[6, 0], x[6, 1] = 2.0 ** -125, 2.0 ** -128
+    x[7, :2] = torch.tensor([-float("inf"), 1.0])
+    codes, scales = gl.mx4_quantize(x.to(_dev()))
+    good = [0, 1, 2, 3, 6]
+    ref, sc = _oracle_quantize(x[good])
+    assert np.array_equal(scales.cpu().numpy()[good], sc)
+    assert np.array_equal(codes.cpu().numpy()[good], ref)
+    assert (scales[[4, 5, 7]] == 255).all() and (codes[[4, 5, 7]] == 0).all()
+    assert torch.isnan(gl.mx4_dequantize(codes, scales)[[4, 5, 7]]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dequantize_every_code_and_scale(dtype):
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat(1, 1).view(16, 16)
+    codes = codes.repeat(256, 1).to(_dev())                       # [4096, 16]: 256 x all bytes
+    scales = torch.arange(256, dtype=torch.int32).to(torch.uint8).repeat_interleave(16).view(-1, 1).to(_dev())
+    got = gl.mx4_dequantize(codes, scales, dtype=DT[dtype]).cpu().double().numpy()
+    ref = oracle.mxfp4.dequantize(codes.cpu().numpy(), scales.cpu().numpy())
+    assert np.isnan(got[-16:]).all()
+    got, ref = got[:-16], ref[:-16]
+    big = np.abs(ref) > float(torch.finfo(DT[dtype]).max)
+    assert np.array_equal(got[~big], ref[~big]) and np.array_equal(got[big], np.sign(ref[big]) * np.inf)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_packed(dtype):
+    """The packed form is the packed copy of the row-major one."""
+    x = _rand((3, 48, 1024), 63).to(DT[dtype]).to(_dev())
+    codes, scales = gl.mx4_quantize(x)
+    pc, ps = gl.mx4_quantize(x, packed=True)
+    assert torch.equal(pc, gl.pack_weights(codes)) and torch.equal(ps, gl.pack_mx_scales(scales))
+
+
+def test_quantized_experts_run_the_block():
+    """Expert weights quantised into the packed layout run the block with the
+    same output, bit for bit, as row-major codes packed afterwards; the codes
+    of the first and last expert are the oracle's."""
+    dev = _dev()
+    cfg = dict(workloads.BEAM, T=40, hidden=512, intermediate=512, x_dtype="bf16", bias="normal",
+               w_dtype="bf16")
+    x, rw, b = (t.to(dev) for t in workloads.make_small_inputs(cfg, 64))
+    w = workloads.make_expert_weights(cfg, 64, dev)
+    outs = []
+    for packed in (True, False):
+        codes, scales = [], []
+        for k in ("w_gate", "w_up", "w_down"):
+            c, s = gl.mx4_quantize(w[k], packed=packed)
+            if not packed:
+                for e in (0, 255):
+                    ref, sc = _oracle_quantize(w[k][e])
+                    assert np.array_equal(c[e].cpu().numpy(), ref) and np.array_equal(s[e].cpu().numpy(), sc)
+                c, s = gl.pack_weights(c), gl.pack_mx_scales(s)
+            codes.append(c)
+            scales.append(s)
+        outs.append(gl.forward(x, rw, b, *codes, scales=tuple(scales), packed=True))
+    assert torch.equal(*outs) and outs[0].abs().max() > 0
+
+
+# ------------------------------------------------------------------ the product
+def _operands(T, N, K, fmt, seed, lo=110, hi=132):
+    """Rows and weights, and their exact values in float64 (on the GPU)."""
+    dev = _dev()
+    w, ws = _bytes((N, K // 2), seed), _bytes((N, K // 32), seed + 1, lo, hi)
+    wv = gl.mx4_dequantize(w, ws, dtype=torch.float32).double()
+    if fmt == "mx4":
+        x, xs = _bytes((T, K // 2), seed + 2), _bytes((T, K // 32), seed + 3, lo, hi)
+        xv = gl.mx4_dequantize(x, xs, dtype=torch.float32).double()
+    else:
+        x = (_rand((T, K), seed + 2) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).to(dev)
+        xv = x.float().double()
+        if fmt == "row":
+            xs = (0.01 + 0.1 * _rand(T, seed + 3).abs()).to(dev)
+            xv = xv * xs.double()[:, None]
+        else:
+            xs = _bytes((T, K // 32), seed + 3, lo, hi)
+            sc = torch.exp2(xs.cpu().double() - 127).to(dev)
+            xv = (xv.view(T, -1, 32) * sc[:, :, None]).view(T, K)
+    return x, xs, w, ws, xv, wv
+
+
+def _tolerance(xv, wv, fmt, out):
+    """The bound of the module docstring for each output of xv wv^T."""
+    T, K = xv.shape
+    ref = xv @ wv.t().contiguous()
+    mag = xv.abs() @ wv.abs().t().contiguous()
+    cut = torch.zeros_like(mag)
+    if fmt != "mx4":
+        x, w = xv.abs().float().view(T, 1, K // 8, 8), wv.abs().float().view(1, -1, K // 8, 8)
+        for t in range(T):  # the largest product of every group of 8
+            cut[t] = (x[t] * w[0]).amax(2).sum(1).double()
+    half = 2.0 ** -8 if out == torch.bfloat16 else U
+    return ref, half * ref.abs() + (K // 8 + 66) * 2 * U * mag + 7 * 2.0 ** -13 * cut
+
+
+def _linear_check(T, N, K, fmt, seed, out=torch.bfloat16, rows=None):
+    x, xs, w, ws, xv, wv = _operands(T, N, K, fmt, seed)
+    got = gl.mx4_linear(x, xs, w, ws, out_dtype=out)
+    assert got.dtype == out and got.shape == (T, N)
+    pick = torch.arange(T, device=_dev()) if rows is None else rows
+    ref, tol = _tolerance(xv[pick], wv, fmt, out)
+    err = (got[pick].double() - ref).abs()
+    bad = err > tol
+    assert not bool(bad.any()), (int(bad.sum()), float((err / tol.clamp(min=1e-300)).max()))
+    # the cut terms are of either sign: far smaller in the norm than in the worst case
+    assert float(err.norm() / ref.norm()) <= (2.0 ** -8 if out == torch.bfloat16 else 2.0 ** -13)
+    return got
+
+
+TOKENS = [1, 2, 15, 16, 17, 33, 64, 65, 100, 129, 200, 257, 520]
+
+
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+@pytest.mark.parametrize("T", TOKENS)
+def test_linear_tokens(T, fmt):
+    """Every token count on either side of a tile, against ragged N and K."""
+    _linear_check(T, 321, 1184, fmt, 70)
+    _linear_check(T, 640, 1024, fmt, 71, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+@pytest.mark.parametrize("N", [1, 3, 15, 16, 31, 64, 100, 255, 256, 257, 1000])
+def test_linear_columns(N, fmt):
+    for T in (3, 40, 300):
+        _linear_check(T, N, 544, fmt, 72)
+
+
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+@pytest.mark.parametrize("K", [32, 64, 96, 128, 160, 256, 288, 480, 512, 992, 1024, 2080, 10240])
+def test_linear_reductions(K, fmt):
+    for T in (2, 50, 270):
+        _linear_check(T, 130, K, fmt, 73, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+def test_linear_beam_width(fmt):
+    for T in (1, 64, 384, 1111):
+        rows = torch.unique(torch.linspace(0, T - 1, 12).int()).long().to(_dev())
+        _linear_check(T, 5120, 5120, fmt, 74, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", ["block", "mx4"])
+def test_linear_scales_are_each_their_own(fmt):
+    """One block at a time with a scale of its own: every (row, block) pair of
+    either operand meets its own scale."""
+    T, N, K = 70, 70, 640
+    x, xs, w, ws, _, _ = _operands(T, N, K, fmt, 75)
+    xs = (100 + (torch.arange(T)[:, None] * 7 + torch.arange(K // 32)[None] * 3) % 50).to(torch.uint8).to(_dev())
+    ws = (100 + (torch.arange(N)[:, None] * 5 + torch.arange(K // 32)[None] * 11) % 50).to(torch.uint8).to(_dev())
+    wv = gl.mx4_dequantize(w, ws, dtype=torch.float32).double()
+    xv = (gl.mx4_dequantize(x, xs, dtype=torch.float32).double() if fmt == "mx4" else
+          (x.float().double().view(T, -1, 32) * torch.exp2(xs.cpu().double() - 127).to(_dev())[:, :, None]).view(T, K))
+    for tokens in (T, 5):  # both kinds of tile
+        got = gl.mx4_linear(x[:tokens].contiguous(), xs[:tokens].contiguous(), w, ws,
+                            out_dtype=torch.float32).double()
+        ref, tol = _tolerance(xv[:tokens], wv, fmt, torch.float32)
+        assert ((got - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("T", [5, 100, 600])
+def test_linear_nan_scales_stay_in_their_rows(T):
+    """A weight scale of 255 makes its column NaN, a row's its row; nothing else."""
+    N, K = 200, 512
+    for fmt in ("block", "mx4"):
+        x, xs, w, ws, _, _ = _operands(T, N, K, fmt, 76)
+        clean = gl.mx4_linear(x, xs, w, ws)
+        ws[17, 3], xs[T - 1, 15] = 255, 255
+        got = gl.mx4_linear(x, xs, w, ws)
+        assert torch.isnan(got[:, 17]).all() and torch.isnan(got[T - 1]).all()
+        keep = torch.ones(N, dtype=torch.bool, device=_dev())
+        keep[17] = False
+        assert torch.equal(got[:T - 1][:, keep], clean[:T - 1][:, keep])
+
+
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+@pytest.mark.parametrize("T,N", [(1, 77), (33, 300), (90, 1000), (300, 129)])
+def test_linear_writes_its_rows_only(T, N, fmt):
+    """Not a byte around the output or the workspace changes."""
+    dev, K = _dev(), 2048
+    x, xs, w, ws, _, _ = _operands(T, N, K, fmt, 77)
+    for dt in (torch.bfloat16, torch.float32):
+        size = 2 if dt == torch.bfloat16 else 4
+        g = Guarded(T * N * size, dev, "out")
+        out = g.tensor((T, N), dt)
+        out.fill_(float("nan"))
+        cfg = gl.BeamMoeLinear(N, K, {"row": 0, "block": 1, "mx4": 2}[fmt], gl._X_DTYPES[dt])
+        need = gl.lib().beam_moe_mx4_linear_workspace_bytes(cfg, T)
+        ws_g = Guarded(max(need, 256), dev, "workspace")
+        r = gl.mx4_linear(x, xs, w, ws, out=out, workspace=ws_g.view)
+        assert r.data_ptr() == out.data_ptr() and not torch.isnan(out).any()
+        g.check()
+        ws_g.check()
+        # whatever the workspace held before
+        ws_g.view.fill_(255)
+        assert torch.equal(gl.mx4_linear(x, xs, w, ws, out_dtype=dt, workspace=ws_g.view), out)
+
+
+def test_linear_no_tokens():
+    x, xs, w, ws, _, _ = _operands(4, 64, 64, "row", 78)
+    assert gl.mx4_linear(x[:0], xs[:0], w, ws).shape == (0, 64)
