@@ -218,12 +218,32 @@ constexpr int64_t kMaxGrid = 1 << 23;  // workgroups of 256: a launch has fewer 
 // loads outstanding and raw barriers publish a stage.
 //
 // LDS of a stage: E4M3 rows 128 bytes, 16-byte chunk c of row r at position
-// c ^ (r & 7); E2M1 rows 64 bytes, chunk c at c ^ ((r >> 1) & 3): the rows of
-// a fragment read spread over all banks. Then one dword per row with the
-// scale bytes of the stage's four blocks.
+// c ^ ((r >> 1) & 7); E2M1 rows 64 bytes, chunk c at c ^ ((r >> 2) & 3). A
+// 16-byte read is served 16 lanes at a time, 0-3, 12-15 and 20-27 of the first
+// 32 and then the rest of them: with these keys each such group covers all 64
+// banks (c ^ (r & 7) and c ^ ((r >> 1) & 3) conflicted on every read). Then one
+// dword per row with the scale bytes of the stage's four blocks.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __align__(16) const uint8_t kZeros[16] = {};
+
+// A pointer that is the same in every lane, kept in scalar registers: loads
+// from it plus a 32-bit lane offset then need one vector register each.
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm("" : "+s"(p));
+#endif
+  return p;
+}
+
+// f(0), f(1), ..., f(N - 1) with compile-time arguments.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void for_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    for_each<N, I + 1>(f);
+  }
+}
 
 // Tiles that run together on one XCD (32 consecutive, dealt to the XCDs in
 // turn) cover 4 token tiles x 8 weight tiles, which share operands in its L2.
@@ -257,11 +277,12 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   constexpr int BM = S::BM, BN = S::BN, XROW = S::XROW, NS = S::NS;
   constexpr int XI = S::X_BYTES / 8192, WI = S::W_BYTES / 8192;  // loads of a wave per stage
   constexpr int SI = (BM + BN) / 512;                            // scale loads of a wave
-  static_assert(S::X_BYTES % 8192 == 0 && S::W_BYTES % 8192 == 0 && (BM + BN) % 512 == 0, "tile");
+  static_assert(S::X_BYTES % 8192 == 0 && S::W_BYTES % 8192 == 0 && (BM + BN) % 512 == 0 &&
+                    BN % 64 == 0, "tile");
   constexpr int PER = XI + WI + (RAGGED ? 0 : SI);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * S::STAGE];
 
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN, r = lane & 31, h = lane >> 5;
   const int K = p.K, nb = K / 32, nk = (K + 127) / 128;
   const int ntt = (p.N + BN - 1) / BN, mtt = (p.T + BM - 1) / BM;
@@ -269,91 +290,96 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   tile_of(blockIdx.x, ntt * mtt, mtt, ntt, mi, ni);
   const int t0 = mi * BM, n0 = ni * BN;
 
-  // sources of this lane's loads: rows past the end repeat the last one
-  const uint8_t* xsrc[XI];
-  int xk[XI];
+  // Sources of this lane's loads, as offsets from the tile's first row (at most
+  // 512 rows of 65536 bytes); rows past the end repeat the last one.
+  const uint8_t* xbase = p.x + (size_t)t0 * (XMODE == 2 ? K / 2 : K);
+  const uint8_t* wbase = p.w + (size_t)n0 * (K / 2);
+  const uint8_t* wsbase = p.ws + (size_t)n0 * nb;
+  const uint8_t* xsbase = XMODE == 0 ? wsbase : (const uint8_t*)p.xs + (size_t)t0 * nb;
+  const int tlast = p.T - 1 - t0, nlast = p.N - 1 - n0;
+  uint32_t xsrc[XI], wsrc[WI], ssrc[SI];
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
     constexpr int L = XROW / 16;  // lanes per row
     const int row = (wave * XI + i) * (64 / L) + lane / L;
-    const int c = XMODE == 2 ? (lane & 3) ^ ((row >> 1) & 3) : (lane & 7) ^ (row & 7);
-    xsrc[i] = p.x + (size_t)min(t0 + row, p.T - 1) * (XMODE == 2 ? K / 2 : K) + c * 16;
-    xk[i] = c * (XMODE == 2 ? 32 : 16);
+    const int c = XMODE == 2 ? (lane & 3) ^ ((row >> 2) & 3) : (lane & 7) ^ ((row >> 1) & 7);
+    xsrc[i] = min(row, tlast) * (XMODE == 2 ? K / 2 : K) + c * 16;
   }
-  const uint8_t* wsrc[WI];
-  int wk[WI];
 #pragma unroll
   for (int i = 0; i < WI; ++i) {
     const int row = (wave * WI + i) * 16 + (lane >> 2);
-    const int c = (lane & 3) ^ ((row >> 1) & 3);
-    wsrc[i] = p.w + (size_t)min(n0 + row, p.N - 1) * (K / 2) + c * 16;
-    wk[i] = c * 32;
+    wsrc[i] = min(row, nlast) * (K / 2) + (((lane & 3) ^ ((row >> 2) & 3)) * 16);
   }
-  // scale rows: the BN weight rows, then the BM token rows (with row scales
-  // there is nothing to load for these: the weights' own are loaded again and
-  // not read)
-  const uint8_t* ssrc[SI];
+  // Scales: the BN weight rows, then the BM token rows, 64 rows a load, so a
+  // load is of one kind. (Row scales have none per block: the weights' own are
+  // loaded a second time and not read, which keeps the loads of all waves equal.)
 #pragma unroll
   for (int i = 0; i < SI; ++i) {
-    const int row = (wave * SI + i) * 64 + lane;
-    if (row < BN || XMODE == 0)
-      ssrc[i] = p.ws + (size_t)min(n0 + row % BN, p.N - 1) * nb;
-    else
-      ssrc[i] = (const uint8_t*)p.xs + (size_t)min(t0 + row - BN, p.T - 1) * nb;
+    const int row0 = (wave * SI + i) * 64;
+    ssrc[i] = (row0 < BN ? min(row0 + lane, nlast)
+                         : min(row0 - BN + lane, XMODE == 0 ? nlast : tlast)) * nb;
   }
-  auto issue = [&](int kt) {
-    uint8_t* st = smem + (kt % NS) * S::STAGE;
-#pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const uint8_t* src = xsrc[i] + (size_t)kt * XROW;
-      if (RAGGED && kt * 128 + xk[i] >= K) src = kZeros;
-      dma16(src, st + (wave * XI + i) * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < WI; ++i) {
-      const uint8_t* src = wsrc[i] + (size_t)kt * 64;
-      if (RAGGED && kt * 128 + wk[i] >= K) src = kZeros;
-      dma16(src, st + S::X_BYTES + (wave * WI + i) * 1024);
-    }
+  // K not a multiple of 128: the first reduction value of a chunk in its stage
+  // (an E4M3 load covers 8 rows: the key of odd ones has bit 2 set)
+  auto xk = [&](int i) {
+    if (!RAGGED) return 0;
+    if (XMODE == 2) return ((lane & 3) ^ ((lane >> 4) & 3)) * 32;
+    return ((lane & 7) ^ ((((wave * XI + i) & 1) * 4 + (lane >> 4)) & 7)) * 16;
+  };
+  const int wk = RAGGED ? ((lane & 3) ^ ((lane >> 4) & 3)) * 32 : 0;
+  // Load q of stage kt, into the slot at byte `slot`: the tokens' XI, the
+  // weights' WI, the scales' SI. Addresses are a scalar base and a lane offset.
+  auto issue_one = [&](int kt, int slot, auto qc) {
+    constexpr int Q = decltype(qc)::value;
+    uint8_t* st = smem + slot;
+    if constexpr (Q < XI) {
+      const uint8_t* src = scalar(xbase + (size_t)kt * XROW) + xsrc[Q];
+      if (RAGGED && kt * 128 + xk(Q) >= K) src = kZeros;
+      dma16(src, st + (wave * XI + Q) * 1024);
+    } else if constexpr (Q < XI + WI) {
+      const uint8_t* src = scalar(wbase + (size_t)kt * 64) + wsrc[Q - XI];
+      if (RAGGED && kt * 128 + wk >= K) src = kZeros;
+      dma16(src, st + S::X_BYTES + (wave * WI + Q - XI) * 1024);
+    } else if constexpr (Q < PER) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (!RAGGED) {
-#pragma unroll
-      for (int i = 0; i < SI; ++i)
-        __builtin_amdgcn_global_load_lds(ssrc[i] + (size_t)kt * 4,
-                                         st + S::X_BYTES + S::W_BYTES + (wave * SI + i) * 256, 4, 0, 0);
-    }
+      const int row0 = (wave * SI + Q - XI - WI) * 64;
+      __builtin_amdgcn_global_load_lds(
+          scalar((row0 < BN ? wsbase : xsbase) + kt * 4) + ssrc[Q - XI - WI],
+          st + S::X_BYTES + S::W_BYTES + row0 * 4, 4, 0, 0);
 #endif
+    }
   };
   // K not a multiple of 128: rows of scales are not 4-byte aligned; their bytes
   // go through registers, 127 (2^0) past the end
-  auto ragged_scales = [&](int kt) {
-    uint8_t* st = smem + (kt % NS) * S::STAGE + S::X_BYTES + S::W_BYTES;
+  auto ragged_scales = [&](int kt, int slot) {
+    uint8_t* st = smem + slot + S::X_BYTES + S::W_BYTES;
 #pragma unroll
     for (int i = 0; i < SI; ++i) {
+      const int row0 = (wave * SI + i) * 64;
+      const uint8_t* src = (row0 < BN ? wsbase : xsbase) + ssrc[i];
       uint32_t v = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b)
-        v |= (uint32_t)(kt * 4 + b < nb ? ssrc[i][kt * 4 + b] : 127) << (8 * b);
-      *reinterpret_cast<uint32_t*>(st + ((wave * SI + i) * 64 + lane) * 4) = v;
+        v |= (uint32_t)(kt * 4 + b < nb ? src[kt * 4 + b] : 127) << (8 * b);
+      *reinterpret_cast<uint32_t*>(st + (row0 + lane) * 4) = v;
     }
   };
 
-  // operand offsets in a stage
-  int xo[FM], wo[FN], xso[FM], wso[FN], xsw[FM], wsw[FN];
+  // Operand offsets in a stage: fragments are 32 rows apart, which leaves the
+  // swizzle as it is. Chunks of half J: E4M3 4 J + h and 4 J + 2 + h, E2M1 2 J + h.
+  const int xrow = wm * FM * 32 + r, wrow = wn * FN * 32 + r;
+  const int xsw = XMODE == 2 ? (r >> 2) & 3 : (r >> 1) & 7, wsw = (r >> 2) & 3;
+  int xo[2][2], wo[2];
 #pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int row = (wm * FM + f) * 32 + r;
-    xo[f] = row * XROW;
-    xsw[f] = XMODE == 2 ? (row >> 1) & 3 : row & 7;
-    xso[f] = S::X_BYTES + S::W_BYTES + (BN + row) * 4;
+  for (int j = 0; j < 2; ++j) {
+    xo[j][0] = xrow * XROW + ((((XMODE == 2 ? 2 : 4) * j + h) ^ xsw) << 4);
+    xo[j][1] = xrow * XROW + (((4 * j + 2 + h) ^ xsw) << 4);
+    wo[j] = S::X_BYTES + wrow * 64 + (((2 * j + h) ^ wsw) << 4);
   }
-#pragma unroll
-  for (int f = 0; f < FN; ++f) {
-    const int row = (wn * FN + f) * 32 + r;
-    wo[f] = S::X_BYTES + row * 64;
-    wsw[f] = (row >> 1) & 3;
-    wso[f] = S::X_BYTES + S::W_BYTES + row * 4;
-  }
+  const int xso = S::X_BYTES + S::W_BYTES + (BN + xrow) * 4;
+  const int wso = S::X_BYTES + S::W_BYTES + wrow * 4;
+  // bytes h and 2 + h (this lane half's blocks) of two rows' scale dwords
+  const uint32_t pick = h ? 0x07030501u : 0x06020400u;
 
   f32x16 acc[FM][FN];
 #pragma unroll
@@ -363,106 +389,180 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
+  // A stage is 2 FM steps: step i multiplies token fragment i % FM of half i / FM
+  // (64 values; lane half h holds block h of them) with the FN weight fragments.
+  // A token fragment is read from LDS three steps before its products, into one
+  // of four register sets, and the weights' of a half some steps before it, so
+  // the matrix core has work while reads and loads issue. The reads of stage
+  // kt + 1 begin at step 2 FM - 3 of stage kt: a barrier there says that every
+  // wave has read all of stage kt, whose slot the next stage refills, and that
+  // stage kt + 1 has landed.
+  constexpr int STEPS = 2 * FM, AHEAD = 3, TURN = STEPS - AHEAD;
+  static_assert(FM >= 2 && STEPS % 4 == 0, "four register sets");
+  struct Frag {
+    u32x4 lo, hi;
+  };
+  Frag xr[4];
+  u32x4 wr[2][FN];
+  auto read_x = [&](const uint8_t* st, auto sc) {
+    constexpr int I = decltype(sc)::value, J = I / FM;
+    xr[I % 4].lo = ld16(st + xo[J][0] + I % FM * 32 * XROW);
+    if constexpr (XMODE != 2) xr[I % 4].hi = ld16(st + xo[J][1] + I % FM * 32 * XROW);
+  };
+  auto read_w = [&](const uint8_t* st, auto jc) {
+    constexpr int J = decltype(jc)::value;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) wr[J][j] = ld16(st + wo[J] + j * 32 * 64);
+  };
+  // The scale dwords as stored (read ahead), and the bytes that this lane half
+  // needs of two fragments in a register: fragment f's of half J in byte 2 J + f % 2
+  uint32_t wraw[FN], xraw[FM];
+  int wsc[(FN + 1) / 2], xsc[(FM + 1) / 2];
+  auto read_scales = [&](const uint8_t* st) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) wraw[j] = *reinterpret_cast<const uint32_t*>(st + wso + j * 128);
+    if constexpr (XMODE != 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) xraw[i] = *reinterpret_cast<const uint32_t*>(st + xso + i * 128);
+    }
+  };
+  auto pick_scales = [&]() {
+#pragma unroll
+    for (int j = 0; j < FN; j += 2)
+      wsc[j / 2] = (int)__builtin_amdgcn_perm(wraw[j + 1 < FN ? j + 1 : j], wraw[j], pick);
+#pragma unroll
+    for (int i = 0; i < FM; i += 2)
+      xsc[i / 2] = XMODE == 0 ? 0x7f7f7f7f : (int)__builtin_amdgcn_perm(xraw[i + 1], xraw[i], pick);
+  };
+  auto multiply = [&](auto sc) {
+    constexpr int I = decltype(sc)::value % FM, J = decltype(sc)::value / FM, R = decltype(sc)::value % 4;
+    i32x8 xf{};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      xf[q] = (int)xr[R].lo[q];
+      if constexpr (XMODE != 2) xf[4 + q] = (int)xr[R].hi[q];
+    }
+    for_each<FN>([&](auto nc) {
+      constexpr int N = decltype(nc)::value;
+      i32x8 wf{};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) wf[q] = (int)wr[J][N][q];
+      acc[I][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          wf, xf, acc[I][N], 4, XMODE == 2 ? 4 : 0, 2 * J + N % 2, wsc[N / 2], 2 * J + I % 2, xsc[I / 2]);
+    });
+  };
+  std::integral_constant<int, 0> j0;
+  std::integral_constant<int, 1> j1;
+
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s)
-    if (s < nk) issue(s);
-  for (int kt = 0; kt < nk; ++kt) {
-    if (RAGGED) ragged_scales(kt);
-    if (kt + NS - 2 < nk)
-      wait_vmcnt<(NS - 2) * PER>();
-    else
-      wait_vmcnt<0>();
-    if (RAGGED) wait_lgkmcnt0();
-    barrier_only();
-    asm volatile("" ::: "memory");
-    if (kt + NS - 1 < nk) issue(kt + NS - 1);
-    const uint8_t* st = smem + (kt % NS) * S::STAGE;
-    int wsc[FN], xsc[FM];
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-      wsc[f] = (int)(*reinterpret_cast<const uint32_t*>(st + wso[f]) >> (8 * h));
-#pragma unroll
-    for (int f = 0; f < FM; ++f)
-      xsc[f] = XMODE == 0 ? 0x7f7f7f7f
-                          : (int)(*reinterpret_cast<const uint32_t*>(st + xso[f]) >> (8 * h));
-    // two halves of 64 values; lane half h holds block h of each
-    auto half = [&](auto jc) {
-      constexpr int J = decltype(jc)::value;
-      i32x8 wf[FN];
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const u32x4 v = ld16(st + wo[f] + (((2 * J + h) ^ wsw[f]) << 4));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          wf[f][q] = (int)v[q];
-          wf[f][4 + q] = 0;
-        }
+    if (s < nk) for_each<PER>([&](auto q) { issue_one(s, s * S::STAGE, q); });
+  if (RAGGED) ragged_scales(0, 0);
+  if (NS - 1 <= nk)
+    wait_vmcnt<(NS - 2) * PER>();
+  else
+    wait_vmcnt<0>();
+  if (RAGGED) wait_lgkmcnt0();
+  barrier_only();
+  asm volatile("" ::: "memory");
+  for_each<AHEAD>([&](auto q) { read_x(smem, q); });
+  read_w(smem, j0);
+  read_scales(smem);
+  pick_scales();
+  int slot = 0, last = (NS - 1) * S::STAGE;  // of stage kt, and of the stage before it
+  auto stage = [&](int kt, auto loads_c) {
+    constexpr bool LOADS = decltype(loads_c)::value;  // stage kt + NS - 1 exists
+    constexpr int LP = (PER + TURN - 1) / TURN;       // loads of a step, all before the barrier
+    const int next = slot == (NS - 1) * S::STAGE ? 0 : slot + S::STAGE;
+    for_each<STEPS>([&](auto sc) {
+      constexpr int I = decltype(sc)::value;
+      if constexpr (I == TURN) {
+        if (RAGGED && kt + 1 < nk) ragged_scales(kt + 1, next);
+        wait_vmcnt<LOADS ? (NS - 2) * PER : 0>();
+        wait_lgkmcnt0();
+        barrier_only();
+        asm volatile("" ::: "memory");
       }
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        i32x8 xf;
-        if constexpr (XMODE == 2) {
-          const u32x4 v = ld16(st + xo[i] + (((2 * J + h) ^ xsw[i]) << 4));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            xf[q] = (int)v[q];
-            xf[4 + q] = 0;
-          }
-        } else {
-          const u32x4 v = ld16(st + xo[i] + (((4 * J + h) ^ xsw[i]) << 4));
-          const u32x4 u = ld16(st + xo[i] + (((4 * J + 2 + h) ^ xsw[i]) << 4));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            xf[q] = (int)v[q];
-            xf[4 + q] = (int)u[q];
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              wf[j], xf, acc[i][j], 4, XMODE == 2 ? 4 : 0, 2 * J, wsc[j], 2 * J, xsc[i]);
+      // past the last stage these read a slot that nothing uses
+      if constexpr (I < TURN)
+        read_x(smem + slot, std::integral_constant<int, I + AHEAD>{});
+      else
+        read_x(smem + next, std::integral_constant<int, I - TURN>{});
+      if constexpr (I == (FM > 3 ? FM - 3 : 0)) read_w(smem + slot, j1);
+      if constexpr (I == TURN) {
+        read_w(smem + next, j0);
+        read_scales(smem + next);
       }
-    };
-    half(std::integral_constant<int, 0>{});
-    half(std::integral_constant<int, 1>{});
-    wait_lgkmcnt0();
-    asm volatile("" ::: "memory");
-  }
+      multiply(sc);
+      if constexpr (LOADS && I < TURN)
+        for_each<LP>([&](auto e) {
+          issue_one(kt + NS - 1, last, std::integral_constant<int, I * LP + decltype(e)::value>{});
+        });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    pick_scales();
+    last = slot;
+    slot = next;
+  };
+  int kt = 0;
+  for (; kt + NS - 1 < nk; ++kt) stage(kt, std::true_type{});
+  for (; kt < nk; ++kt) stage(kt, std::false_type{});
 
-  // lane (r, h): token r of the fragment, columns 8 q + 4 h .. + 3
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int t = t0 + (wm * FM + i) * 32 + r;
-    if (t >= p.T) continue;
-    const float sc = XMODE == 0 ? ((const float*)p.xs)[t] : 1.0f;
+  // Output: lane (r, h) of a fragment holds token r, columns 8 q + 4 h .. + 3.
+  // 32 tokens of the wave at a time go through its own piece of the ring (rows
+  // padded by 16 bytes), so that a store writes whole 128-byte runs of a row.
+  // Stored straight from the registers, 8 bytes a lane, the tile's output took
+  // as long as a quarter of its reduction at K = 5120.
+  asm volatile("" ::: "memory");
+  barrier_only();  // every wave has read the last stage
+  asm volatile("" ::: "memory");
+  constexpr int OB = OUT_F32 ? 4 : 2, COLS = FN * 32, PITCH = COLS * OB + 16;
+  static_assert(8 * 32 * PITCH <= NS * S::STAGE, "output staging");
+  uint8_t* mine = smem + wave * (32 * PITCH);
+  const int c0 = n0 + wn * COLS, cols = min(COLS, p.N - c0);
+  const bool whole = p.N % (16 / OB) == 0 && cols == COLS;
+  for_each<FM>([&](auto ic) {
+    constexpr int I = decltype(ic)::value;
+    const int tb = t0 + (wm * FM + I) * 32;
+    const float scale = XMODE == 0 ? ((const float*)p.xs)[min(tb + r, p.T - 1)] : 1.0f;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int n = n0 + (wn * FN + j) * 32 + 8 * q + 4 * h;
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * sc;
-        const size_t at = (size_t)t * p.N + n;
-        if (n + 4 <= p.N && p.N % 4 == 0) {
-          if (OUT_F32)
-            st16((float*)p.out + at, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                           __float_as_uint(v[2]), __float_as_uint(v[3])});
-          else
-            *reinterpret_cast<u32x2*>((uint16_t*)p.out + at) =
-                u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < p.N) {
-              if (OUT_F32)
-                ((float*)p.out)[at + e] = v[e];
-              else
-                ((uint16_t*)p.out)[at + e] = (uint16_t)f32_to_bf16_bits(v[e]);
-            }
-        }
+        for (int e = 0; e < 4; ++e) v[e] = acc[I][j][4 * q + e] * scale;
+        uint8_t* at = mine + r * PITCH + (j * 32 + 8 * q + 4 * h) * OB;
+        if constexpr (OUT_F32)
+          st16(at, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                         __float_as_uint(v[3])});
+        else
+          *reinterpret_cast<u32x2*>(at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
       }
-  }
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+    uint8_t* out = (uint8_t*)p.out + ((size_t)tb * p.N + c0) * OB;
+    if (whole) {
+      constexpr int L = COLS * OB / 16, RS = 64 / L;  // lanes of a row, rows of a store
+#pragma unroll
+      for (int g = 0; g < 32 / RS; ++g) {
+        const int row = g * RS + lane / L;
+        if (tb + row < p.T)
+          st16(out + (size_t)row * p.N * OB + (lane % L) * 16,
+               ld16(mine + row * PITCH + (lane % L) * 16));
+      }
+    } else {
+      for (int row = 0; row < 32 && tb + row < p.T; ++row)
+        for (int c = lane; c < cols; c += 64) {
+          if constexpr (OUT_F32)
+            ((float*)(out + (size_t)row * p.N * OB))[c] = ((const float*)(mine + row * PITCH))[c];
+          else
+            ((uint16_t*)(out + (size_t)row * p.N * OB))[c] = ((const uint16_t*)(mine + row * PITCH))[c];
+        }
+    }
+    wait_lgkmcnt0();
+    asm volatile("" ::: "memory");
+  });
 }
 
 template <int XMODE, int FM, int FN, int WM, int WN>
