@@ -15,6 +15,7 @@ namespace beam {
 namespace {
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Eight values, at most 8 in magnitude, to E2M1 codes: nearest, ties to the
 // even code, magnitudes beyond 6 to 6; value i in bits 4 i .. 4 i + 3.
@@ -147,84 +148,6 @@ __global__ __launch_bounds__(256) void mx4_dequantize_kernel(const uint8_t* __re
 // E4M3: lane group a holds values 16 a .. + 15 of the step's first half and
 // the same of its second half.
 
-// One 16 x 16 tile per wave, straight from memory.
-template <int XMODE, bool OUT_F32>
-__global__ __launch_bounds__(256) void mx4_linear_kernel(Mx4LinearArgs p) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int nbn = (p.N + 63) / 64;
-  const int n0 = (blockIdx.x % nbn * 4 + wave) * 16, t0 = blockIdx.x / nbn * 16;
-  const int K = p.K, nb = K / 32;
-  const int n = min(n0 + r, p.N - 1), t = min(t0 + r, p.T - 1);
-  const uint8_t* wr = p.w + (size_t)n * (K / 2);
-  const uint8_t* wsr = p.ws + (size_t)n * nb;
-  const uint8_t* xr = p.x + (size_t)t * (XMODE == 2 ? K / 2 : K);
-  const uint8_t* xsr = (const uint8_t*)p.xs + (size_t)t * nb;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int b0 = 0; b0 < nb; b0 += 4) {
-    const int b = b0 + g;
-    i32x8 a{}, x{};
-    int sa = 127, sx = 127;
-    if (b < nb) {
-      const u32x4 v = ld16(wr + b * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = (int)v[i];
-      sa = wsr[b];
-      if (XMODE != 0) sx = xsr[b];
-    }
-    if constexpr (XMODE == 2) {
-      if (b < nb) {
-        const u32x4 v = ld16(xr + b * 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (int)v[i];
-      }
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, acc, 4, 4, 0, sa, 0, sx);
-    } else {
-      const int k = b0 * 32 + 16 * g;
-      if (k < K) {
-        const u32x4 v = ld16(xr + k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (int)v[i];
-      }
-      if (k + 64 < K) {
-        const u32x4 v = ld16(xr + k + 64);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 + i] = (int)v[i];
-      }
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, x, acc, 4, 0, 0, sa, 0, sx);
-    }
-  }
-  if (t0 + r >= p.T) return;
-  const float s = XMODE == 0 ? ((const float*)p.xs)[t] : 1.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = n0 + 4 * g + i;
-    if (c < p.N) {
-      if (OUT_F32)
-        ((float*)p.out)[(size_t)t * p.N + c] = acc[i] * s;
-      else
-        ((uint16_t*)p.out)[(size_t)t * p.N + c] = (uint16_t)f32_to_bf16_bits(acc[i] * s);
-    }
-  }
-}
-
-constexpr int64_t kMaxGrid = 1 << 23;  // workgroups of 256: a launch has fewer than 2^32 threads
-
-// ------------------------------------------------------------------ tiles
-// 8 waves as WM x WN, each FM x FN fragments of 32 tokens x 32 weight rows on
-// 32x32x64 scaled MFMAs (weights first, so a lane ends with runs of 4
-// consecutive output columns of one token). Operands go from memory straight
-// into LDS (16 bytes a lane) through a ring of NS stages of 128 reduction
-// values, filled NS - 1 stages ahead; waits leave only the later stages'
-// loads outstanding and raw barriers publish a stage.
-//
-// LDS of a stage: E4M3 rows 128 bytes, 16-byte chunk c of row r at position
-// c ^ ((r >> 1) & 7); E2M1 rows 64 bytes, chunk c at c ^ ((r >> 2) & 3). A
-// 16-byte read is served 16 lanes at a time, 0-3, 12-15 and 20-27 of the first
-// 32 and then the rest of them: with these keys each such group covers all 64
-// banks (c ^ (r & 7) and c ^ ((r >> 1) & 3) conflicted on every read). Then one
-// dword per row with the scale bytes of the stage's four blocks.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 __device__ __align__(16) const uint8_t kZeros[16] = {};
 
 // A pointer that is the same in every lane, kept in scalar registers: loads
@@ -245,6 +168,224 @@ __device__ __forceinline__ void for_each(F&& f) {
   }
 }
 
+// LDS rows of a reduction step of 128: E4M3 128 bytes, 16-byte chunk c of row r
+// at position c ^ ((r >> 1) & 7); E2M1 64 bytes, chunk c at c ^ ((r >> 2) & 3).
+// A 16-byte read is served 16 lanes at a time, 0-3, 12-15 and 20-27 of the first
+// 32 and then the rest of them: with these keys each such group covers all 64
+// banks (c ^ (r & 7) and c ^ ((r >> 1) & 3) conflicted on every read).
+template <int ROW>
+__device__ __forceinline__ int swizzle(int row) {
+  return ROW == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
+}
+
+// ------------------------------------------------------------------ few tokens
+// Up to 64 tokens the weights are read once and bound the time. A workgroup
+// takes 32 weight rows; its waves split the reduction, and each loads its own
+// share of the weights and of the TR token rows into a ring of its own in LDS,
+// NS steps of 128 values ahead, with no barrier until the partial tiles are
+// added through LDS in wave order. (The same loads into registers, 16 bytes of 32
+// rows a lane pair, took 17 us for 64 tokens at N = K = 5120: each touches 32
+// lines. Through LDS a load is whole lines of 8 rows.)
+template <int XMODE, int TR>
+struct StreamShape {
+  static constexpr int FM = TR > 32 ? TR / 32 : 1, WAVES = TR > 32 ? 4 : 8;
+  static constexpr int XROW = XMODE == 2 ? 64 : 128;
+  static constexpr int XU = TR * XROW / 1024;             // loads of token rows
+  static constexpr int SROWS = XMODE == 0 ? 32 : 32 + TR;  // rows with block scales
+  static constexpr int SU = (SROWS + 63) / 64;
+  static constexpr int STAGE = XU * 1024 + 2048 + SU * 256;
+  static constexpr int NS0 = 158 * 1024 / WAVES / STAGE, NS = NS0 > 4 ? 4 : NS0;
+  static constexpr int PITCH = 36;  // floats of a staged output row: 32 columns, padded
+  static constexpr int OUT = WAVES * FM * 32 * PITCH * 4;
+  static constexpr int LDS = WAVES * NS * STAGE > OUT ? WAVES * NS * STAGE : OUT;
+  static_assert(NS >= 2, "ring too small");
+};
+
+template <int XMODE, int TR, bool RAGGED, bool OUT_F32>
+__global__ __launch_bounds__(TR > 32 ? 256 : 512)
+void mx4_linear_stream_kernel(Mx4LinearArgs p) {
+  using S = StreamShape<XMODE, TR>;
+  constexpr int FM = S::FM, XROW = S::XROW, XU = S::XU, SU = S::SU, NS = S::NS, WAVES = S::WAVES;
+  constexpr int PER = XU + 2 + (RAGGED ? 0 : SU);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::LDS];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = lane & 31, h = lane >> 5;
+  const int K = p.K, nb = K / 32, nk = (K + 127) / 128;
+  const int ntn = (p.N + 31) / 32;
+  const int n0 = blockIdx.x % ntn * 32, t0 = blockIdx.x / ntn * TR;
+  const int k0 = nk * wave / WAVES, k1 = nk * (wave + 1) / WAVES;
+  uint8_t* ring = smem + wave * (NS * S::STAGE);
+
+  const uint8_t* xbase = p.x + (size_t)t0 * (XMODE == 2 ? K / 2 : K);
+  const uint8_t* wbase = p.w + (size_t)n0 * (K / 2);
+  const uint8_t* wsbase = p.ws + (size_t)n0 * nb;
+  const uint8_t* xsbase = (const uint8_t*)p.xs + (size_t)t0 * nb;
+  const int nlast = p.N - 1 - n0, tlast = p.T - 1 - t0;
+  uint32_t xsrc[XU], wsrc[2], ssrc[SU];
+  int xk[XU], wk[2];
+#pragma unroll
+  for (int i = 0; i < XU; ++i) {
+    constexpr int L = XROW / 16;
+    const int row = i * (64 / L) + lane / L, c = (lane % L) ^ swizzle<XROW>(row);
+    xsrc[i] = min(row, tlast) * (XMODE == 2 ? K / 2 : K) + c * 16;
+    xk[i] = c * (XMODE == 2 ? 32 : 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = i * 16 + (lane >> 2), c = (lane & 3) ^ swizzle<64>(row);
+    wsrc[i] = min(row, nlast) * (K / 2) + c * 16;
+    wk[i] = c * 32;
+  }
+  // scale rows: 32 of the weights, then the tokens'; what is past them repeats a row
+  const uint8_t* sbase[SU];
+#pragma unroll
+  for (int i = 0; i < SU; ++i) {
+    const int row = i * 64 + lane;
+    sbase[i] = row < 32 || XMODE == 0 ? wsbase : xsbase;
+    ssrc[i] = (row < 32 || XMODE == 0 ? min(row & 31, nlast) : min(row - 32, tlast)) * nb;
+  }
+  auto issue = [&](int kt, uint8_t* st) {
+#pragma unroll
+    for (int i = 0; i < XU; ++i) {
+      const uint8_t* src = scalar(xbase + (size_t)kt * XROW) + xsrc[i];
+      if (RAGGED && kt * 128 + xk[i] >= K) src = kZeros;
+      dma16(src, st + i * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t* src = scalar(wbase + (size_t)kt * 64) + wsrc[i];
+      if (RAGGED && kt * 128 + wk[i] >= K) src = kZeros;
+      dma16(src, st + XU * 1024 + i * 1024);
+    }
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (!RAGGED) {
+#pragma unroll
+      for (int i = 0; i < SU; ++i)
+        __builtin_amdgcn_global_load_lds(sbase[i] + kt * 4 + ssrc[i], st + XU * 1024 + 2048 + i * 256, 4, 0, 0);
+    }
+#endif
+  };
+  // K not a multiple of 128: rows of scales are not 4-byte aligned; the bytes of
+  // a step are read one by one, 127 (2^0) past the end
+  auto ragged_scales = [&](int kt, uint8_t* st) {
+#pragma unroll
+    for (int i = 0; i < SU; ++i) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        v |= (uint32_t)(kt * 4 + b < nb ? sbase[i][ssrc[i] + kt * 4 + b] : 127) << (8 * b);
+      *reinterpret_cast<uint32_t*>(st + XU * 1024 + 2048 + (i * 64 + lane) * 4) = v;
+    }
+  };
+
+  f32x16 acc[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[i][q] = 0.f;
+  const int rx = TR < 32 ? r & (TR - 1) : r;  // fewer than 32 rows stand twice
+  const int xsw = swizzle<XROW>(rx), wsw = swizzle<64>(r);
+  auto multiply = [&](const uint8_t* st) {
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + XU * 1024 + 2048);
+    const int ws = (int)(sc[r] >> (8 * h));
+    u32x4 w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      w[j] = ld16(st + XU * 1024 + r * 64 + (((2 * j + h) ^ wsw) << 4));
+    for_each<FM>([&](auto ic) {
+      constexpr int I = decltype(ic)::value;
+      const int xs = XMODE == 0 ? 0x7f7f7f7f : (int)(sc[32 + I * 32 + rx] >> (8 * h));
+      const uint8_t* xr = st + (I * 32 + rx) * XROW;
+      for_each<2>([&](auto jc) {
+        constexpr int J = decltype(jc)::value;
+        i32x8 wf{}, xf{};
+        const u32x4 lo = ld16(xr + ((((XMODE == 2 ? 2 : 4) * J + h) ^ xsw) << 4));
+        u32x4 hi = lo;
+        if constexpr (XMODE != 2) hi = ld16(xr + (((4 * J + 2 + h) ^ xsw) << 4));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          wf[q] = (int)w[J][q];
+          xf[q] = (int)lo[q];
+          if constexpr (XMODE != 2) xf[4 + q] = (int)hi[q];
+        }
+        acc[I] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            wf, xf, acc[I], 4, XMODE == 2 ? 4 : 0, 2 * J, ws, 2 * J, xs);
+      });
+    });
+  };
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (k0 + s < k1) issue(k0 + s, ring + s * S::STAGE);
+  int slot = 0;
+  for (int kt = k0; kt < k1; ++kt) {
+    uint8_t* st = ring + slot;
+    if (RAGGED) ragged_scales(kt, st);
+    if (kt + NS - 1 < k1)
+      wait_vmcnt<(NS - 1) * PER>();
+    else
+      wait_vmcnt<0>();
+    asm volatile("" ::: "memory");
+    multiply(st);
+    if (kt + NS < k1) {
+      wait_lgkmcnt0();  // the step has been read
+      asm volatile("" ::: "memory");
+      issue(kt + NS, st);
+    }
+    slot = slot == (NS - 1) * S::STAGE ? 0 : slot + S::STAGE;
+  }
+
+  __syncthreads();  // the rings become the staging of the partial tiles
+  float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      st16(part + ((wave * FM + i) * 32 + r) * S::PITCH + 8 * q + 4 * h,
+           u32x4{__float_as_uint(acc[i][4 * q]), __float_as_uint(acc[i][4 * q + 1]),
+                 __float_as_uint(acc[i][4 * q + 2]), __float_as_uint(acc[i][4 * q + 3])});
+  __syncthreads();
+  const int c = threadIdx.x & 31;
+  for (int t = threadIdx.x >> 5; t < FM * 32; t += WAVES * 2) {
+    float v = part[t * S::PITCH + c];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += part[(w * FM * 32 + t) * S::PITCH + c];
+    if (t <= tlast && n0 + c < p.N) {
+      if (XMODE == 0) v *= ((const float*)p.xs)[t0 + t];
+      const size_t at = (size_t)(t0 + t) * p.N + n0 + c;
+      if (OUT_F32)
+        ((float*)p.out)[at] = v;
+      else
+        ((uint16_t*)p.out)[at] = (uint16_t)f32_to_bf16_bits(v);
+    }
+  }
+}
+
+template <int XMODE, int TR>
+void stream_launch(const Mx4LinearArgs& a, hipStream_t st) {
+  const int grid = (a.N + 31) / 32 * ((a.T + TR - 1) / TR), threads = 64 * StreamShape<XMODE, TR>::WAVES;
+  const bool ragged = a.K % 128 != 0;
+  if (ragged && a.out_f32)
+    mx4_linear_stream_kernel<XMODE, TR, true, true><<<grid, threads, 0, st>>>(a);
+  else if (ragged)
+    mx4_linear_stream_kernel<XMODE, TR, true, false><<<grid, threads, 0, st>>>(a);
+  else if (a.out_f32)
+    mx4_linear_stream_kernel<XMODE, TR, false, true><<<grid, threads, 0, st>>>(a);
+  else
+    mx4_linear_stream_kernel<XMODE, TR, false, false><<<grid, threads, 0, st>>>(a);
+}
+
+// ------------------------------------------------------------------ tiles
+// Waves as WM x WN, each FM x FN fragments of 32 tokens x 32 weight rows on
+// 32x32x64 scaled MFMAs (weights first, so a lane ends with runs of 4
+// consecutive output columns of one token). Operands go from memory straight
+// into LDS (16 bytes a lane) through a ring of NS stages of 128 reduction
+// values, filled NS - 1 stages ahead; waits leave only the later stages'
+// loads outstanding and raw barriers publish a stage.
+//
+// LDS of a stage: the token rows and the weight rows, swizzled as above. The block
+// scales of four stages are 16 bytes of a row and are loaded together, into one of
+// two buffers, while the four stages before them are multiplied (a load per stage,
+// 4 bytes of each row, was half of all requests to L2).
 // Tiles that run together on one XCD (32 consecutive, dealt to the XCDs in
 // turn) cover 4 token tiles x 8 weight tiles, which share operands in its L2.
 __device__ __forceinline__ void tile_of(int b, int n_tiles, int mt, int nt, int& m, int& n) {
@@ -252,6 +393,10 @@ __device__ __forceinline__ void tile_of(int b, int n_tiles, int mt, int nt, int&
   if (b < n_tiles / R * R) {
     const int q = b >> 3;
     b = ((q / 32) * 8 + (b & 7)) * 32 + q % 32;
+  } else {
+    // the last, partial round: each XCD takes consecutive tiles too
+    const int b0 = n_tiles / R * R, n = n_tiles - b0, x = (b - b0) & 7, q = (b - b0) >> 3;
+    b = b0 + x * (n / 8) + min(x, n % 8) + q;
   }
   const int mb = b / (GM * nt), rem = b - mb * GM * nt;
   const int gm = min(GM, mt - mb * GM);
@@ -259,28 +404,36 @@ __device__ __forceinline__ void tile_of(int b, int n_tiles, int mt, int nt, int&
   m = mb * GM + rem % gm;
 }
 
-template <int XMODE, int FM, int FN, int WM, int WN, bool RAGGED>
+template <int XMODE, int FM, int FN, int WM, int WN>
 struct TileShape {
+  static constexpr int WAVES = WM * WN;
   static constexpr int BM = 32 * FM * WM, BN = 32 * FN * WN;
   static constexpr int XROW = XMODE == 2 ? 64 : 128;  // bytes of a row in a stage
-  static constexpr int X_BYTES = BM * XROW, W_BYTES = BN * 64;
-  static constexpr int S_BYTES = (BM + BN) * 4;
-  static constexpr int STAGE = X_BYTES + W_BYTES + S_BYTES;
-  static constexpr int NS = 158 * 1024 / STAGE > 4 ? 4 : 158 * 1024 / STAGE;
-  static_assert(NS >= 2, "ring too small");
+  static constexpr int X_BYTES = BM * XROW, W_BYTES = BN * 64, STAGE = X_BYTES + W_BYTES;
+  static constexpr int SROWS = XMODE == 0 ? BN : BM + BN;  // rows with block scales
+  static constexpr int SCALES = SROWS * 16;                // of four stages
+  static constexpr int PITCH = FN * 32 * 4 + 16;           // staged output row (fp32)
+  // 8 waves have a CU's LDS for themselves, fewer share it with another workgroup
+  static constexpr int ROOM = (WAVES == 8 ? 160 : 80) * 1024 - 2 * SCALES;
+  static constexpr int NS = ROOM / STAGE > 4 ? 4 : ROOM / STAGE;
+  static constexpr int OUT = WAVES * 32 * PITCH;
+  static constexpr int LDS = NS * STAGE + 2 * SCALES > OUT ? NS * STAGE + 2 * SCALES : OUT;
+  static_assert(NS >= 2 && BN % 64 == 0 && BM % 64 == 0, "tile");
 };
 
 template <int XMODE, int FM, int FN, int WM, int WN, bool RAGGED, bool OUT_F32>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx4_linear_tile_kernel(Mx4LinearArgs p) {
-  using S = TileShape<XMODE, FM, FN, WM, WN, RAGGED>;
-  constexpr int BM = S::BM, BN = S::BN, XROW = S::XROW, NS = S::NS;
-  constexpr int XI = S::X_BYTES / 8192, WI = S::W_BYTES / 8192;  // loads of a wave per stage
-  constexpr int SI = (BM + BN) / 512;                            // scale loads of a wave
-  static_assert(S::X_BYTES % 8192 == 0 && S::W_BYTES % 8192 == 0 && (BM + BN) % 512 == 0 &&
-                    BN % 64 == 0, "tile");
-  constexpr int PER = XI + WI + (RAGGED ? 0 : SI);
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[NS * S::STAGE];
+  using S = TileShape<XMODE, FM, FN, WM, WN>;
+  constexpr int BM = S::BM, BN = S::BN, XROW = S::XROW, NS = S::NS, WAVES = S::WAVES;
+  // Loads of a stage: 1 KB of rows each, the tokens', then the weights'; and every
+  // four stages 64 rows' scales each, the weights', then the tokens'. They are
+  // dealt to the waves in turn; what is left over repeats the last one, so that
+  // every wave waits for the same count.
+  constexpr int XU = S::X_BYTES / 1024, WU = S::W_BYTES / 1024, SU = S::SROWS / 64;
+  constexpr int PER = (XU + WU + WAVES - 1) / WAVES, SI = (SU + WAVES - 1) / WAVES;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::LDS];
+  uint8_t* scales = smem + NS * S::STAGE;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN, r = lane & 31, h = lane >> 5;
@@ -291,84 +444,72 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   const int t0 = mi * BM, n0 = ni * BN;
 
   // Sources of this lane's loads, as offsets from the tile's first row (at most
-  // 512 rows of 65536 bytes); rows past the end repeat the last one.
+  // 256 rows of 65536 bytes); rows past the end repeat the last one.
   const uint8_t* xbase = p.x + (size_t)t0 * (XMODE == 2 ? K / 2 : K);
   const uint8_t* wbase = p.w + (size_t)n0 * (K / 2);
   const uint8_t* wsbase = p.ws + (size_t)n0 * nb;
   const uint8_t* xsbase = XMODE == 0 ? wsbase : (const uint8_t*)p.xs + (size_t)t0 * nb;
   const int tlast = p.T - 1 - t0, nlast = p.N - 1 - n0;
-  uint32_t xsrc[XI], wsrc[WI], ssrc[SI];
+  uint32_t dsrc[PER], ssrc[SI];
+  int dk[RAGGED ? PER : 1];  // first reduction value of the lane's chunk in a stage
+  auto unit = [&](int q) { return min(q * WAVES + wave, XU + WU - 1); };
+  auto sunit = [&](int q) { return min(q * WAVES + wave, SU - 1); };
 #pragma unroll
-  for (int i = 0; i < XI; ++i) {
-    constexpr int L = XROW / 16;  // lanes per row
-    const int row = (wave * XI + i) * (64 / L) + lane / L;
-    const int c = XMODE == 2 ? (lane & 3) ^ ((row >> 2) & 3) : (lane & 7) ^ ((row >> 1) & 7);
-    xsrc[i] = min(row, tlast) * (XMODE == 2 ? K / 2 : K) + c * 16;
+  for (int q = 0; q < PER; ++q) {
+    const int u = unit(q);
+    if (XMODE != 2 && u < XU) {
+      const int row = u * 8 + (lane >> 3), c = (lane & 7) ^ swizzle<128>(row);
+      dsrc[q] = min(row, tlast) * K + c * 16;
+      if (RAGGED) dk[q] = c * 16;
+    } else {
+      const int row = (u < XU ? u : u - XU) * 16 + (lane >> 2), c = (lane & 3) ^ swizzle<64>(row);
+      dsrc[q] = min(row, u < XU ? tlast : nlast) * (K / 2) + c * 16;
+      if (RAGGED) dk[q] = c * 32;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < WI; ++i) {
-    const int row = (wave * WI + i) * 16 + (lane >> 2);
-    wsrc[i] = min(row, nlast) * (K / 2) + (((lane & 3) ^ ((row >> 2) & 3)) * 16);
+  for (int q = 0; q < SI; ++q) {
+    const int row = sunit(q) * 64 + lane;
+    ssrc[q] = (sunit(q) < BN / 64 ? min(row, nlast) : min(row - BN, tlast)) * nb;
   }
-  // Scales: the BN weight rows, then the BM token rows, 64 rows a load, so a
-  // load is of one kind. (Row scales have none per block: the weights' own are
-  // loaded a second time and not read, which keeps the loads of all waves equal.)
-#pragma unroll
-  for (int i = 0; i < SI; ++i) {
-    const int row0 = (wave * SI + i) * 64;
-    ssrc[i] = (row0 < BN ? min(row0 + lane, nlast)
-                         : min(row0 - BN + lane, XMODE == 0 ? nlast : tlast)) * nb;
-  }
-  // K not a multiple of 128: the first reduction value of a chunk in its stage
-  // (an E4M3 load covers 8 rows: the key of odd ones has bit 2 set)
-  auto xk = [&](int i) {
-    if (!RAGGED) return 0;
-    if (XMODE == 2) return ((lane & 3) ^ ((lane >> 4) & 3)) * 32;
-    return ((lane & 7) ^ ((((wave * XI + i) & 1) * 4 + (lane >> 4)) & 7)) * 16;
-  };
-  const int wk = RAGGED ? ((lane & 3) ^ ((lane >> 4) & 3)) * 32 : 0;
-  // Load q of stage kt, into the slot at byte `slot`: the tokens' XI, the
-  // weights' WI, the scales' SI. Addresses are a scalar base and a lane offset.
+  auto sbase = [&](int q) { return sunit(q) < BN / 64 ? wsbase : xsbase; };
+  // Load q of stage kt, into the slot at byte `slot`. Addresses are a scalar
+  // base and a lane offset.
   auto issue_one = [&](int kt, int slot, auto qc) {
     constexpr int Q = decltype(qc)::value;
-    uint8_t* st = smem + slot;
-    if constexpr (Q < XI) {
-      const uint8_t* src = scalar(xbase + (size_t)kt * XROW) + xsrc[Q];
-      if (RAGGED && kt * 128 + xk(Q) >= K) src = kZeros;
-      dma16(src, st + (wave * XI + Q) * 1024);
-    } else if constexpr (Q < XI + WI) {
-      const uint8_t* src = scalar(wbase + (size_t)kt * 64) + wsrc[Q - XI];
-      if (RAGGED && kt * 128 + wk >= K) src = kZeros;
-      dma16(src, st + S::X_BYTES + (wave * WI + Q - XI) * 1024);
-    } else if constexpr (Q < PER) {
-#if defined(__HIP_DEVICE_COMPILE__)
-      const int row0 = (wave * SI + Q - XI - WI) * 64;
-      __builtin_amdgcn_global_load_lds(
-          scalar((row0 < BN ? wsbase : xsbase) + kt * 4) + ssrc[Q - XI - WI],
-          st + S::X_BYTES + S::W_BYTES + row0 * 4, 4, 0, 0);
-#endif
+    if constexpr (Q < PER) {
+      const int u = unit(Q);
+      const uint8_t* src = scalar(u < XU ? xbase + (size_t)kt * XROW : wbase + (size_t)kt * 64) + dsrc[Q];
+      if (RAGGED && kt * 128 + dk[RAGGED ? Q : 0] >= K) src = kZeros;
+      dma16(src, smem + slot + u * 1024);
     }
   };
-  // K not a multiple of 128: rows of scales are not 4-byte aligned; their bytes
-  // go through registers, 127 (2^0) past the end
-  auto ragged_scales = [&](int kt, int slot) {
-    uint8_t* st = smem + slot + S::X_BYTES + S::W_BYTES;
+  // Scales of stages 4 g .. 4 g + 3: 16 bytes of every row. The last group ends
+  // with the last stage, so that nothing is read past a row.
+  auto first_of = [&](int g) { return RAGGED ? 4 * g : min(4 * g, nk - 4); };
+  auto issue_scales = [&](int g) {
 #pragma unroll
-    for (int i = 0; i < SI; ++i) {
-      const int row0 = (wave * SI + i) * 64;
-      const uint8_t* src = (row0 < BN ? wsbase : xsbase) + ssrc[i];
+    for (int q = 0; q < SI; ++q)
+      dma16(scalar(sbase(q) + first_of(g) * 4) + ssrc[q], scales + (g & 1) * S::SCALES + sunit(q) * 1024);
+  };
+  // K not a multiple of 128, or below 512: the bytes of a stage go through
+  // registers, 127 (2^0) past the end
+  auto ragged_scales = [&](int kt) {
+    uint8_t* at = scales + (kt >> 2 & 1) * S::SCALES + (kt & 3) * 4 + lane * 16;
+#pragma unroll
+    for (int q = 0; q < SI; ++q) {
       uint32_t v = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b)
-        v |= (uint32_t)(kt * 4 + b < nb ? src[kt * 4 + b] : 127) << (8 * b);
-      *reinterpret_cast<uint32_t*>(st + (row0 + lane) * 4) = v;
+        v |= (uint32_t)(kt * 4 + b < nb ? sbase(q)[ssrc[q] + kt * 4 + b] : 127) << (8 * b);
+      *reinterpret_cast<uint32_t*>(at + sunit(q) * 1024) = v;
     }
   };
 
   // Operand offsets in a stage: fragments are 32 rows apart, which leaves the
   // swizzle as it is. Chunks of half J: E4M3 4 J + h and 4 J + 2 + h, E2M1 2 J + h.
   const int xrow = wm * FM * 32 + r, wrow = wn * FN * 32 + r;
-  const int xsw = XMODE == 2 ? (r >> 2) & 3 : (r >> 1) & 7, wsw = (r >> 2) & 3;
+  const int xsw = swizzle<XROW>(r), wsw = swizzle<64>(r);
   int xo[2][2], wo[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -376,8 +517,7 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
     xo[j][1] = xrow * XROW + (((4 * j + 2 + h) ^ xsw) << 4);
     wo[j] = S::X_BYTES + wrow * 64 + (((2 * j + h) ^ wsw) << 4);
   }
-  const int xso = S::X_BYTES + S::W_BYTES + (BN + xrow) * 4;
-  const int wso = S::X_BYTES + S::W_BYTES + wrow * 4;
+  const int xso = (BN + xrow) * 16, wso = wrow * 16;
   // bytes h and 2 + h (this lane half's blocks) of two rows' scale dwords
   const uint32_t pick = h ? 0x07030501u : 0x06020400u;
 
@@ -418,12 +558,14 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   // needs of two fragments in a register: fragment f's of half J in byte 2 J + f % 2
   uint32_t wraw[FN], xraw[FM];
   int wsc[(FN + 1) / 2], xsc[(FM + 1) / 2];
-  auto read_scales = [&](const uint8_t* st) {
+  auto read_scales = [&](int kt) {
+    const int g = kt >> 2;
+    const uint8_t* at = scales + (g & 1) * S::SCALES + (kt - first_of(g)) * 4;
 #pragma unroll
-    for (int j = 0; j < FN; ++j) wraw[j] = *reinterpret_cast<const uint32_t*>(st + wso + j * 128);
+    for (int j = 0; j < FN; ++j) wraw[j] = *reinterpret_cast<const uint32_t*>(at + wso + j * 512);
     if constexpr (XMODE != 0) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) xraw[i] = *reinterpret_cast<const uint32_t*>(st + xso + i * 128);
+      for (int i = 0; i < FM; ++i) xraw[i] = *reinterpret_cast<const uint32_t*>(at + xso + i * 512);
     }
   };
   auto pick_scales = [&]() {
@@ -451,13 +593,12 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
           wf, xf, acc[I][N], 4, XMODE == 2 ? 4 : 0, 2 * J + N % 2, wsc[N / 2], 2 * J + I % 2, xsc[I / 2]);
     });
   };
-  std::integral_constant<int, 0> j0;
-  std::integral_constant<int, 1> j1;
 
+  if (!RAGGED) issue_scales(0);
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s)
     if (s < nk) for_each<PER>([&](auto q) { issue_one(s, s * S::STAGE, q); });
-  if (RAGGED) ragged_scales(0, 0);
+  if (RAGGED) ragged_scales(0);
   if (NS - 1 <= nk)
     wait_vmcnt<(NS - 2) * PER>();
   else
@@ -465,34 +606,38 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   if (RAGGED) wait_lgkmcnt0();
   barrier_only();
   asm volatile("" ::: "memory");
+  std::integral_constant<int, 0> j0;
+  std::integral_constant<int, 1> j1;
   for_each<AHEAD>([&](auto q) { read_x(smem, q); });
   read_w(smem, j0);
-  read_scales(smem);
+  read_scales(0);
   pick_scales();
   int slot = 0, last = (NS - 1) * S::STAGE;  // of stage kt, and of the stage before it
   auto stage = [&](int kt, auto loads_c) {
     constexpr bool LOADS = decltype(loads_c)::value;  // stage kt + NS - 1 exists
     constexpr int LP = (PER + TURN - 1) / TURN;       // loads of a step, all before the barrier
     const int next = slot == (NS - 1) * S::STAGE ? 0 : slot + S::STAGE;
+    // The scales of the next four stages: their buffer was last read before the
+    // barrier of stage kt - 1; they are read three stages on, when the loads of
+    // these three (more than any wait leaves outstanding) are behind them.
+    if (!RAGGED && (kt & 3) == 0 && kt + 4 < nk) issue_scales((kt >> 2) + 1);
     for_each<STEPS>([&](auto sc) {
       constexpr int I = decltype(sc)::value;
       if constexpr (I == TURN) {
-        if (RAGGED && kt + 1 < nk) ragged_scales(kt + 1, next);
+        if (RAGGED && kt + 1 < nk) ragged_scales(kt + 1);
         wait_vmcnt<LOADS ? (NS - 2) * PER : 0>();
         wait_lgkmcnt0();
         barrier_only();
         asm volatile("" ::: "memory");
       }
-      // past the last stage these read a slot that nothing uses
+      // past the last stage these read what nothing uses
       if constexpr (I < TURN)
         read_x(smem + slot, std::integral_constant<int, I + AHEAD>{});
       else
         read_x(smem + next, std::integral_constant<int, I - TURN>{});
       if constexpr (I == (FM > 3 ? FM - 3 : 0)) read_w(smem + slot, j1);
-      if constexpr (I == TURN) {
-        read_w(smem + next, j0);
-        read_scales(smem + next);
-      }
+      if constexpr (I == (TURN > FM ? TURN : FM)) read_w(smem + next, j0);  // half 0 is done
+      if constexpr (I == TURN) read_scales(min(kt + 1, nk - 1));
       multiply(sc);
       if constexpr (LOADS && I < TURN)
         for_each<LP>([&](auto e) {
@@ -517,7 +662,7 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   barrier_only();  // every wave has read the last stage
   asm volatile("" ::: "memory");
   constexpr int OB = OUT_F32 ? 4 : 2, COLS = FN * 32, PITCH = COLS * OB + 16;
-  static_assert(8 * 32 * PITCH <= NS * S::STAGE, "output staging");
+  static_assert(WAVES * 32 * PITCH <= S::LDS, "output staging");
   uint8_t* mine = smem + wave * (32 * PITCH);
   const int c0 = n0 + wn * COLS, cols = min(COLS, p.N - c0);
   const bool whole = p.N % (16 / OB) == 0 && cols == COLS;
@@ -567,18 +712,20 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
 
 template <int XMODE, int FM, int FN, int WM, int WN>
 void tile_launch(const Mx4LinearArgs& a, hipStream_t st) {
-  using S = TileShape<XMODE, FM, FN, WM, WN, false>;
+  using S = TileShape<XMODE, FM, FN, WM, WN>;
   const int grid = (a.T + S::BM - 1) / S::BM * ((a.N + S::BN - 1) / S::BN);
-  const bool ragged = a.K % 128 != 0;
+  const bool ragged = a.K % 128 != 0 || a.K < 512;
   if (ragged && a.out_f32)
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, true, true><<<grid, 512, 0, st>>>(a);
+    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, true, true><<<grid, 64 * S::WAVES, 0, st>>>(a);
   else if (ragged)
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, true, false><<<grid, 512, 0, st>>>(a);
+    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, true, false><<<grid, 64 * S::WAVES, 0, st>>>(a);
   else if (a.out_f32)
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, false, true><<<grid, 512, 0, st>>>(a);
+    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, false, true><<<grid, 64 * S::WAVES, 0, st>>>(a);
   else
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, false, false><<<grid, 512, 0, st>>>(a);
+    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, false, false><<<grid, 64 * S::WAVES, 0, st>>>(a);
 }
+
+constexpr int64_t kMaxGrid = 1 << 23;  // workgroups of 256: a launch has fewer than 2^32 threads
 
 }  // namespace
 
@@ -610,15 +757,42 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
 
 size_t mx4_linear_workspace(int T, int N, int K, int x_mode) { return 0; }
 
+// Which kernel takes a product. A CU runs one workgroup of any of them at about
+// its own rate, so the time goes by how many rounds of 256 workgroups there are;
+// us a round at K = 5120 with E4M3 rows, and its workgroup:
+//   stream, 64 tokens x 32 columns     7.7
+//   tile,   64 tokens x 128 columns   14.3
+//   tile,  128 tokens x 128 columns   20.5
+//   tile,  256 tokens x 256 columns   50
+// (4-bit rows: the last three 13, 16 and 40.) Measured at N = K = 5120 around the
+// borders: T = 128, stream 14.1 and 64 x 128 tiles 14.5; T = 512, 64 x 128 tiles
+// 24.9 and 128 x 128 tiles 20.6; T = 2048, 128 x 128 tiles 57 and 256 x 256 tiles
+// 50; T = 4096, 102 and 109. Up to 32 tokens the weights alone bound the time and
+// the stream reads them once.
+enum class Variant { kStream16, kStream32, kStream64, kTile64, kTile128, kTile256 };
+Variant variant_of(int T, int N) {
+  if (T <= 16) return Variant::kStream16;
+  if (T <= 32) return Variant::kStream32;
+  auto rounds = [&](int64_t bm, int64_t bn) { return ((T + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256; };
+  const int64_t cost[4] = {77 * rounds(64, 32), 143 * rounds(64, 128), 205 * rounds(128, 128),
+                           500 * rounds(256, 256)};
+  int best = 0;
+  for (int i = 1; i < 4; ++i)
+    if (cost[i] < cost[best]) best = i;
+  return (Variant)((int)Variant::kStream64 + best);
+}
+
 hipError_t launch_mx4_linear(const Mx4LinearArgs& a, int x_mode, hipStream_t st) {
-  const int grid = (a.N + 63) / 64 * ((a.T + 15) / 16);
   auto go = [&](auto m) {
-    if (a.T > 64)
-      tile_launch<decltype(m)::value, 4, 2, 2, 4>(a, st);
-    else if (a.out_f32)
-      mx4_linear_kernel<decltype(m)::value, true><<<grid, 256, 0, st>>>(a);
-    else
-      mx4_linear_kernel<decltype(m)::value, false><<<grid, 256, 0, st>>>(a);
+    constexpr int XMODE = decltype(m)::value;
+    switch (variant_of(a.T, a.N)) {
+      case Variant::kStream16: stream_launch<XMODE, 16>(a, st); break;
+      case Variant::kStream32: stream_launch<XMODE, 32>(a, st); break;
+      case Variant::kStream64: stream_launch<XMODE, 64>(a, st); break;
+      case Variant::kTile64: tile_launch<XMODE, 2, 1, 1, 4>(a, st); break;
+      case Variant::kTile128: tile_launch<XMODE, 2, 2, 2, 2>(a, st); break;
+      case Variant::kTile256: tile_launch<XMODE, 4, 2, 2, 4>(a, st); break;
+    }
   };
   if (x_mode == 0)
     go(std::integral_constant<int, 0>{});
