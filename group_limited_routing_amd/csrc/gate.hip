@@ -79,9 +79,10 @@ __device__ __forceinline__ void load_logits(const T* z, int lane, int E, float (
 // took 100 us at 16384 tokens x 8, all on 256 addresses.
 constexpr int kCountShare = 16384;  // slots of a workgroup
 
-__global__ __launch_bounds__(256) void gate_zero_kernel(int32_t* counts, int E) {
-  const int e = blockIdx.x * 256 + threadIdx.x;
-  if (e < E) counts[e] = 0;
+// The routing's first workgroup zeroes them.
+__device__ __forceinline__ void zero_counts(const GateArgs& p) {
+  if (p.counts && blockIdx.x == 0)
+    for (int e = threadIdx.x; e < p.E; e += 256) p.counts[e] = 0;
 }
 
 __global__ __launch_bounds__(1024) void gate_count_kernel(const int32_t* __restrict__ idx, int64_t n,
@@ -103,20 +104,12 @@ __global__ __launch_bounds__(1024) void gate_count_kernel(const int32_t* __restr
   }
 }
 
+// One token by a whole wave, lane l with the experts KPL l .. KPL l + KPL - 1 and
+// every key in fp64. lds_keys: E doubles of the wave's own.
 template <typename T, int KPL>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
-  extern __shared__ double lds_keys[];  // [4][E], groups that are not whole powers of two of lanes
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int t = blockIdx.x * 4 + wave;
-  if (t >= p.T) return;  // no barrier below: a wave works alone
+__device__ __forceinline__ void gate_token(const GateArgs& p, int t, double* lds_keys) {
+  const int lane = threadIdx.x & 63;
   const int E = p.E, k = p.k;
-  if (p.valid && !p.valid[t]) {
-    if (lane < k) {
-      p.idx[(size_t)t * k + lane] = -1;
-      p.w[(size_t)t * k + lane] = 0.f;
-    }
-    return;
-  }
   float z[KPL];
   load_logits<T, KPL>((const T*)p.z + (size_t)t * E, lane, E, z);
 
@@ -174,7 +167,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
       stride = lpg;
       mine = lane / lpg;
     } else {
-      double* keys = lds_keys + (size_t)wave * E;
+      double* keys = lds_keys;
 #pragma unroll
       for (int i = 0; i < KPL; ++i)
         if (lane * KPL + i < E) keys[lane * KPL + i] = key[i];
@@ -235,6 +228,289 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
     const double w = p.renorm ? (sum > 0 ? my_f / sum : 0.0) : my_f;
     p.idx[(size_t)t * k + lane] = my_e;
     p.w[(size_t)t * k + lane] = (float)((double)p.rsf * w);
+  }
+}
+
+template <typename T, int KPL>
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
+  extern __shared__ double lds_keys[];  // [4][E] with groups
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + wave;
+  zero_counts(p);
+  if (t >= p.T) return;  // no barrier below: a wave works alone
+  if (p.valid && !p.valid[t]) {
+    if (lane < p.k) {
+      p.idx[(size_t)t * p.k + lane] = -1;
+      p.w[(size_t)t * p.k + lane] = 0.f;
+    }
+    return;
+  }
+  gate_token<T, KPL>(p, t, lds_keys + (size_t)wave * p.E);
+}
+
+// ------------------------------------------------------------------ four tokens a wave
+// Up to 256 experts in 1, 2, 4, 8 or 16 groups and top_k <= 16: 16 lanes per
+// token, a group on whole lanes, at most KPL experts a lane. The order is decided
+// on 32-bit keys: the score with its bias, or without a bias the logit itself
+// (the score grows with it), in fp32, its 24 leading bits in the order of unsigned
+// integers with 255 - expert below them. So a maximum is one integer maximum, it
+// says which expert it is, and ties go to the lower index. Where two neighbours of
+// the first top_k + 1 keys, or the last kept group and the first dropped one, lie
+// so near each other that the fp64 keys might stand the other way, the token is
+// done over in fp64 by the whole wave (about 1% of tokens with random logits).
+// With bf16 logits and no bias the 24 bits are the logit, and equal ones are ties.
+// Weights are fp64 from the chosen logits in either case. 16384 tokens x 256
+// experts, 8 groups, top 8: 8 rounds of the fp64 maximum over a wave per token
+// took 33 us.
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float row_dpp(float v) {
+  return __uint_as_float(row_dpp<CTRL>(__float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double row_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)row_dpp<CTRL>((uint32_t)(b >> 32)) << 32 |
+                                        row_dpp<CTRL>((uint32_t)b));
+}
+// op over the 16 lanes of a row, in every lane: pairs, quads, then the mirrored
+// quad and the mirrored half.
+template <typename F, typename Op>
+__device__ __forceinline__ F row_reduce(F v, Op op) {
+  v = op(v, row_dpp<0xB1>(v));
+  v = op(v, row_dpp<0x4E>(v));
+  v = op(v, row_dpp<0x141>(v));
+  return op(v, row_dpp<0x140>(v));
+}
+
+// Up to here a wave per token is faster: a wave of four tokens has four times as
+// much to do before the first is done (16384 x 256, us, wave per token and this:
+// 64 tokens 6.3 and 7.0, 4096 11.1 and 11.9, 8192 18.5 and 15.7, 16384 33 and 16).
+constexpr int kWaveTokens = 4096;
+constexpr uint32_t kLow = 255;          // the expert's bits of a key
+constexpr uint32_t kMasked = kLow + 1;  // leading bits of a masked expert; a free slot is 0
+__device__ __forceinline__ uint32_t key_bits(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+}
+
+// A lane's cnt of at most c values at q, `fill` behind them; `whole`: cnt is c or 0
+// for every lane, and q a multiple of c values from an aligned row.
+template <int KPL, typename T>
+__device__ __forceinline__ void load_share(const T* q, int c, int cnt, bool whole, float fill,
+                                           float (&v)[KPL]) {
+  constexpr int VE = 16 / sizeof(T);
+  if (KPL % VE == 0 && whole && c % VE == 0) {  // 16 bytes at a time
+#pragma unroll
+    for (int i = 0; i < KPL; i += VE) {
+      T w[VE];
+      if (i < cnt) __builtin_memcpy(w, __builtin_assume_aligned(q + i, 16), 16);
+#pragma unroll
+      for (int j = 0; j < VE; ++j)
+        if (i + j < KPL) v[i + j] = i < cnt ? to_f32(w[j]) : fill;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) v[i] = i < cnt ? to_f32(q[i]) : fill;
+  }
+}
+
+template <typename T, int KPL>
+__global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
+  extern __shared__ double lds_keys[];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15;
+  zero_counts(p);
+  const int E = p.E, k = p.k, G = p.n_group;
+  const int t0 = (blockIdx.x * 4 + wave) * 4, t = t0 + (lane >> 4);
+  const bool live = t < p.T && !(p.valid && !p.valid[t]);
+  const T* zr = (const T*)p.z + (size_t)min(t, p.T - 1) * E;
+
+  // this lane's experts: c of its group's gs
+  const int gs = E / G, lpg = 16 / G, c = (gs + lpg - 1) / lpg;
+  const int grp = l / lpg, at = (l % lpg) * c;
+  const int e0 = grp * gs + at, cnt = min(c, max(0, gs - at));
+  float z[KPL];
+  load_share<KPL>(zr + e0, c, cnt, gs % c == 0, -INFINITY, z);
+
+  float m = -INFINITY;
+  if (p.softmax) {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) m = fmaxf(m, z[i]);
+    m = row_reduce(m, [](float a, float b) { return fmaxf(a, b); });
+  }
+  // scores in fp32, where they are compared: with a bias, or summed for groups
+  const bool scored = p.bias || (G > 1 && p.top2);
+  float v[KPL];
+  if (scored) {
+    float inv = 1.f;
+    if (p.softmax) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) {
+        v[i] = z[i] > -INFINITY ? __expf(z[i] - m) : 0.f;
+        sum += v[i];
+      }
+      sum = row_reduce(sum, [](float a, float b) { return a + b; });
+      inv = 1.f / sum;
+    }
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      if (p.softmax) {
+        v[i] *= inv;
+      } else {
+        const float e = __expf(-fabsf(z[i]));
+        v[i] = (z[i] >= 0.f ? 1.f : e) * __builtin_amdgcn_rcpf(1.f + e);
+      }
+    }
+    if (p.bias) {
+      float b[KPL];
+      load_share<KPL>(p.bias + e0, c, cnt, gs % c == 0, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) v[i] += b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) v[i] = z[i];
+  }
+  // Logits stand for their scores, but not where fp64 scores saturate or vanish.
+  auto saturated = [&](float lower) {
+    return p.softmax ? !(m - lower < 600.f) : !(lower < 16.f && lower > -600.f);
+  };
+  bool near = false;
+  uint32_t key[KPL];
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    const bool off = !(z[i] > -INFINITY) || !(v[i] > -INFINITY);
+    if (off) v[i] = -INFINITY;
+    const uint32_t low = kLow - (uint32_t)(e0 + i);
+    const float order = p.bias ? v[i] : z[i];
+    key[i] = i >= cnt ? 0u : (off ? kMasked : key_bits(order) & ~kLow) | low;
+  }
+
+  if (G > 1 && p.topk_group < G) {
+    float t1 = -INFINITY, t2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      t2 = fmaxf(t2, fminf(t1, v[i]));
+      t1 = fmaxf(t1, v[i]);
+    }
+    auto merge = [&](float o1, float o2) {
+      t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+      t1 = fmaxf(t1, o1);
+    };
+    if (lpg > 1) merge(row_dpp<0xB1>(t1), row_dpp<0xB1>(t2));
+    if (lpg > 2) merge(row_dpp<0x4E>(t1), row_dpp<0x4E>(t2));
+    if (lpg > 4) merge(row_dpp<0x141>(t1), row_dpp<0x141>(t2));
+    const float score = p.top2 && gs > 1 ? t1 + t2 : t1;
+    int rank = 0;
+    for (int g = 0; g < G; ++g) {
+      const float o = __shfl(score, (lane & 48) + g * lpg);
+      rank += (o > score || (o == score && g < grp)) ? 1 : 0;
+    }
+    const bool kept = rank < p.topk_group;
+    const float lo = row_reduce(kept ? score : INFINITY, [](float a, float b) { return fminf(a, b); });
+    const float hi = row_reduce(kept ? -INFINITY : score, [](float a, float b) { return fmaxf(a, b); });
+    if (!scored) {
+      near = !(lo - hi > 0x1p-28f) || saturated(hi);
+    } else {
+      // a score is within 2^-21, and relative to itself within 2^-16 down to 1e-30
+      // (its exponential's argument is rounded)
+      near = !(lo - hi > (p.bias ? 0x1p-18f * (fabsf(lo) + fabsf(hi) + 1.f) : 0x1p-15f * (lo + hi)));
+      near |= !p.bias && !(lo > 1e-30f);
+    }
+    if (!kept) {
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) key[i] = 0u;
+    }
+  }
+
+  // the k largest keys, lane j of the row keeps the j-th; `next`: the one after
+  uint32_t mine = 0, next = 0;
+  for (int j = 0; j <= k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < KPL; ++i) best = max(best, key[i]);
+    best = row_reduce(best, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    if (l == j) mine = best;
+    if (j == k) next = best;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) key[i] = key[i] == best ? 0u : key[i];
+  }
+  uint32_t after = __shfl(mine, lane + 1);
+  if (l == k - 1) after = next;
+  int e = (int)(kLow - (mine & kLow));
+  const float zc = l < k && live ? to_f32(zr[e]) : -INFINITY;
+  bool close = false;  // to the one after
+  if (l < k && after >= 2 * kMasked) {  // neither is masked
+    const bool exact = sizeof(T) == 2 && !p.bias;
+    const float lo = key_value(mine & ~kLow), hi = key_value(exact ? after & ~kLow : after | kLow);
+    // with a bias both keys are within 2^-20, and their sums' rounding; logits are
+    // exact, but fp64 scores of logits this near could be equal
+    const float tol = p.bias ? 0x1p-18f + 0x1p-21f * (fabsf(lo) + fabsf(hi)) : 0x1p-28f;
+    close = !(lo - hi > tol || (exact && lo == hi));
+    if (!p.bias) near |= saturated(hi);
+  }
+
+  double f = 0;
+  const bool on = zc > -INFINITY;
+  if (p.softmax) {
+    // renormalised weights are the softmax over the chosen alone
+    if (on) f = zc == m ? 1.0 : exp((double)zc - (double)m);
+    if (!p.renorm) {
+      double sum = 0;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i)
+        if (i < c) sum += z[i] > -INFINITY ? exp((double)z[i] - (double)m) : 0.0;
+      sum = row_reduce(sum, [](double a, double b) { return a + b; });
+      if (sum > 0) f /= sum;
+    }
+    if (!(m < INFINITY)) near = true;
+  } else if (on) {
+    const double x = exp(-fabs((double)zc));
+    f = (zc >= 0.f ? 1.0 : x) / (1.0 + x);
+  }
+  // Two of the chosen that are close, apart from the others: their fp64 scores say
+  // which comes first. (Softmax scores with a bias have no fp64 form here.)
+  if (__any(close)) {
+    // (lane exchanges outside of any condition: every lane has to take part)
+    const int cb = __shfl((int)close, lane - 1), ca = __shfl((int)close, lane + 1);
+    const bool before = cb && l > 0, behind = ca && l < 15;
+    const bool pair = close && l < k - 1 && !before && !behind && !(p.softmax && p.bias);
+    near |= close && !pair;
+    const int pb = __shfl((int)pair, lane - 1);
+    const bool second = pb && l > 0;
+    double key64 = f;
+    if (p.bias && l < k) key64 += (double)p.bias[e];
+    const int other = pair ? lane + 1 : second ? lane - 1 : lane;
+    const double okey = __shfl(key64, other), of = __shfl(f, other);
+    const int oe = __shfl(e, other);
+    const bool wins = key64 > okey || (key64 == okey && e < oe);  // comes before the other
+    if ((pair && !wins) || (second && wins)) {
+      e = oe;
+      f = of;
+    }
+  }
+  if (p.renorm) {
+    const double sum = row_reduce(f, [](double a, double b) { return a + b; });
+    f = sum > 0 ? f / sum : 0.0;
+    if (p.softmax && m > -INFINITY && !(sum > 0)) near = true;  // all chosen far below the maximum
+  }
+  if (l < k && t < p.T) {
+    p.idx[(size_t)t * k + l] = live ? e : -1;
+    p.w[(size_t)t * k + l] = live ? (float)((double)p.rsf * f) : 0.f;
+  }
+  // tokens to do over, one after the other
+  uint64_t again = __ballot(near && live);
+  while (again) {
+    const int row = (__ffsll((unsigned long long)again) - 1) >> 4;
+    gate_token<T, (KPL + 3) / 4>(p, t0 + row, lds_keys + (size_t)wave * E);
+    again &= ~(0xffffull << (16 * row));
   }
 }
 
@@ -326,15 +602,22 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(GateBwdArgs p) {
       if (ej == lane * KPL + i) dz[i] += oj;
   }
   T* out = (T*)p.dz + (size_t)t * E;
+  T o[KPL];
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
-    const int c = lane * KPL + i;
-    if (c < E) {
-      if constexpr (sizeof(T) == 4)
-        out[c] = dz[i];
-      else
-        out[c] = (T)f32_to_bf16_bits(dz[i]);
-    }
+    if constexpr (sizeof(T) == 4)
+      o[i] = dz[i];
+    else
+      o[i] = (T)f32_to_bf16_bits(dz[i]);
+  }
+  constexpr int BYTES = KPL * sizeof(T);
+  if (BYTES >= 4 && BYTES <= 16 && E % KPL == 0) {  // as the logits are read
+    if (lane * KPL < E)
+      __builtin_memcpy(__builtin_assume_aligned(out + lane * KPL, BYTES <= 16 ? BYTES : 4), o, BYTES);
+  } else {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i)
+      if (lane * KPL + i < E) out[lane * KPL + i] = o[i];
   }
 }
 
@@ -355,21 +638,40 @@ void by_keys(int E, F&& f) {
 
 }  // namespace
 
-hipError_t launch_gate(const GateArgs& a, int f32, hipStream_t st) {
+hipError_t launch_gate(const GateArgs& args, int f32, hipStream_t st) {
+  GateArgs a = args;
+  const int64_t slots = (int64_t)a.T * a.k;
+  const int shares = (int)((slots + kCountShare - 1) / kCountShare);
+  if (shares == 1) a.counts = nullptr;  // the count kernel writes them itself
   const size_t lds = a.n_group > 1 ? (size_t)4 * a.E * sizeof(double) : 0;
-  const int grid = (a.T + 3) / 4;
-  by_keys(a.E, [&](auto c) {
-    if (f32)
-      gate_kernel<float, decltype(c)::value><<<grid, 256, lds, st>>>(a);
+  const int G = a.n_group;
+  if (a.T > kWaveTokens && a.E <= 256 && G <= 16 && (G & (G - 1)) == 0 && a.k <= 16) {
+    const int lpg = 16 / G, c = (a.E / G + lpg - 1) / lpg;  // experts of a lane
+    const int grid = (a.T + 15) / 16;
+    auto go = [&](auto kpl) {
+      if (f32)
+        gate_rows_kernel<float, decltype(kpl)::value><<<grid, 256, lds, st>>>(a);
+      else
+        gate_rows_kernel<uint16_t, decltype(kpl)::value><<<grid, 256, lds, st>>>(a);
+    };
+    if (c <= 4)
+      go(std::integral_constant<int, 4>{});
+    else if (c <= 8)
+      go(std::integral_constant<int, 8>{});
     else
-      gate_kernel<uint16_t, decltype(c)::value><<<grid, 256, lds, st>>>(a);
-  });
-  if (a.counts) {
-    const int64_t n = (int64_t)a.T * a.k;
-    const int shares = (int)((n + kCountShare - 1) / kCountShare);
-    if (shares > 1) gate_zero_kernel<<<(a.E + 255) / 256, 256, 0, st>>>(a.counts, a.E);
-    gate_count_kernel<<<shares, 1024, 0, st>>>(a.idx, n, a.E, a.counts);
+      go(std::integral_constant<int, 16>{});
+  } else {
+    const int grid = (a.T + 3) / 4;
+    by_keys(a.E, [&](auto c) {
+      if (f32)
+        gate_kernel<float, decltype(c)::value><<<grid, 256, lds, st>>>(a);
+      else
+        gate_kernel<uint16_t, decltype(c)::value><<<grid, 256, lds, st>>>(a);
+    });
   }
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || !args.counts) return err;
+  gate_count_kernel<<<shares, 1024, 0, st>>>(a.idx, slots, a.E, args.counts);
   return hipGetLastError();
 }
 

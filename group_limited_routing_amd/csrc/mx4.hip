@@ -179,40 +179,42 @@ __device__ __forceinline__ int swizzle(int row) {
 }
 
 // ------------------------------------------------------------------ few tokens
-// Up to 64 tokens the weights are read once and bound the time. A workgroup
-// takes 32 weight rows; its waves split the reduction, and each loads its own
+// Few tokens: the weights are read once and bound the time. A workgroup takes
+// 32 FN weight rows; its waves split the reduction, and each loads its own
 // share of the weights and of the TR token rows into a ring of its own in LDS,
 // NS steps of 128 values ahead, with no barrier until the partial tiles are
 // added through LDS in wave order. (The same loads into registers, 16 bytes of 32
 // rows a lane pair, took 17 us for 64 tokens at N = K = 5120: each touches 32
 // lines. Through LDS a load is whole lines of 8 rows.)
-template <int XMODE, int TR>
+template <int XMODE, int TR, int FN>
 struct StreamShape {
   static constexpr int FM = TR > 32 ? TR / 32 : 1, WAVES = TR > 32 ? 4 : 8;
   static constexpr int XROW = XMODE == 2 ? 64 : 128;
   static constexpr int XU = TR * XROW / 1024;             // loads of token rows
-  static constexpr int SROWS = XMODE == 0 ? 32 : 32 + TR;  // rows with block scales
+  static constexpr int BN = 32 * FN, WU = 2 * FN;          // weight rows and their loads
+  static constexpr int SROWS = XMODE == 0 ? BN : BN + TR;  // rows with block scales
   static constexpr int SU = (SROWS + 63) / 64;
-  static constexpr int STAGE = XU * 1024 + 2048 + SU * 256;
+  static constexpr int STAGE = (XU + WU) * 1024 + SU * 256;
   static constexpr int NS0 = 158 * 1024 / WAVES / STAGE, NS = NS0 > 4 ? 4 : NS0;
-  static constexpr int PITCH = 36;  // floats of a staged output row: 32 columns, padded
+  static constexpr int PITCH = BN + 4;  // floats of a staged output row, padded
   static constexpr int OUT = WAVES * FM * 32 * PITCH * 4;
   static constexpr int LDS = WAVES * NS * STAGE > OUT ? WAVES * NS * STAGE : OUT;
   static_assert(NS >= 2, "ring too small");
 };
 
-template <int XMODE, int TR, bool RAGGED, bool OUT_F32>
+template <int XMODE, int TR, int FN, bool RAGGED, bool OUT_F32>
 __global__ __launch_bounds__(TR > 32 ? 256 : 512)
 void mx4_linear_stream_kernel(Mx4LinearArgs p) {
-  using S = StreamShape<XMODE, TR>;
-  constexpr int FM = S::FM, XROW = S::XROW, XU = S::XU, SU = S::SU, NS = S::NS, WAVES = S::WAVES;
-  constexpr int PER = XU + 2 + (RAGGED ? 0 : SU);
+  using S = StreamShape<XMODE, TR, FN>;
+  constexpr int FM = S::FM, XROW = S::XROW, XU = S::XU, WU = S::WU, SU = S::SU, NS = S::NS;
+  constexpr int WAVES = S::WAVES, BN = S::BN, SOFF = (XU + WU) * 1024;
+  constexpr int PER = XU + WU + (RAGGED ? 0 : SU);
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::LDS];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 31, h = lane >> 5;
   const int K = p.K, nb = K / 32, nk = (K + 127) / 128;
-  const int ntn = (p.N + 31) / 32;
-  const int n0 = blockIdx.x % ntn * 32, t0 = blockIdx.x / ntn * TR;
+  const int ntn = (p.N + BN - 1) / BN;
+  const int n0 = blockIdx.x % ntn * BN, t0 = blockIdx.x / ntn * TR;
   const int k0 = nk * wave / WAVES, k1 = nk * (wave + 1) / WAVES;
   uint8_t* ring = smem + wave * (NS * S::STAGE);
 
@@ -221,8 +223,8 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
   const uint8_t* wsbase = p.ws + (size_t)n0 * nb;
   const uint8_t* xsbase = (const uint8_t*)p.xs + (size_t)t0 * nb;
   const int nlast = p.N - 1 - n0, tlast = p.T - 1 - t0;
-  uint32_t xsrc[XU], wsrc[2], ssrc[SU];
-  int xk[XU], wk[2];
+  uint32_t xsrc[XU], wsrc[WU], ssrc[SU];
+  int xk[XU], wk[WU];
 #pragma unroll
   for (int i = 0; i < XU; ++i) {
     constexpr int L = XROW / 16;
@@ -231,18 +233,18 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
     xk[i] = c * (XMODE == 2 ? 32 : 16);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < WU; ++i) {
     const int row = i * 16 + (lane >> 2), c = (lane & 3) ^ swizzle<64>(row);
     wsrc[i] = min(row, nlast) * (K / 2) + c * 16;
     wk[i] = c * 32;
   }
-  // scale rows: 32 of the weights, then the tokens'; what is past them repeats a row
+  // scale rows: the weights', then the tokens'; what is past them repeats a row
   const uint8_t* sbase[SU];
 #pragma unroll
   for (int i = 0; i < SU; ++i) {
     const int row = i * 64 + lane;
-    sbase[i] = row < 32 || XMODE == 0 ? wsbase : xsbase;
-    ssrc[i] = (row < 32 || XMODE == 0 ? min(row & 31, nlast) : min(row - 32, tlast)) * nb;
+    sbase[i] = row < BN || XMODE == 0 ? wsbase : xsbase;
+    ssrc[i] = (row < BN || XMODE == 0 ? min(row % BN, nlast) : min(row - BN, tlast)) * nb;
   }
   auto issue = [&](int kt, uint8_t* st) {
 #pragma unroll
@@ -252,7 +254,7 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
       dma16(src, st + i * 1024);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < WU; ++i) {
       const uint8_t* src = scalar(wbase + (size_t)kt * 64) + wsrc[i];
       if (RAGGED && kt * 128 + wk[i] >= K) src = kZeros;
       dma16(src, st + XU * 1024 + i * 1024);
@@ -261,7 +263,7 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
     if constexpr (!RAGGED) {
 #pragma unroll
       for (int i = 0; i < SU; ++i)
-        __builtin_amdgcn_global_load_lds(sbase[i] + kt * 4 + ssrc[i], st + XU * 1024 + 2048 + i * 256, 4, 0, 0);
+        __builtin_amdgcn_global_load_lds(sbase[i] + kt * 4 + ssrc[i], st + SOFF + i * 256, 4, 0, 0);
     }
 #endif
   };
@@ -274,42 +276,53 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         v |= (uint32_t)(kt * 4 + b < nb ? sbase[i][ssrc[i] + kt * 4 + b] : 127) << (8 * b);
-      *reinterpret_cast<uint32_t*>(st + XU * 1024 + 2048 + (i * 64 + lane) * 4) = v;
+      *reinterpret_cast<uint32_t*>(st + SOFF + (i * 64 + lane) * 4) = v;
     }
   };
 
-  f32x16 acc[FM];
+  f32x16 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int q = 0; q < 16; ++q) acc[i][q] = 0.f;
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][n][q] = 0.f;
   const int rx = TR < 32 ? r & (TR - 1) : r;  // fewer than 32 rows stand twice
   const int xsw = swizzle<XROW>(rx), wsw = swizzle<64>(r);
   auto multiply = [&](const uint8_t* st) {
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + XU * 1024 + 2048);
-    const int ws = (int)(sc[r] >> (8 * h));
-    u32x4 w[2];
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + SOFF);
+    int ws[FN];
+    u32x4 w[FN][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      w[j] = ld16(st + XU * 1024 + r * 64 + (((2 * j + h) ^ wsw) << 4));
+    for (int n = 0; n < FN; ++n) {
+      ws[n] = (int)(sc[n * 32 + r] >> (8 * h));
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        w[n][j] = ld16(st + XU * 1024 + (n * 32 + r) * 64 + (((2 * j + h) ^ wsw) << 4));
+    }
     for_each<FM>([&](auto ic) {
       constexpr int I = decltype(ic)::value;
-      const int xs = XMODE == 0 ? 0x7f7f7f7f : (int)(sc[32 + I * 32 + rx] >> (8 * h));
+      const int xs = XMODE == 0 ? 0x7f7f7f7f : (int)(sc[BN + I * 32 + rx] >> (8 * h));
       const uint8_t* xr = st + (I * 32 + rx) * XROW;
       for_each<2>([&](auto jc) {
         constexpr int J = decltype(jc)::value;
-        i32x8 wf{}, xf{};
+        i32x8 xf{};
         const u32x4 lo = ld16(xr + ((((XMODE == 2 ? 2 : 4) * J + h) ^ xsw) << 4));
         u32x4 hi = lo;
         if constexpr (XMODE != 2) hi = ld16(xr + (((4 * J + 2 + h) ^ xsw) << 4));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          wf[q] = (int)w[J][q];
           xf[q] = (int)lo[q];
           if constexpr (XMODE != 2) xf[4 + q] = (int)hi[q];
         }
-        acc[I] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            wf, xf, acc[I], 4, XMODE == 2 ? 4 : 0, 2 * J, ws, 2 * J, xs);
+        for_each<FN>([&](auto nc) {
+          constexpr int N = decltype(nc)::value;
+          i32x8 wf{};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) wf[q] = (int)w[N][J][q];
+          acc[I][N] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              wf, xf, acc[I][N], 4, XMODE == 2 ? 4 : 0, 2 * J, ws[N], 2 * J, xs);
+        });
       });
     });
   };
@@ -339,13 +352,15 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      st16(part + ((wave * FM + i) * 32 + r) * S::PITCH + 8 * q + 4 * h,
-           u32x4{__float_as_uint(acc[i][4 * q]), __float_as_uint(acc[i][4 * q + 1]),
-                 __float_as_uint(acc[i][4 * q + 2]), __float_as_uint(acc[i][4 * q + 3])});
+    for (int n = 0; n < FN; ++n)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        st16(part + ((wave * FM + i) * 32 + r) * S::PITCH + n * 32 + 8 * q + 4 * h,
+             u32x4{__float_as_uint(acc[i][n][4 * q]), __float_as_uint(acc[i][n][4 * q + 1]),
+                   __float_as_uint(acc[i][n][4 * q + 2]), __float_as_uint(acc[i][n][4 * q + 3])});
   __syncthreads();
-  const int c = threadIdx.x & 31;
-  for (int t = threadIdx.x >> 5; t < FM * 32; t += WAVES * 2) {
+  const int c = threadIdx.x % BN;
+  for (int t = threadIdx.x / BN; t < TR; t += WAVES * 64 / BN) {
     float v = part[t * S::PITCH + c];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += part[(w * FM * 32 + t) * S::PITCH + c];
@@ -360,18 +375,19 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
   }
 }
 
-template <int XMODE, int TR>
+template <int XMODE, int TR, int FN>
 void stream_launch(const Mx4LinearArgs& a, hipStream_t st) {
-  const int grid = (a.N + 31) / 32 * ((a.T + TR - 1) / TR), threads = 64 * StreamShape<XMODE, TR>::WAVES;
+  using S = StreamShape<XMODE, TR, FN>;
+  const int grid = (a.N + S::BN - 1) / S::BN * ((a.T + TR - 1) / TR), threads = 64 * S::WAVES;
   const bool ragged = a.K % 128 != 0;
   if (ragged && a.out_f32)
-    mx4_linear_stream_kernel<XMODE, TR, true, true><<<grid, threads, 0, st>>>(a);
+    mx4_linear_stream_kernel<XMODE, TR, FN, true, true><<<grid, threads, 0, st>>>(a);
   else if (ragged)
-    mx4_linear_stream_kernel<XMODE, TR, true, false><<<grid, threads, 0, st>>>(a);
+    mx4_linear_stream_kernel<XMODE, TR, FN, true, false><<<grid, threads, 0, st>>>(a);
   else if (a.out_f32)
-    mx4_linear_stream_kernel<XMODE, TR, false, true><<<grid, threads, 0, st>>>(a);
+    mx4_linear_stream_kernel<XMODE, TR, FN, false, true><<<grid, threads, 0, st>>>(a);
   else
-    mx4_linear_stream_kernel<XMODE, TR, false, false><<<grid, threads, 0, st>>>(a);
+    mx4_linear_stream_kernel<XMODE, TR, FN, false, false><<<grid, threads, 0, st>>>(a);
 }
 
 // ------------------------------------------------------------------ tiles
@@ -758,37 +774,52 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
 size_t mx4_linear_workspace(int T, int N, int K, int x_mode) { return 0; }
 
 // Which kernel takes a product. A CU runs one workgroup of any of them at about
-// its own rate, so the time goes by how many rounds of 256 workgroups there are;
-// us a round at K = 5120 with E4M3 rows, and its workgroup:
-//   stream, 64 tokens x 32 columns     7.7
-//   tile,   64 tokens x 128 columns   14.3
-//   tile,  128 tokens x 128 columns   20.5
-//   tile,  256 tokens x 256 columns   50
-// (4-bit rows: the last three 13, 16 and 40.) Measured at N = K = 5120 around the
-// borders: T = 128, stream 14.1 and 64 x 128 tiles 14.5; T = 512, 64 x 128 tiles
-// 24.9 and 128 x 128 tiles 20.6; T = 2048, 128 x 128 tiles 57 and 256 x 256 tiles
-// 50; T = 4096, 102 and 109. Up to 32 tokens the weights alone bound the time and
-// the stream reads them once.
-enum class Variant { kStream16, kStream32, kStream64, kTile64, kTile128, kTile256 };
+// its own rate, so the time goes by how many rounds of 256 workgroups there are.
+// Tenths of a us a round at K = 5120 with E4M3 rows:
+//   stream,  16 tokens x  32 columns   50      32 tokens x  32 columns   56
+//            16 tokens x  64 columns   65      32 tokens x  64 columns   79
+//            64 tokens x  32 columns   77      64 tokens x  64 columns  101
+//   tile,    64 tokens x 128 columns  143     128 tokens x 128 columns  205
+//           256 tokens x 256 columns  500
+// (4-bit rows: the tiles 130, 160 and 400.) Measured at N = K = 5120 around the
+// borders, us: T = 128, stream of 32 columns 14.1 and 64 x 128 tiles 14.5; T = 512,
+// 64 x 128 tiles 24.9 and 128 x 128 tiles 20.6; T = 2048, 128 x 128 tiles 57 and
+// 256 x 256 tiles 50; T = 4096, 102 and 109. At N = K = 10240: 1 token, streams of
+// 32 and 64 columns 17.0 and 15.3; 32 tokens 21.8 and 17.3.
+enum class Variant { kStream16, kStream16Wide, kStream32, kStream32Wide, kStream64, kStream64Wide,
+                     kTile64, kTile128, kTile256 };
 Variant variant_of(int T, int N) {
-  if (T <= 16) return Variant::kStream16;
-  if (T <= 32) return Variant::kStream32;
-  auto rounds = [&](int64_t bm, int64_t bn) { return ((T + bm - 1) / bm * ((N + bn - 1) / bn) + 255) / 256; };
-  const int64_t cost[4] = {77 * rounds(64, 32), 143 * rounds(64, 128), 205 * rounds(128, 128),
-                           500 * rounds(256, 256)};
-  int best = 0;
-  for (int i = 1; i < 4; ++i)
-    if (cost[i] < cost[best]) best = i;
-  return (Variant)((int)Variant::kStream64 + best);
+  struct {
+    Variant v;
+    int bm, bn, cost;
+  } const all[] = {{Variant::kStream16, 16, 32, 50},   {Variant::kStream16Wide, 16, 64, 65},
+                   {Variant::kStream32, 32, 32, 56},   {Variant::kStream32Wide, 32, 64, 79},
+                   {Variant::kStream64, 64, 32, 77},   {Variant::kStream64Wide, 64, 64, 101},
+                   {Variant::kTile64, 64, 128, 143},   {Variant::kTile128, 128, 128, 205},
+                   {Variant::kTile256, 256, 256, 500}};
+  Variant best = Variant::kTile256;
+  int64_t least = INT64_MAX;
+  for (const auto& c : all) {
+    const int64_t wgs = (int64_t)((T + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const int64_t cost = (wgs + 255) / 256 * c.cost;
+    if (cost < least) {
+      least = cost;
+      best = c.v;
+    }
+  }
+  return best;
 }
 
 hipError_t launch_mx4_linear(const Mx4LinearArgs& a, int x_mode, hipStream_t st) {
   auto go = [&](auto m) {
     constexpr int XMODE = decltype(m)::value;
     switch (variant_of(a.T, a.N)) {
-      case Variant::kStream16: stream_launch<XMODE, 16>(a, st); break;
-      case Variant::kStream32: stream_launch<XMODE, 32>(a, st); break;
-      case Variant::kStream64: stream_launch<XMODE, 64>(a, st); break;
+      case Variant::kStream16: stream_launch<XMODE, 16, 1>(a, st); break;
+      case Variant::kStream16Wide: stream_launch<XMODE, 16, 2>(a, st); break;
+      case Variant::kStream32: stream_launch<XMODE, 32, 1>(a, st); break;
+      case Variant::kStream32Wide: stream_launch<XMODE, 32, 2>(a, st); break;
+      case Variant::kStream64: stream_launch<XMODE, 64, 1>(a, st); break;
+      case Variant::kStream64Wide: stream_launch<XMODE, 64, 2>(a, st); break;
       case Variant::kTile64: tile_launch<XMODE, 2, 1, 1, 4>(a, st); break;
       case Variant::kTile128: tile_launch<XMODE, 2, 2, 2, 2>(a, st); break;
       case Variant::kTile256: tile_launch<XMODE, 4, 2, 2, 4>(a, st); break;

@@ -52,6 +52,16 @@ def _check(z, k, bias=None, valid=None, kind="sigmoid", G=1, keep=1, pick="top2"
     assert np.array_equal(r["topk_idx"].cpu().numpy(), idx)
     assert np.array_equal(r["expert_counts"].cpu().numpy(), counts)
     assert (np.abs(f64(r["topk_w"]) - w) <= (U + 2.0 ** -40) * np.abs(w) + 2.0 ** -150).all()
+    # the same tokens over and over in a batch of thousands, which other kernels take
+    n = 4200 // z.shape[0] + 1
+    many = gl.gate(z.repeat(n, 1), top_k=k, expert_bias=bias, score=kind, n_group=G, topk_group=keep,
+                   group_score=pick, renormalise=renorm, routed_scaling_factor=rsf,
+                   valid=None if valid is None else valid.repeat(n), return_counts=True)
+    assert torch.equal(many["topk_idx"], r["topk_idx"].repeat(n, 1))
+    assert torch.equal(many["expert_counts"], n * r["expert_counts"])
+    # one rounding each of fp64 values that agree to 2^-40
+    d = (many["topk_w"].double() - r["topk_w"].repeat(n, 1).double()).abs()
+    assert (d <= (2 * U + 2.0 ** -39) * r["topk_w"].repeat(n, 1).abs() + 2.0 ** -149).all()
     return r
 
 
@@ -146,7 +156,7 @@ def test_gate_equals_the_blocks_route():
 
 def test_gate_many_tokens_count():
     """More tokens than fit the chip at once: the counts are those of the indices."""
-    z = _logits(20011, 256, 43)
+    z = _logits(20011, 256, 43)  # a part of the tokens is decided over in fp64
     valid = torch.arange(20011, device=_dev()) % 7 != 0
     r = gl.gate(z, top_k=8, n_group=8, topk_group=4, valid=valid, return_counts=True)
     live = r["topk_idx"][valid].flatten().long()
