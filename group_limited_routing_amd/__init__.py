@@ -260,6 +260,8 @@ def _ptr(t):
 
 
 def _check(t, name, shape, dtypes, device):
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.device == device:
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
@@ -568,6 +570,9 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 class _Here:
     """The context of a call on the current device and stream: nothing to switch."""
 
@@ -584,10 +589,10 @@ _HERE_CTX = _Here()
 def _on(device, stream):
     """The context in which a call allocates and launches: ``stream``, else the
     current stream of the tensors' device (made current if another device is)."""
-    if device.type != "cuda":
+    if not device.type == "cuda":
         raise ValueError(f"tensors are on {device}, expected a GPU")
     if stream is None:
-        return _HERE_CTX if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE_CTX if device.index == _current_device() else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
@@ -633,9 +638,9 @@ def add_rms_norm(x, norm_weight, *, stream_in=None, keep=1.0, add=1.0, norm_eps=
         if return_y:
             y = torch.empty_like(x)
         if quant is not None:
-            q = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
+            q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
             scale = (torch.empty(T, dtype=torch.float32, device=dev) if quant == "row" else
-                     torch.empty((T, H // 32), dtype=torch.uint8, device=dev))
+                     torch.empty(T, H // 32, dtype=torch.uint8, device=dev))
         _launch("beam_moe_add_rms_norm", dev, lib().beam_moe_add_rms_norm, ctypes.byref(cfg), T,
                 _p(x), _p(stream_in), _p(norm_weight), _p(stream_out), _p(y), _p(q), _p(scale))
     return {"stream_out": stream_out, "y": y, "q": q, "q_scale": scale}
@@ -698,8 +703,8 @@ def gate(logits, *, top_k, expert_bias=None, score="sigmoid", n_group=1, topk_gr
         _check(valid, "valid", (T,), (torch.bool, torch.uint8), dev)
     counts = None
     with _on(dev, stream):
-        idx = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-        w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        idx = torch.empty(T, top_k, dtype=torch.int32, device=dev)
+        w = torch.empty(T, top_k, dtype=torch.float32, device=dev)
         if return_counts:
             counts = (torch.empty if T else torch.zeros)(E, dtype=torch.int32, device=dev)
         _launch("beam_moe_gate", dev, lib().beam_moe_gate, ctypes.byref(cfg), T, _p(logits),
@@ -751,8 +756,8 @@ def mx4_quantize(x, *, packed=False, stream=None):
     if packed and x.shape[1] % 16:
         raise ValueError(f"x has {x.shape[1]} rows per expert, expected a multiple of 16")
     with _on(dev, stream):
-        codes = torch.empty((*x.shape[:-1], C // 2), dtype=torch.uint8, device=dev)
-        scales = torch.empty((*x.shape[:-1], C // 32), dtype=torch.uint8, device=dev)
+        codes = torch.empty(*x.shape[:-1], C // 2, dtype=torch.uint8, device=dev)
+        scales = torch.empty(*x.shape[:-1], C // 32, dtype=torch.uint8, device=dev)
         _launch("beam_moe_mx4_quantize", dev, lib().beam_moe_mx4_quantize, _p(x), x.numel() // C,
                 C, _X_DTYPES[x.dtype], BEAM_LAYOUT_PACKED if packed else BEAM_LAYOUT_ROW_MAJOR,
                 _p(codes), _p(scales))
@@ -771,7 +776,7 @@ def mx4_dequantize(codes, scales, *, dtype=torch.bfloat16, stream=None):
     _check(codes, "codes", codes.shape, _U8, dev)
     _check(scales, "scales", (*codes.shape[:-1], C // 32), _U8, dev)
     with _on(dev, stream):
-        out = torch.empty((*codes.shape[:-1], C), dtype=dtype, device=dev)
+        out = torch.empty(*codes.shape[:-1], C, dtype=dtype, device=dev)
         _launch("beam_moe_mx4_dequantize", dev, lib().beam_moe_mx4_dequantize, _p(codes),
                 _p(scales), out.numel() // C, C, _X_DTYPES[dtype], _p(out))
     return out
@@ -808,7 +813,7 @@ def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, wo
     cfg = BeamMoeLinear(N, K, fmt, _X_DTYPES[out_dtype])
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((T, N), dtype=out_dtype, device=dev)
+            out = torch.empty(T, N, dtype=out_dtype, device=dev)
         need = int(lib().beam_moe_mx4_linear_workspace_bytes(ctypes.byref(cfg), T))
         workspace = _scratch(workspace, need, dev) if need else None
         _launch("beam_moe_mx4_linear", dev, lib().beam_moe_mx4_linear, ctypes.byref(cfg), T, _p(x),

@@ -11,44 +11,13 @@
 // by the values themselves, not by an fp32 rounding of them.
 #include "common.h"
 #include "operators.h"
+#include "wave.h"
 
 namespace beam {
 namespace {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(uint16_t v) { return bf16_bits_to_f32(v); }
-
-// Maximum over the wave, in every lane: the moves of wave_max in the router,
-// on both words of a double.
-template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ double dpp_max(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const int lo = (int)(uint32_t)b, hi = (int)(uint32_t)(b >> 32);
-  const uint32_t olo = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xF, false);
-  const uint32_t ohi = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xF, false);
-  return fmax(v, __builtin_bit_cast(double, (uint64_t)ohi << 32 | olo));
-}
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_max(double v) {
-  v = dpp_max<0xB1>(v);
-  v = dpp_max<0x4E>(v);
-  v = dpp_max<0x141>(v);
-  v = dpp_max<0x140>(v);
-  v = dpp_max<0x142, 0xA>(v);
-  v = dpp_max<0x143, 0xC>(v);
-  return lane_value(v, 63);
-}
-template <typename F>
-__device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
 
 // Keeps the two largest of (t1 >= t2) and v.
 __device__ __forceinline__ void top2_add(double& t1, double& t2, double v) {
@@ -262,30 +231,6 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
 // Weights are fp64 from the chosen logits in either case. 16384 tokens x 256
 // experts, 8 groups, top 8: 8 rounds of the fp64 maximum over a wave per token
 // took 33 us.
-template <int CTRL>
-__device__ __forceinline__ uint32_t row_dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
-}
-template <int CTRL>
-__device__ __forceinline__ float row_dpp(float v) {
-  return __uint_as_float(row_dpp<CTRL>(__float_as_uint(v)));
-}
-template <int CTRL>
-__device__ __forceinline__ double row_dpp(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)row_dpp<CTRL>((uint32_t)(b >> 32)) << 32 |
-                                        row_dpp<CTRL>((uint32_t)b));
-}
-// op over the 16 lanes of a row, in every lane: pairs, quads, then the mirrored
-// quad and the mirrored half.
-template <typename F, typename Op>
-__device__ __forceinline__ F row_reduce(F v, Op op) {
-  v = op(v, row_dpp<0xB1>(v));
-  v = op(v, row_dpp<0x4E>(v));
-  v = op(v, row_dpp<0x141>(v));
-  return op(v, row_dpp<0x140>(v));
-}
-
 // Up to here a wave per token is faster: a wave of four tokens has four times as
 // much to do before the first is done (16384 x 256, us, wave per token and this:
 // 64 tokens 6.3 and 7.0, 4096 11.1 and 11.9, 8192 18.5 and 15.7, 16384 33 and 16).
@@ -404,9 +349,9 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
       t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
       t1 = fmaxf(t1, o1);
     };
-    if (lpg > 1) merge(row_dpp<0xB1>(t1), row_dpp<0xB1>(t2));
-    if (lpg > 2) merge(row_dpp<0x4E>(t1), row_dpp<0x4E>(t2));
-    if (lpg > 4) merge(row_dpp<0x141>(t1), row_dpp<0x141>(t2));
+    if (lpg > 1) merge(dpp_move<0xB1>(t1, t1), dpp_move<0xB1>(t2, t2));
+    if (lpg > 2) merge(dpp_move<0x4E>(t1, t1), dpp_move<0x4E>(t2, t2));
+    if (lpg > 4) merge(dpp_move<0x141>(t1, t1), dpp_move<0x141>(t2, t2));
     const float score = p.top2 && gs > 1 ? t1 + t2 : t1;
     int rank = 0;
     for (int g = 0; g < G; ++g) {
@@ -556,8 +501,7 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(GateBwdArgs p) {
     } else {
       m = on ? zc : -INFINITY;
     }
-#pragma unroll
-    for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+    m = wave_max(m);
     if (full) {
 #pragma unroll
       for (int i = 0; i < KPL; ++i) {

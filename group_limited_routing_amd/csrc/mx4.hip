@@ -8,6 +8,7 @@
 // consecutive elements of a row share an E8M0 scale 2^(byte - 127).
 #include "common.h"
 #include "operators.h"
+#include "wave.h"
 
 #include <algorithm>
 
@@ -79,10 +80,8 @@ __global__ __launch_bounds__(256) void mx4_quantize_kernel(const T* __restrict__
       const uint32_t a = __float_as_uint(v[u]) & 0x7fffffffu;
       m = a > m ? a : m;
     }
-    uint32_t o = __shfl_xor(m, 1);
-    m = o > m ? o : m;
-    o = __shfl_xor(m, 2);
-    m = o > m ? o : m;
+    m = max(m, dpp_move<0xB1>(m, m));
+    m = max(m, dpp_move<0x4E>(m, m));
     const bool bad = m >= 0x7f800000u;
     const uint32_t byte = bad ? 255u : (uint32_t)max((int)(m >> 23) - 2, 0);
     const float inv = __uint_as_float((254u - (bad ? 127u : byte)) << 23);

@@ -11,6 +11,7 @@
 // loaded it from its load to its last use.
 #include "common.h"
 #include "operators.h"
+#include "wave.h"
 
 #include <algorithm>
 
@@ -119,27 +120,11 @@ __device__ __forceinline__ void store_unit(T* p, int tid, int nt, int j, int H, 
 }
 
 // ------------------------------------------------------------------ sums
-template <typename F>
-__device__ __forceinline__ F wave_sum(F v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-template <typename F>
-__device__ __forceinline__ F wave_amax(F v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const F x = __shfl_xor(v, o);
-    v = x > v ? x : v;
-  }
-  return v;
-}
-
 // Sum / maximum over the row's waves, in every thread: wave results through
 // LDS in wave order (the same order for every thread and every run).
 template <bool MAX, typename F>
-__device__ __forceinline__ F row_reduce(F v, F* lds, int nwaves) {
-  v = MAX ? wave_amax(v) : wave_sum(v);
+__device__ __forceinline__ F block_reduce(F v, F* lds, int nwaves) {
+  v = MAX ? wave_max(v) : wave_sum(v);
   if (nwaves == 1) return v;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -220,7 +205,7 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
       store_unit<VEC>((T*)p.stream_out + off, tid, nt, j, H, v);
     }
   }
-  sq = row_reduce<false>(sq, lds[0], nwaves);
+  sq = block_reduce<false>(sq, lds[0], nwaves);
   F r;
   if constexpr (QUANT)
     r = 1.0 / sqrt(sq / H + (double)p.eps);
@@ -251,7 +236,7 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
         const double a = fabs(s[j][u]);
         m = a > m ? a : m;
       }
-    m = row_reduce<true>(m, lds[1], nwaves);
+    m = block_reduce<true>(m, lds[1], nwaves);
     const double ym = m * r;
     const bool zero = m == 0;
     const double inv = zero ? 0.0 : 448.0 / m;
@@ -289,10 +274,8 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
         const uint32_t hi = (uint32_t)(__builtin_bit_cast(uint64_t, y[u]) >> 32) & 0x7fffffffu;
         top = hi > top ? hi : top;
       }
-      uint32_t o = __shfl_xor(top, 1);
-      top = o > top ? o : top;
-      o = __shfl_xor(top, 2);
-      top = o > top ? o : top;
+      top = max(top, dpp_move<0xB1>(top, top));
+      top = max(top, dpp_move<0x4E>(top, top));
       const int be = (int)(top >> 20);  // biased exponent; 0x7ff: infinity or NaN in the block
       const int e = min(max(be - 1023 - 8, -127), 127);
       const double inv = __builtin_bit_cast(double, (uint64_t)(1023 - e) << 52);
