@@ -167,6 +167,11 @@ __device__ __forceinline__ u32x2 e4m3x8(const float (&v)[8]) {
 // to the exact quotient, not to one with an fp32 rounding on either side of a
 // border. fp64 runs at the unpacked fp32 rate here and the kernel is bound by
 // memory. Without an 8-bit output everything is fp32.
+// Bound by memory where there are many rows: 8192 x 5120 bf16 with the stream's
+// update, E4M3 blocks and no bf16 output 58 us (295 MB, 5.0 TB/s; a large copy
+// reaches 5.2). Few rows wait for one row's chain of loads and two reductions:
+// 64 x 5120 with row scales and a bf16 output 5.6 us, one row 3.2 us. Narrow rows
+// with an 8-bit output are bound by fp64: 65536 x 256 45 us, 22 us without.
 template <typename T, bool VEC, int V, int QUANT>
 __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormArgs p, int nt) {
   using F = typename std::conditional<QUANT != 0, double, float>::type;
@@ -301,7 +306,11 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
 //   dw = sum over rows of dy n.
 // A workgroup walks the rows b, b + gridDim.x, ...; it keeps its partial dw in
 // registers over all of them and writes it once (norm_dw_kernel adds the
-// partials in order: no atomics).
+// partials in order: no atomics). The rows stay packed across the reduction
+// (repack), so that three of them and the partial fit in registers.
+// Bound by memory: 16384 x 5120 bf16, five arrays of 168 MB, 154 us with the
+// weight gradient (5.4 TB/s) and 141 us without; 1537 x 1001 fp32 (rows that
+// start anywhere, 4 bytes a lane) 12 and 6 us.
 template <typename T, bool VEC, int V, bool DW>
 __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
   __shared__ float lds[2][2][16];  // double buffered over rows: one barrier per row
@@ -382,15 +391,28 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(N
     }
   }
   if (DW) {
-    // rows side by side have partials of their own
-    float* out = p.part + (size_t)(nt == 64 ? first : (int)blockIdx.x) * H;
+    float* out = p.part + (size_t)blockIdx.x * H;
+    if constexpr (V == 1) {  // rows of one wave have one unit: the waves' sums are added
+      __shared__ float side[4][8][64];
+      if (nt == 64) {
+        const int wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) side[wave][u][tid] = dw[0][u];
+        __syncthreads();
+        if (wave > 0) return;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          for (int i = 1; i < per; ++i) dw[0][u] += side[i][u][tid];
+      }
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) store_unit<VEC>(out, tid, nt, j, H, dw[DW ? j : 0]);
   }
 }
 
 // dw[c] = sum over the groups of part[group, c]: 32 columns per workgroup, 32
-// shares of the groups side by side, added in order.
+// shares of the groups side by side, added in order. 768 partials of 5120 values
+// (16 MB, from L2 and the last-level cache) 4.5 us.
 __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, int groups,
                                                        int H, float* __restrict__ dw) {
   __shared__ float lds[32][33];
@@ -475,12 +497,16 @@ void bwd_units(const NormBwdArgs& a, RowShape rs, int grid, hipStream_t st) {
     bwd_launch<T, VEC, 8>(a, rs.nt, grid, st);
 }
 
-constexpr int kNormThreads = 512;     // threads of a row before it takes more units
+// Threads of a row before it takes more units. Less threads with more units each
+// leave a row longer on its way where there are few rows, and nothing is gained
+// with many: 512 and 256 threads at 5120 values, forward 64 rows 5.6 and 6.5 us,
+// 8192 rows 58 and 63; backward 64 rows 6.9 and 7.2, 16384 rows 154 and 155.
+constexpr int kNormThreads = 512;
 
 // Workgroups of the backward pass with a weight gradient, each with a partial of H
-// values that is written and read again. At 16384 x 5120 (bf16): 256 workgroups
-// 186 us, 512 219, 768 176, 1024 180, 2048 177; at 1537 x 1001 (fp32) 16, 12.5,
-// 12.2, 13.2 and 15.7. Without the weight gradient 146 us (5.7 TB/s).
+// values that is written and read again. bf16, us, 512 / 768 / 1024 workgroups:
+// 65536 x 256 44 / 40 / 38, 65536 x 512 65 / 65 / 67, 8192 x 512 13.2 / 12.9 / 13.7;
+// 16384 x 5120 was 219 / 176 / 180 when the reductions still cost more.
 constexpr int kNormBwdGroups = 768;
 
 }  // namespace
@@ -499,7 +525,7 @@ hipError_t launch_add_rms_norm(const NormArgs& a, int f32, int quant, hipStream_
 int norm_bwd_groups(int T, int H) {
   const RowShape rs = row_shape(H, kNormThreads);
   const int per = rs.nt == 64 ? 4 : 1;
-  return std::min((T + per - 1) / per, kNormBwdGroups / per) * per;
+  return std::min((T + per - 1) / per, kNormBwdGroups);
 }
 
 hipError_t launch_add_rms_norm_backward(const NormBwdArgs& a, int f32, hipStream_t st) {
@@ -507,7 +533,7 @@ hipError_t launch_add_rms_norm_backward(const NormBwdArgs& a, int f32, hipStream
   if (rs.nt > 1024) return hipErrorInvalidValue;
   const int per = rs.nt == 64 ? 4 : 1;
   const int groups = norm_bwd_groups(a.T, a.H);
-  const int grid = a.part ? groups / per : (a.T + per - 1) / per;
+  const int grid = a.part ? groups : (a.T + per - 1) / per;
   const bool vec = a.H % 8 == 0;
   if (f32)
     vec ? bwd_units<float, true>(a, rs, grid, st) : bwd_units<float, false>(a, rs, grid, st);

@@ -154,7 +154,7 @@ def test_norm_writes_its_rows_only():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (70, 64), (5, 512), (1100, 96), (33, 1001),
+@pytest.mark.parametrize("T,H", [(1, 1), (3, 7), (70, 64), (5, 512), (1100, 96), (3500, 72), (33, 1001),
                                  (2049, 520), (300, 5120), (3, 16384), (2, 20000), (1, 65536)])
 def test_norm_gradient(T, H, dtype):
     """ds adds two sums of H terms (at most 86 roundings each, one of them of
