@@ -42,7 +42,7 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route", "beam_moe_forward",
             "beam_moe_forward_shard", "beam_moe_forward_noalloc", "beam_moe_add_rms_norm",
             "beam_moe_add_rms_norm_backward_workspace_bytes", "beam_moe_add_rms_norm_backward",
             "beam_moe_gate", "beam_moe_gate_backward", "beam_moe_mx4_quantize",
-            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear_workspace_bytes",
+            "beam_moe_mx4_dequantize",
             "beam_moe_mx4_linear")
 
 # Scratch size of beam_moe_forward_noalloc (BEAM_MOE_NOALLOC_MAX_BYTES in the header)
@@ -186,9 +186,7 @@ def lib():
         L.beam_moe_gate_backward.argtypes = [gatep, i32, vp, vp, vp, vp, vp]
         L.beam_moe_mx4_quantize.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp]
         L.beam_moe_mx4_dequantize.argtypes = [vp, vp, i64, i32, i32, vp, vp]
-        L.beam_moe_mx4_linear_workspace_bytes.argtypes = [linp, i32]
-        L.beam_moe_mx4_linear_workspace_bytes.restype = sz
-        L.beam_moe_mx4_linear.argtypes = [linp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_moe_mx4_linear.argtypes = [linp, i32, vp, vp, vp, vp, vp, vp]
         for name in ("add_rms_norm", "add_rms_norm_backward", "gate", "gate_backward",
                      "mx4_quantize", "mx4_dequantize", "mx4_linear"):
             getattr(L, "beam_moe_" + name).restype = ctypes.c_int
@@ -782,8 +780,7 @@ def mx4_dequantize(codes, scales, *, dtype=torch.bfloat16, stream=None):
     return out
 
 
-def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, workspace=None,
-               stream=None):
+def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, stream=None):
     """x W^T with MXFP4 weights (row-major codes ``w`` [N, K / 2] and scales
     ``w_scale`` [N, K / 32], as from mx4_quantize()). The token rows ``x`` are
     E4M3 codes [T, K] (float8_e4m3fn) with ``x_scale`` fp32 [T] or E8M0 bytes
@@ -814,11 +811,8 @@ def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, wo
     with _on(dev, stream):
         if out is None:
             out = torch.empty(T, N, dtype=out_dtype, device=dev)
-        need = int(lib().beam_moe_mx4_linear_workspace_bytes(ctypes.byref(cfg), T))
-        workspace = _scratch(workspace, need, dev) if need else None
         _launch("beam_moe_mx4_linear", dev, lib().beam_moe_mx4_linear, ctypes.byref(cfg), T, _p(x),
-                _p(x_scale), _p(w), _p(w_scale), _p(out), _p(workspace),
-                0 if workspace is None else workspace.numel())
+                _p(x_scale), _p(w), _p(w_scale), _p(out))
     return out
 
 

@@ -770,8 +770,6 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
   return hipGetLastError();
 }
 
-size_t mx4_linear_workspace(int T, int N, int K, int x_mode) { return 0; }
-
 // Which kernel takes a product. A CU runs one workgroup of any of them at about
 // its own rate, so the time goes by how many rounds of 256 workgroups there are.
 // Tenths of a us a round at K = 5120 with E4M3 rows:

@@ -83,12 +83,10 @@ struct Mx4LinearArgs {
   const uint8_t* w;    // [N, K / 2] E2M1 codes
   const uint8_t* ws;   // [N, K / 32] E8M0
   void* out;           // [T, N]
-  float* part;         // workspace: partial sums of a split reduction
   int T, N, K;
   int out_f32;
 };
 // x_mode: 0 E4M3 with row scales, 1 E4M3 with block scales, 2 MXFP4
-size_t mx4_linear_workspace(int T, int N, int K, int x_mode);
 hipError_t launch_mx4_linear(const Mx4LinearArgs& a, int x_mode, hipStream_t st);
 
 }  // namespace beam

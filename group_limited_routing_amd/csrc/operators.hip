@@ -185,23 +185,16 @@ beam_status beam_moe_mx4_dequantize(const void* codes, const void* scales, int64
                                         out_dtype == BEAM_F32, out, (hipStream_t)stream));
 }
 
-size_t beam_moe_mx4_linear_workspace_bytes(const beam_moe_linear* cfg, int32_t T) {
-  if (check_linear(cfg, T) != BEAM_OK || T == 0) return 0;
-  return mx4_linear_workspace(T, cfg->n, cfg->k, cfg->x_format);
-}
-
 beam_status beam_moe_mx4_linear(const beam_moe_linear* cfg, int32_t T, const void* x,
                                 const void* x_scale, const void* w, const void* w_scale,
-                                void* out, void* workspace, size_t workspace_bytes, void* stream) {
+                                void* out, void* stream) {
   const beam_status cs = check_linear(cfg, T);
   if (cs != BEAM_OK) return cs;
   if (T == 0) return BEAM_OK;
   if (!x || !x_scale || !w || !w_scale || !out) return BEAM_ERR_NULL;
-  const size_t need = mx4_linear_workspace(T, cfg->n, cfg->k, cfg->x_format);
-  if (need && (!workspace || workspace_bytes < need)) return BEAM_ERR_WORKSPACE;
-  if (any_misaligned(x, x_scale, w, w_scale, out, workspace)) return BEAM_ERR_ALIGN;
+  if (any_misaligned(x, x_scale, w, w_scale, out)) return BEAM_ERR_ALIGN;
   const Mx4LinearArgs a{(const uint8_t*)x, x_scale, (const uint8_t*)w, (const uint8_t*)w_scale,
-                        out, (float*)workspace, T, cfg->n, cfg->k, cfg->out_dtype == BEAM_F32};
+                        out, T, cfg->n, cfg->k, cfg->out_dtype == BEAM_F32};
   return launched(launch_mx4_linear(a, cfg->x_format, (hipStream_t)stream));
 }
 

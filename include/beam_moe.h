@@ -564,8 +564,6 @@ typedef enum beam_x_format {
  *               beam_moe_mx4_quantize make them).
  *   w, w_scale  row-major codes [n, k / 2] and scales [n, k / 32].
  *   out         out [T, n], out_dtype (BEAM_BF16 or BEAM_F32).
- *   workspace   device scratch of beam_moe_mx4_linear_workspace_bytes(cfg, T)
- *               (which may be 0: then it may be NULL).
  * Supported: n in [1, 1048576], k a multiple of 32 in [32, 65536].
  */
 typedef struct beam_moe_linear {
@@ -575,11 +573,9 @@ typedef struct beam_moe_linear {
   int32_t out_dtype; /* beam_dtype */
 } beam_moe_linear;
 
-size_t beam_moe_mx4_linear_workspace_bytes(const beam_moe_linear* cfg, int32_t T);
-
 beam_status beam_moe_mx4_linear(const beam_moe_linear* cfg, int32_t T, const void* x,
                                 const void* x_scale, const void* w, const void* w_scale,
-                                void* out, void* workspace, size_t workspace_bytes, void* stream);
+                                void* out, void* stream);
 
 /* Static, NUL-terminated description of a status code; never NULL. */
 const char* beam_moe_status_string(int32_t status);

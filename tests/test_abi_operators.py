@@ -140,12 +140,11 @@ def test_mx4_row_checks(L):
         assert L.beam_moe_mx4_dequantize(p[0], p[1], 4, 64, 1, p[2], None) == gl.BEAM_ERR_ALIGN
 
 
-def _linear(L, T=8, cfg=(640, 512, 0, gl.BEAM_BF16), ws_bytes=1 << 40, **over):
-    p = dict(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, out=FAKE, work=FAKE)
+def _linear(L, T=8, cfg=(640, 512, 0, gl.BEAM_BF16), **over):
+    p = dict(x=FAKE, xs=FAKE, w=FAKE, ws=FAKE, out=FAKE)
     p.update(over)
     c = ctypes.byref(gl.BeamMoeLinear(*cfg)) if cfg else None
-    return L.beam_moe_mx4_linear(c, T, p["x"], p["xs"], p["w"], p["ws"], p["out"], p["work"],
-                                 ws_bytes, None)
+    return L.beam_moe_mx4_linear(c, T, p["x"], p["xs"], p["w"], p["ws"], p["out"], None)
 
 
 def test_linear_checks(L):
@@ -155,21 +154,12 @@ def test_linear_checks(L):
                     ((640, 65568, 0, 1), gl.BEAM_ERR_SHAPE), ((640, 512, 3, 1), gl.BEAM_ERR_CONFIG),
                     ((640, 512, -1, 1), gl.BEAM_ERR_CONFIG), ((640, 512, 0, 2), gl.BEAM_ERR_DTYPE)]:
         assert _linear(L, cfg=cfg) == st, cfg
-        assert L.beam_moe_mx4_linear_workspace_bytes(ctypes.byref(gl.BeamMoeLinear(*cfg)), 8) == 0
     assert _linear(L, T=-1) == gl.BEAM_ERR_SHAPE
     for name in ("x", "xs", "w", "ws", "out"):
         assert _linear(L, **{name: None}) == gl.BEAM_ERR_NULL, name
-    for name in ("x", "xs", "w", "ws", "out", "work"):
+    for name in ("x", "xs", "w", "ws", "out"):
         assert _linear(L, **{name: FAKE + 8}) == gl.BEAM_ERR_ALIGN, name
-    assert _linear(L, T=0, x=None, work=None) == gl.BEAM_OK
-    # wherever a workspace is asked for, a missing or short one is refused
-    for T in (1, 8, 64, 256, 2048):
-        for fmt in (0, 1, 2):
-            cfg = (640, 8192, fmt, gl.BEAM_BF16)
-            need = L.beam_moe_mx4_linear_workspace_bytes(ctypes.byref(gl.BeamMoeLinear(*cfg)), T)
-            if need:
-                assert _linear(L, T=T, cfg=cfg, work=None) == gl.BEAM_ERR_WORKSPACE
-                assert _linear(L, T=T, cfg=cfg, ws_bytes=need - 1) == gl.BEAM_ERR_WORKSPACE
+    assert _linear(L, T=0, x=None) == gl.BEAM_OK
 
 
 def test_binding_refuses_bad_tensors():
