@@ -19,13 +19,23 @@ namespace beam {
 namespace {
 
 // ------------------------------------------------------------------ rows
-// A row is held by NT threads, V units of 8 values each. VEC (H a multiple of
-// 8, so every row is 16-byte aligned): unit j of thread i is the chunk
-// i + j NT, read and written 16 bytes at a time. Else: value u of unit j is
-// element i + (8 j + u) NT, one at a time, neighbours in neighbouring lanes.
-template <bool VEC>
-__device__ __forceinline__ int elem(int tid, int nt, int j, int u) {
-  return VEC ? (tid + j * nt) * 8 + u : tid + (j * 8 + u) * nt;
+// A row is held by NT threads, V units of 8 values each: unit j of thread i is the
+// chunk i + j NT, read and written whole. kVec (H a multiple of 8): every row, so
+// every chunk, is 16-byte aligned. Else a chunk starts at any element, which the
+// memory unit allows, and the row's last one is taken value by value; of fp32 rows
+// a unit is then 8 / CH chunks of CH values, NT chunks apart, so that neighbouring
+// lanes read neighbouring bytes. Odd rows, us, value by value and in chunks:
+//   bf16, 8192 x 5001: row scales 293 and 83, without 162 and 76, gradient 263 and 142
+//   fp32, 4096 x 5001: row scales 169 and 71 (chunks of 4); the gradient, which
+//   also writes fp32 partials, 90 and 96 (chunks of 8: 107), so it takes single values
+enum Form { kVec, kAny, kFour, kOne };
+template <Form F>
+constexpr int kChunk = F == kFour ? 4 : F == kOne ? 1 : 8;
+// The element that value u of a unit is; u a multiple of the chunk.
+template <Form F>
+__device__ __forceinline__ int elem(int tid, int nt, int j, int u = 0) {
+  constexpr int CH = kChunk<F>;
+  return (tid + (j * (8 / CH) + u / CH) * nt) * CH;
 }
 
 // 8 raw values of a row: bf16 pairs or fp32.
@@ -44,6 +54,7 @@ struct Raw<uint16_t> {
       v[u >> 1] = b;
   }
   __device__ __forceinline__ void load(const uint16_t* p) { v = ld16(p); }
+  __device__ __forceinline__ void load_any(const uint16_t* p) { __builtin_memcpy(&v, p, 16); }
   // From here on the values are unpacked again from the packed form: their fp32
   // forms are not kept in registers across the row's reduction.
   __device__ __forceinline__ void repack() {
@@ -68,26 +79,46 @@ struct Raw<float> {
     lo = ld16(p);
     hi = ld16(p + 4);
   }
+  __device__ __forceinline__ void load_any(const float* p) {
+    __builtin_memcpy(&lo, p, 16);
+    __builtin_memcpy(&hi, p + 4, 16);
+  }
   __device__ __forceinline__ void repack() {}
 };
 
 // Unit j of the row at p; values past the row read as 0.
-template <typename T, bool VEC>
+template <Form F, typename T>
 __device__ __forceinline__ Raw<T> load_unit(const T* p, int tid, int nt, int j, int H) {
   Raw<T> r;
-  if constexpr (VEC) {
-    const int e = elem<true>(tid, nt, j, 0);
-    if (e < H) {
-      r.load(p + e);
-    } else {
+  if constexpr (F == kFour) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) r.set(u, T(0));
+    for (int h = 0; h < 8; h += 4) {
+      const int e = elem<F>(tid, nt, j, h);
+      u32x4 v{};
+      if (e + 4 <= H) {
+        __builtin_memcpy(&v, p + e, 16);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = e + u < H ? __float_as_uint(p[e + u]) : 0u;
+      }
+      (h ? r.hi : r.lo) = v;
     }
-  } else {
+  } else if constexpr (F == kOne) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int e = elem<false>(tid, nt, j, u);
+      const int e = elem<F>(tid, nt, j, u);
       r.set(u, e < H ? p[e] : T(0));
+    }
+  } else {
+    const int e = elem<F>(tid, nt, j);
+    if (F == kVec ? e < H : e + 8 <= H) {
+      if constexpr (F == kVec)
+        r.load(p + e);
+      else
+        r.load_any(p + e);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) r.set(u, F != kVec && e + u < H ? p[e + u] : T(0));
     }
   }
   return r;
@@ -96,25 +127,36 @@ __device__ __forceinline__ Raw<T> load_unit(const T* p, int tid, int nt, int j, 
 __device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
 
-template <bool VEC, typename T>
+template <Form F>
+__device__ __forceinline__ void store16(void* p, u32x4 v) {
+  if constexpr (F == kVec)
+    st16(p, v);
+  else
+    __builtin_memcpy(p, &v, 16);
+}
+
+template <Form F, typename T>
 __device__ __forceinline__ void store_unit(T* p, int tid, int nt, int j, int H, const float (&v)[8]) {
-  if constexpr (VEC) {
-    const int e = elem<true>(tid, nt, j, 0);
-    if (e >= H) return;
-    if constexpr (sizeof(T) == 2) {
-      st16(p + e, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                        pack_bf16x2(v[6], v[7])});
-    } else {
-      st16(p + e, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                        __float_as_uint(v[3])});
-      st16(p + e + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]),
-                            __float_as_uint(v[7])});
-    }
-  } else {
+  constexpr int CH = kChunk<F>;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int e = elem<false>(tid, nt, j, u);
-      if (e < H) store_value(p + e, v[u]);
+  for (int h = 0; h < 8; h += CH) {
+    const int e = elem<F>(tid, nt, j, h);
+    if constexpr (CH == 1) {
+      if (e < H) store_value(p + e, v[h]);
+    } else if (F == kVec ? e < H : e + CH <= H) {
+      if constexpr (sizeof(T) == 2) {
+        store16<F>(p + e, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])});
+      } else {
+#pragma unroll
+        for (int u = h; u < h + CH; u += 4)
+          store16<F>(p + e + u - h, u32x4{__float_as_uint(v[u]), __float_as_uint(v[u + 1]),
+                                          __float_as_uint(v[u + 2]), __float_as_uint(v[u + 3])});
+      }
+    } else if (F != kVec) {
+#pragma unroll
+      for (int u = 0; u < CH; ++u)
+        if (e + u < H) store_value(p + e + u, v[h + u]);
     }
   }
 }
@@ -171,11 +213,13 @@ __device__ __forceinline__ u32x2 e4m3x8(const float (&v)[8]) {
 // update, E4M3 blocks and no bf16 output 58 us (295 MB, 5.0 TB/s; a large copy
 // reaches 5.2). Few rows wait for one row's chain of loads and two reductions:
 // 64 x 5120 with row scales and a bf16 output 5.6 us, one row 3.2 us. Narrow rows
-// with an 8-bit output are bound by fp64: 65536 x 256 45 us, 22 us without.
+// with an 8-bit output are bound by fp64: 65536 x 256 45 us, 22 us without. Odd
+// rows: 8192 x 5001 83 us with row scales, 76 us without an 8-bit output.
 template <typename T, bool VEC, int V, int QUANT>
 __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormArgs p, int nt) {
-  using F = typename std::conditional<QUANT != 0, double, float>::type;
-  __shared__ F lds[2][16];
+  using A = typename std::conditional<QUANT != 0, double, float>::type;
+  constexpr Form F = VEC ? kVec : sizeof(T) == 2 ? kAny : kFour;
+  __shared__ A lds[2][16];
   const int nwaves = nt >> 6;
   // rows of one wave: four of them in a workgroup
   const int row = nt == 64 ? blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
@@ -187,17 +231,17 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
   Raw<T> xr[V], sr[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    xr[j] = load_unit<T, VEC>((const T*)p.x + off, tid, nt, j, H);
-    if (p.stream_in) sr[j] = load_unit<T, VEC>((const T*)p.stream_in + off, tid, nt, j, H);
+    xr[j] = load_unit<F, T>((const T*)p.x + off, tid, nt, j, H);
+    if (p.stream_in) sr[j] = load_unit<F, T>((const T*)p.stream_in + off, tid, nt, j, H);
   }
-  F s[V][8], sq = 0;
-  const F keep = p.keep, add = p.add;
+  A s[V][8], sq = 0;
+  const A keep = p.keep, add = p.add;
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      F h = add * (F)xr[j].get(u);
-      if (p.stream_in) h += keep * (F)sr[j].get(u);
+      A h = add * (A)xr[j].get(u);
+      if (p.stream_in) h += keep * (A)sr[j].get(u);
       s[j][u] = h;
       sq += h * h;
     }
@@ -207,11 +251,11 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
       float v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) v[u] = (float)s[j][u];
-      store_unit<VEC>((T*)p.stream_out + off, tid, nt, j, H, v);
+      store_unit<F>((T*)p.stream_out + off, tid, nt, j, H, v);
     }
   }
   sq = block_reduce<false>(sq, lds[0], nwaves);
-  F r;
+  A r;
   if constexpr (QUANT)
     r = 1.0 / sqrt(sq / H + (double)p.eps);
   else
@@ -220,14 +264,14 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
   // s becomes s w; y = r (s w)
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const Raw<float> w = load_unit<float, VEC>(p.w, tid, nt, j, H);
+    const Raw<float> w = load_unit<F, float>(p.w, tid, nt, j, H);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) s[j][u] *= (F)w.get(u);
+    for (int u = 0; u < 8; ++u) s[j][u] *= (A)w.get(u);
     if (p.y) {
       float v[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) v[u] = (float)(s[j][u] * r);
-      store_unit<VEC>((T*)p.y + off, tid, nt, j, H, v);
+      store_unit<F>((T*)p.y + off, tid, nt, j, H, v);
     }
   }
   if constexpr (QUANT == 1) {
@@ -252,14 +296,19 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
 #pragma unroll
       for (int u = 0; u < 8; ++u) v[u] = round_to_odd(s[j][u] * inv);
       const u32x2 c = e4m3x8(v);
-      if constexpr (VEC) {
-        const int e = elem<true>(tid, nt, j, 0);
-        if (e < H) *reinterpret_cast<u32x2*>(p.q + off + e) = c;
-      } else {
+      constexpr int CH = kChunk<F>;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int e = elem<false>(tid, nt, j, u);
-          if (e < H) p.q[off + e] = (uint8_t)(c[u >> 2] >> (8 * (u & 3)));
+      for (int h = 0; h < 8; h += CH) {
+        const int e = elem<F>(tid, nt, j, h);
+        if (F == kVec ? e < H : e + CH <= H) {
+          if constexpr (F == kVec)
+            *reinterpret_cast<u32x2*>(p.q + off + e) = c;
+          else
+            __builtin_memcpy(p.q + off + e, (const char*)&c + h, CH);
+        } else if (F != kVec) {
+#pragma unroll
+          for (int u = h; u < h + CH; ++u)
+            if (e + u - h < H) p.q[off + e + u - h] = (uint8_t)(c[u >> 2] >> (8 * (u & 3)));
         }
       }
     }
@@ -289,7 +338,7 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
       for (int u = 0; u < 8; ++u) v[u] = round_to_odd(y[u] * inv);
       u32x2 c = e4m3x8(v);
       if (be == 0x7ff) c = u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
-      const int at = elem<true>(tid, nt, j, 0);
+      const int at = elem<F>(tid, nt, j);
       if (at < H) {
         *reinterpret_cast<u32x2*>(p.q + off + at) = c;
         if ((tid & 3) == 0)
@@ -309,10 +358,13 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
 // partials in order: no atomics). The rows stay packed across the reduction
 // (repack), so that three of them and the partial fit in registers.
 // Bound by memory: 16384 x 5120 bf16, five arrays of 168 MB, 154 us with the
-// weight gradient (5.4 TB/s) and 141 us without; 1537 x 1001 fp32 (rows that
-// start anywhere, 4 bytes a lane) 12 and 6 us.
+// weight gradient (5.4 TB/s) and 141 us without; odd rows, 8192 x 5001 bf16, 142 us.
+// Rows over 16384 values need more registers than their threads have and spill: 512
+// x 65536 336 us (five arrays of 67 MB).
 template <typename T, bool VEC, int V, bool DW>
-__global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
+__global__ __launch_bounds__(V == 8 ? 1024 : 512)
+void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
+  constexpr Form F = VEC ? kVec : sizeof(T) == 2 ? kAny : kOne;
   __shared__ float lds[2][2][16];  // double buffered over rows: one barrier per row
   const int nwaves = nt >> 6;
   const int per = nt == 64 ? (blockDim.x >> 6) : 1;  // rows side by side in the workgroup
@@ -324,7 +376,7 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(N
   float dw[DW ? V : 1][8];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    w[j] = load_unit<float, VEC>(p.w, tid, nt, j, H);
+    w[j] = load_unit<F, float>(p.w, tid, nt, j, H);
     if (DW)
 #pragma unroll
       for (int u = 0; u < 8; ++u) dw[DW ? j : 0][u] = 0.f;
@@ -335,10 +387,10 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(N
     Raw<T> s[V], dy[V], d[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      s[j] = load_unit<T, VEC>((const T*)p.s + off, tid, nt, j, H);
-      dy[j] = load_unit<T, VEC>((const T*)p.dy + off, tid, nt, j, H);
+      s[j] = load_unit<F, T>((const T*)p.s + off, tid, nt, j, H);
+      dy[j] = load_unit<F, T>((const T*)p.dy + off, tid, nt, j, H);
       if (p.d_stream_out)
-        d[j] = load_unit<T, VEC>((const T*)p.d_stream_out + off, tid, nt, j, H);
+        d[j] = load_unit<F, T>((const T*)p.d_stream_out + off, tid, nt, j, H);
       else
         d[j] = Raw<T>{};
     }
@@ -386,8 +438,8 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(N
         a[u] = p.add * ds;
         b[u] = p.keep * ds;
       }
-      store_unit<VEC>((T*)p.dx + off, tid, nt, j, H, a);
-      if (p.d_stream_in) store_unit<VEC>((T*)p.d_stream_in + off, tid, nt, j, H, b);
+      store_unit<F>((T*)p.dx + off, tid, nt, j, H, a);
+      if (p.d_stream_in) store_unit<F>((T*)p.d_stream_in + off, tid, nt, j, H, b);
     }
   }
   if (DW) {
@@ -406,7 +458,7 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_bwd_kernel(N
       }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) store_unit<VEC>(out, tid, nt, j, H, dw[DW ? j : 0]);
+    for (int j = 0; j < V; ++j) store_unit<F>(out, tid, nt, j, H, dw[DW ? j : 0]);
   }
 }
 
