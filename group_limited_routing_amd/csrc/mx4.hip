@@ -177,6 +177,33 @@ __device__ __forceinline__ int swizzle(int row) {
   return ROW == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
 }
 
+// K not a multiple of 128: a row's K / 32 scale bytes start anywhere in a dword. The
+// aligned dwords that hold them are loaded, and a step's four bytes are cut out of
+// two neighbours; the bytes past the row's end count as 127 (2^0: their codes are
+// 0, and a 255 would make them NaN). Rows that are multiples of 4 apart start at the
+// same byte, so one count of bytes serves all of a lane's rows. Behind the last
+// scale of all up to 3 bytes of its own dword are read. (Loaded byte by byte where
+// they are needed, which waits for every load before them, the scales more than
+// doubled the time: 512 tokens, N = 5120, row scales, K = 5120 21 us, K = 5152 56 us.)
+struct ScaleCut {
+  uint32_t first, keep, fill;  // first byte of lane row r; the last step's bytes of the row
+  int last;
+  __device__ __forceinline__ ScaleCut(int r, int nb, int nk)
+      : first((r * nb) & 3), last(nk - 1) {
+    const int bytes = nb - 4 * (nk - 1);
+    keep = bytes == 4 ? ~0u : (1u << (8 * bytes)) - 1;
+    fill = 0x7f7f7f7fu & ~keep;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t lo, uint32_t hi, int kt) const {
+    const uint32_t v = __builtin_amdgcn_alignbyte(hi, lo, first);
+    return kt == last ? (v & keep) | fill : v;
+  }
+};
+// Offset of the last dword that holds scales of rows 0 .. row, from row 0's first.
+__device__ __forceinline__ uint32_t last_dword(int row, int nb) {
+  return (uint32_t)min(((uint64_t)row + 1) * nb - 1, (uint64_t)UINT32_MAX) & ~3u;
+}
+
 // ------------------------------------------------------------------ few tokens
 // Few tokens: the weights are read once and bound the time. A workgroup takes
 // 32 FN weight rows; its waves split the reduction, and each loads its own
@@ -185,7 +212,7 @@ __device__ __forceinline__ int swizzle(int row) {
 // added through LDS in wave order. (The same loads into registers, 16 bytes of 32
 // rows a lane pair, took 17 us for 64 tokens at N = K = 5120: each touches 32
 // lines. Through LDS a load is whole lines of 8 rows.)
-template <int XMODE, int TR, int FN>
+template <int XMODE, int TR, int FN, bool RAGGED>
 struct StreamShape {
   static constexpr int FM = TR > 32 ? TR / 32 : 1, WAVES = TR > 32 ? 4 : 8;
   static constexpr int XROW = XMODE == 2 ? 64 : 128;
@@ -193,7 +220,8 @@ struct StreamShape {
   static constexpr int BN = 32 * FN, WU = 2 * FN;          // weight rows and their loads
   static constexpr int SROWS = XMODE == 0 ? BN : BN + TR;  // rows with block scales
   static constexpr int SU = (SROWS + 63) / 64;
-  static constexpr int STAGE = (XU + WU) * 1024 + SU * 256;
+  static constexpr int SD = RAGGED ? 2 : 1;                // scale dwords of a row in a step
+  static constexpr int STAGE = (XU + WU) * 1024 + SD * SU * 256;
   static constexpr int NS0 = 158 * 1024 / WAVES / STAGE, NS = NS0 > 4 ? 4 : NS0;
   static constexpr int PITCH = BN + 4;  // floats of a staged output row, padded
   static constexpr int OUT = WAVES * FM * 32 * PITCH * 4;
@@ -204,10 +232,10 @@ struct StreamShape {
 template <int XMODE, int TR, int FN, bool RAGGED, bool OUT_F32>
 __global__ __launch_bounds__(TR > 32 ? 256 : 512)
 void mx4_linear_stream_kernel(Mx4LinearArgs p) {
-  using S = StreamShape<XMODE, TR, FN>;
+  using S = StreamShape<XMODE, TR, FN, RAGGED>;
   constexpr int FM = S::FM, XROW = S::XROW, XU = S::XU, WU = S::WU, SU = S::SU, NS = S::NS;
   constexpr int WAVES = S::WAVES, BN = S::BN, SOFF = (XU + WU) * 1024;
-  constexpr int PER = XU + WU + (RAGGED ? 0 : SU);
+  constexpr int PER = XU + WU + S::SD * SU;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S::LDS];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 31, h = lane >> 5;
@@ -237,13 +265,20 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
     wsrc[i] = min(row, nlast) * (K / 2) + c * 16;
     wk[i] = c * 32;
   }
-  // scale rows: the weights', then the tokens'; what is past them repeats a row
+  // scale rows: the weights', then the tokens'; what is past them repeats a row.
+  // Of ragged rows the aligned dwords are loaded (see below), the last of all at slast.
   const uint8_t* sbase[SU];
+  uint32_t slast[RAGGED ? SU : 1];
 #pragma unroll
   for (int i = 0; i < SU; ++i) {
     const int row = i * 64 + lane;
-    sbase[i] = row < BN || XMODE == 0 ? wsbase : xsbase;
-    ssrc[i] = (row < BN || XMODE == 0 ? min(row % BN, nlast) : min(row - BN, tlast)) * nb;
+    const bool of_w = row < BN || XMODE == 0;
+    sbase[i] = of_w ? wsbase : xsbase;
+    ssrc[i] = (of_w ? min(row % BN, nlast) : min(row - BN, tlast)) * nb;
+    if (RAGGED) {
+      ssrc[i] &= ~3u;
+      slast[RAGGED ? i : 0] = last_dword(of_w ? nlast : tlast, nb);
+    }
   }
   auto issue = [&](int kt, uint8_t* st) {
 #pragma unroll
@@ -259,24 +294,22 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
       dma16(src, st + XU * 1024 + i * 1024);
     }
 #if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (!RAGGED) {
 #pragma unroll
-      for (int i = 0; i < SU; ++i)
-        __builtin_amdgcn_global_load_lds(sbase[i] + kt * 4 + ssrc[i], st + SOFF + i * 256, 4, 0, 0);
-    }
+    for (int i = 0; i < SU; ++i)
+#pragma unroll
+      for (int d = 0; d < S::SD; ++d) {
+        const uint32_t at = ssrc[i] + (kt + d) * 4;
+        __builtin_amdgcn_global_load_lds(sbase[i] + (RAGGED ? min(at, slast[RAGGED ? i : 0]) : at),
+                                         st + SOFF + (i * S::SD + d) * 256, 4, 0, 0);
+      }
 #endif
   };
-  // K not a multiple of 128: rows of scales are not 4-byte aligned; the bytes of
-  // a step are read one by one, 127 (2^0) past the end
-  auto ragged_scales = [&](int kt, uint8_t* st) {
-#pragma unroll
-    for (int i = 0; i < SU; ++i) {
-      uint32_t v = 0;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        v |= (uint32_t)(kt * 4 + b < nb ? sbase[i][ssrc[i] + kt * 4 + b] : 127) << (8 * b);
-      *reinterpret_cast<uint32_t*>(st + SOFF + (i * 64 + lane) * 4) = v;
-    }
+  const ScaleCut cut(r, nb, nk);
+  auto scale = [&](const uint8_t* st, int row, int kt) {
+    const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + SOFF);
+    if constexpr (!RAGGED) return sc[row];
+    const uint32_t* at = sc + (row >> 6) * 128 + (row & 63);
+    return cut(at[0], at[64], kt);
   };
 
   f32x16 acc[FM][FN];
@@ -288,20 +321,19 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
       for (int q = 0; q < 16; ++q) acc[i][n][q] = 0.f;
   const int rx = TR < 32 ? r & (TR - 1) : r;  // fewer than 32 rows stand twice
   const int xsw = swizzle<XROW>(rx), wsw = swizzle<64>(r);
-  auto multiply = [&](const uint8_t* st) {
-    const uint32_t* sc = reinterpret_cast<const uint32_t*>(st + SOFF);
+  auto multiply = [&](const uint8_t* st, int kt) {
     int ws[FN];
     u32x4 w[FN][2];
 #pragma unroll
     for (int n = 0; n < FN; ++n) {
-      ws[n] = (int)(sc[n * 32 + r] >> (8 * h));
+      ws[n] = (int)(scale(st, n * 32 + r, kt) >> (8 * h));
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         w[n][j] = ld16(st + XU * 1024 + (n * 32 + r) * 64 + (((2 * j + h) ^ wsw) << 4));
     }
     for_each<FM>([&](auto ic) {
       constexpr int I = decltype(ic)::value;
-      const int xs = XMODE == 0 ? 0x7f7f7f7f : (int)(sc[BN + I * 32 + rx] >> (8 * h));
+      const int xs = XMODE == 0 ? 0x7f7f7f7f : (int)(scale(st, BN + I * 32 + rx, kt) >> (8 * h));
       const uint8_t* xr = st + (I * 32 + rx) * XROW;
       for_each<2>([&](auto jc) {
         constexpr int J = decltype(jc)::value;
@@ -331,13 +363,12 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
   int slot = 0;
   for (int kt = k0; kt < k1; ++kt) {
     uint8_t* st = ring + slot;
-    if (RAGGED) ragged_scales(kt, st);
     if (kt + NS - 1 < k1)
       wait_vmcnt<(NS - 1) * PER>();
     else
       wait_vmcnt<0>();
     asm volatile("" ::: "memory");
-    multiply(st);
+    multiply(st, kt);
     if (kt + NS < k1) {
       wait_lgkmcnt0();  // the step has been read
       asm volatile("" ::: "memory");
@@ -376,7 +407,7 @@ void mx4_linear_stream_kernel(Mx4LinearArgs p) {
 
 template <int XMODE, int TR, int FN>
 void stream_launch(const Mx4LinearArgs& a, hipStream_t st) {
-  using S = StreamShape<XMODE, TR, FN>;
+  using S = StreamShape<XMODE, TR, FN, false>;
   const int grid = (a.N + S::BN - 1) / S::BN * ((a.T + TR - 1) / TR), threads = 64 * S::WAVES;
   const bool ragged = a.K % 128 != 0;
   if (ragged && a.out_f32)
@@ -433,13 +464,18 @@ struct TileShape {
   static constexpr int NS = ROOM / STAGE > 4 ? 4 : ROOM / STAGE;
   static constexpr int OUT = WAVES * 32 * PITCH;
   static constexpr int LDS = NS * STAGE + 2 * SCALES > OUT ? NS * STAGE + 2 * SCALES : OUT;
-  static_assert(NS >= 2 && BN % 64 == 0 && BM % 64 == 0, "tile");
+  static_assert(NS >= 3 && BN % 64 == 0 && BM % 64 == 0, "tile");
 };
 
-template <int XMODE, int FM, int FN, int WM, int WN, bool RAGGED, bool OUT_F32>
+// How the scales come: four stages at a time, cut out of unaligned rows, or (fewer
+// than four stages) byte by byte.
+enum Scales { kAligned, kCut, kShort };
+
+template <int XMODE, int FM, int FN, int WM, int WN, Scales SC, bool OUT_F32>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   using S = TileShape<XMODE, FM, FN, WM, WN>;
+  constexpr bool RAGGED = SC != kAligned;  // the last stage may end within the row
   constexpr int BM = S::BM, BN = S::BN, XROW = S::XROW, NS = S::NS, WAVES = S::WAVES;
   // Loads of a stage: 1 KB of rows each, the tokens', then the weights'; and every
   // four stages 64 rows' scales each, the weights', then the tokens'. They are
@@ -486,31 +522,44 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   for (int q = 0; q < SI; ++q) {
     const int row = sunit(q) * 64 + lane;
     ssrc[q] = (sunit(q) < BN / 64 ? min(row, nlast) : min(row - BN, tlast)) * nb;
+    if (SC == kCut) ssrc[q] &= ~3u;
   }
   auto sbase = [&](int q) { return sunit(q) < BN / 64 ? wsbase : xsbase; };
   // Load q of stage kt, into the slot at byte `slot`. Addresses are a scalar
   // base and a lane offset.
-  auto issue_one = [&](int kt, int slot, auto qc) {
+  auto issue_one = [&](int kt, int slot, auto qc, bool end) {  // end: it is the last stage
     constexpr int Q = decltype(qc)::value;
     if constexpr (Q < PER) {
       const int u = unit(Q);
       const uint8_t* src = scalar(u < XU ? xbase + (size_t)kt * XROW : wbase + (size_t)kt * 64) + dsrc[Q];
-      if (RAGGED && kt * 128 + dk[RAGGED ? Q : 0] >= K) src = kZeros;
+      if (RAGGED && end && kt * 128 + dk[RAGGED ? Q : 0] >= K) src = kZeros;
       dma16(src, smem + slot + u * 1024);
     }
   };
   // Scales of stages 4 g .. 4 g + 3: 16 bytes of every row. The last group ends
-  // with the last stage, so that nothing is read past a row.
-  auto first_of = [&](int g) { return RAGGED ? 4 * g : min(4 * g, nk - 4); };
+  // with the last stage, so that nothing is read past a row (kCut: past the dword
+  // of its last stage; the one after it is loaded by itself, into the slot `tail`,
+  // when no stage needs that any more).
+  auto first_of = [&](int g) { return SC == kShort ? 4 * g : min(4 * g, nk - 4); };
   auto issue_scales = [&](int g) {
 #pragma unroll
     for (int q = 0; q < SI; ++q)
       dma16(scalar(sbase(q) + first_of(g) * 4) + ssrc[q], scales + (g & 1) * S::SCALES + sunit(q) * 1024);
   };
-  // K not a multiple of 128, or below 512: the bytes of a stage go through
-  // registers, 127 (2^0) past the end
-  auto ragged_scales = [&](int kt) {
-    uint8_t* at = scales + (kt >> 2 & 1) * S::SCALES + (kt & 3) * 4 + lane * 16;
+  int tail = 0;
+  auto issue_tail = [&](int slot) {
+    tail = slot;
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int q = 0; q < SI; ++q)
+      __builtin_amdgcn_global_load_lds(
+          sbase(q) + min(ssrc[q] + nk * 4, last_dword(sunit(q) < BN / 64 ? nlast : tlast, nb)),
+          smem + slot + sunit(q) * 256, 4, 0, 0);
+#endif
+  };
+  // fewer than four stages: the bytes of a stage go through registers
+  auto short_scales = [&](int kt) {
+    uint8_t* at = scales + (kt & 3) * 4 + lane * 16;
 #pragma unroll
     for (int q = 0; q < SI; ++q) {
       uint32_t v = 0;
@@ -573,14 +622,30 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   // needs of two fragments in a register: fragment f's of half J in byte 2 J + f % 2
   uint32_t wraw[FN], xraw[FM];
   int wsc[(FN + 1) / 2], xsc[(FM + 1) / 2];
+  const ScaleCut cut(r, nb, nk);
   auto read_scales = [&](int kt) {
     const int g = kt >> 2;
     const uint8_t* at = scales + (g & 1) * S::SCALES + (kt - first_of(g)) * 4;
+    const auto dword = [](const uint8_t* q) { return *reinterpret_cast<const uint32_t*>(q); };
 #pragma unroll
-    for (int j = 0; j < FN; ++j) wraw[j] = *reinterpret_cast<const uint32_t*>(at + wso + j * 512);
+    for (int j = 0; j < FN; ++j) wraw[j] = dword(at + wso + j * 512);
     if constexpr (XMODE != 0) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) xraw[i] = *reinterpret_cast<const uint32_t*>(at + xso + i * 512);
+      for (int i = 0; i < FM; ++i) xraw[i] = dword(at + xso + i * 512);
+    }
+    if constexpr (SC == kCut) {
+      // the dwords after them: the next group's first one has landed
+      const int g1 = (kt + 1) >> 2, pitch = kt + 1 < nk ? 16 : 4;
+      const uint8_t* next = kt + 1 < nk ? scales + (g1 & 1) * S::SCALES + (kt + 1 - first_of(g1)) * 4
+                                        : smem + tail;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        wraw[j] = cut(wraw[j], dword(next + (wrow + j * 32) * pitch), kt);
+      if constexpr (XMODE != 0) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          xraw[i] = cut(xraw[i], dword(next + (BN + xrow + i * 32) * pitch), kt);
+      }
     }
   };
   auto pick_scales = [&]() {
@@ -609,16 +674,16 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
     });
   };
 
-  if (!RAGGED) issue_scales(0);
+  if (SC != kShort) issue_scales(0);
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s)
-    if (s < nk) for_each<PER>([&](auto q) { issue_one(s, s * S::STAGE, q); });
-  if (RAGGED) ragged_scales(0);
+    if (s < nk) for_each<PER>([&](auto q) { issue_one(s, s * S::STAGE, q, s + 1 == nk); });
+  if (SC == kShort) short_scales(0);
   if (NS - 1 <= nk)
     wait_vmcnt<(NS - 2) * PER>();
   else
     wait_vmcnt<0>();
-  if (RAGGED) wait_lgkmcnt0();
+  if (SC == kShort) wait_lgkmcnt0();
   barrier_only();
   asm volatile("" ::: "memory");
   std::integral_constant<int, 0> j0;
@@ -629,17 +694,19 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
   pick_scales();
   int slot = 0, last = (NS - 1) * S::STAGE;  // of stage kt, and of the stage before it
   auto stage = [&](int kt, auto loads_c) {
-    constexpr bool LOADS = decltype(loads_c)::value;  // stage kt + NS - 1 exists
+    // stage kt + NS - 1: 0 there is none, 2 it is the last one
+    constexpr int LOADS = decltype(loads_c)::value;
     constexpr int LP = (PER + TURN - 1) / TURN;       // loads of a step, all before the barrier
     const int next = slot == (NS - 1) * S::STAGE ? 0 : slot + S::STAGE;
     // The scales of the next four stages: their buffer was last read before the
     // barrier of stage kt - 1; they are read three stages on, when the loads of
     // these three (more than any wait leaves outstanding) are behind them.
-    if (!RAGGED && (kt & 3) == 0 && kt + 4 < nk) issue_scales((kt >> 2) + 1);
+    if (SC != kShort && (kt & 3) == 0 && kt + 4 < nk) issue_scales((kt >> 2) + 1);
+    if (SC == kCut && !LOADS && kt + NS - 1 == nk) issue_tail(last);
     for_each<STEPS>([&](auto sc) {
       constexpr int I = decltype(sc)::value;
       if constexpr (I == TURN) {
-        if (RAGGED && kt + 1 < nk) ragged_scales(kt + 1);
+        if (SC == kShort && kt + 1 < nk) short_scales(kt + 1);
         wait_vmcnt<LOADS ? (NS - 2) * PER : 0>();
         wait_lgkmcnt0();
         barrier_only();
@@ -656,7 +723,8 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
       multiply(sc);
       if constexpr (LOADS && I < TURN)
         for_each<LP>([&](auto e) {
-          issue_one(kt + NS - 1, last, std::integral_constant<int, I * LP + decltype(e)::value>{});
+          issue_one(kt + NS - 1, last, std::integral_constant<int, I * LP + decltype(e)::value>{},
+                    LOADS == 2);
         });
       __builtin_amdgcn_sched_barrier(0);
     });
@@ -665,8 +733,9 @@ void mx4_linear_tile_kernel(Mx4LinearArgs p) {
     slot = next;
   };
   int kt = 0;
-  for (; kt + NS - 1 < nk; ++kt) stage(kt, std::true_type{});
-  for (; kt < nk; ++kt) stage(kt, std::false_type{});
+  for (; kt + NS - 1 < nk - (RAGGED ? 1 : 0); ++kt) stage(kt, j1);
+  if (RAGGED && kt + NS - 1 < nk) stage(kt++, std::integral_constant<int, 2>{});
+  for (; kt < nk; ++kt) stage(kt, j0);
 
   // Output: lane (r, h) of a fragment holds token r, columns 8 q + 4 h .. + 3.
   // 32 tokens of the wave at a time go through its own piece of the ring (rows
@@ -729,15 +798,19 @@ template <int XMODE, int FM, int FN, int WM, int WN>
 void tile_launch(const Mx4LinearArgs& a, hipStream_t st) {
   using S = TileShape<XMODE, FM, FN, WM, WN>;
   const int grid = (a.T + S::BM - 1) / S::BM * ((a.N + S::BN - 1) / S::BN);
-  const bool ragged = a.K % 128 != 0 || a.K < 512;
-  if (ragged && a.out_f32)
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, true, true><<<grid, 64 * S::WAVES, 0, st>>>(a);
-  else if (ragged)
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, true, false><<<grid, 64 * S::WAVES, 0, st>>>(a);
-  else if (a.out_f32)
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, false, true><<<grid, 64 * S::WAVES, 0, st>>>(a);
+  auto go = [&](auto sc) {
+    constexpr Scales SC = decltype(sc)::value;
+    if (a.out_f32)
+      mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, SC, true><<<grid, 64 * S::WAVES, 0, st>>>(a);
+    else
+      mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, SC, false><<<grid, 64 * S::WAVES, 0, st>>>(a);
+  };
+  if (a.K <= 384)
+    go(std::integral_constant<Scales, kShort>{});
+  else if (a.K % 128 != 0)
+    go(std::integral_constant<Scales, kCut>{});
   else
-    mx4_linear_tile_kernel<XMODE, FM, FN, WM, WN, false, false><<<grid, 64 * S::WAVES, 0, st>>>(a);
+    go(std::integral_constant<Scales, kAligned>{});
 }
 
 constexpr int64_t kMaxGrid = 1 << 23;  // workgroups of 256: a launch has fewer than 2^32 threads

@@ -562,7 +562,10 @@ typedef enum beam_x_format {
  * product (E2M1 products are narrower: nothing is cut).
  *   x, x_scale  token rows in x_format (beam_moe_add_rms_norm and
  *               beam_moe_mx4_quantize make them).
- *   w, w_scale  row-major codes [n, k / 2] and scales [n, k / 32].
+ *   w, w_scale  row-major codes [n, k / 2] and scales [n, k / 32]. With k not a
+ *               multiple of 128, scale rows are read in aligned 4-byte words: up
+ *               to 3 bytes behind the last scale, in its own word, are read too
+ *               and not used.
  *   out         out [T, n], out_dtype (BEAM_BF16 or BEAM_F32).
  * Supported: n in [1, 1048576], k a multiple of 32 in [32, 65536].
  */

@@ -234,6 +234,35 @@ def test_linear_beam_width(fmt):
         _linear_check(T, 5120, 5120, fmt, 74, rows=rows)
 
 
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+@pytest.mark.parametrize("K", [96, 160, 384, 416, 448, 480, 544, 672, 1184])
+@pytest.mark.parametrize("T,N", [(250, 5121), (500, 5100), (2020, 5115)])
+def test_linear_tiles_odd_reductions(T, N, K, fmt):
+    """Each of the large tiles with rows of scales that start at any byte."""
+    rows = torch.unique(torch.linspace(0, T - 1, 12).int()).long().to(_dev())
+    _linear_check(T, N, K, fmt, 79, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", ["row", "block", "mx4"])
+@pytest.mark.parametrize("T,N", [(5, 70), (50, 700), (250, 5121), (500, 5100), (2020, 5115)])
+@pytest.mark.parametrize("K", [160, 416, 544, 608])
+def test_linear_scales_behind_a_row_stay_out(T, N, K, fmt):
+    """A NaN scale at a row's start, right behind the row before it, is its own row's."""
+    x, xs, w, ws, _, _ = _operands(T, N, K, fmt, 80)
+    clean = gl.mx4_linear(x, xs, w, ws)
+    assert torch.isfinite(clean).all()
+    ws[1::7, 0] = 255
+    keep = torch.ones(N, dtype=torch.bool, device=_dev())
+    keep[1::7] = False
+    live = torch.ones(T, dtype=torch.bool, device=_dev())
+    if fmt != "row":
+        xs[1::5, 0] = 255
+        live[1::5] = False
+    got = gl.mx4_linear(x, xs, w, ws)
+    assert torch.equal(got[live][:, keep], clean[live][:, keep])
+    assert torch.isnan(got[:, ~keep]).all() and torch.isnan(got[~live]).all()
+
+
 @pytest.mark.parametrize("fmt", ["block", "mx4"])
 def test_linear_scales_are_each_their_own(fmt):
     """One block at a time with a scale of its own: every (row, block) pair of
