@@ -218,12 +218,13 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
 }
 
 // ------------------------------------------------------------------ four tokens a wave
-// Up to 256 experts in 1, 2, 4, 8 or 16 groups and top_k <= 16: 16 lanes per
+// Up to 512 experts in 1, 2, 4, 8 or 16 groups and top_k <= 16: 16 lanes per
 // token, a group on whole lanes, at most KPL experts a lane. The order is decided
 // on 32-bit keys: the score with its bias, or without a bias the logit itself
-// (the score grows with it), in fp32, its 24 leading bits in the order of unsigned
-// integers with 255 - expert below them. So a maximum is one integer maximum, it
-// says which expert it is, and ties go to the lower index. Where two neighbours of
+// (the score grows with it), in fp32, its 24 leading bits (23 with more than 16
+// experts a lane) in the order of unsigned integers, with 255 (511) - expert below
+// them. So a maximum is one integer maximum, it says which expert it is, and ties
+// go to the lower index. Where two neighbours of
 // the first top_k + 1 keys, or the last kept group and the first dropped one, lie
 // so near each other that the fp64 keys might stand the other way, the token is
 // done over in fp64 by the whole wave (about 1% of tokens with random logits).
@@ -233,10 +234,9 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
 // took 33 us.
 // Up to here a wave per token is faster: a wave of four tokens has four times as
 // much to do before the first is done (16384 x 256, us, wave per token and this:
-// 64 tokens 6.3 and 7.0, 4096 11.1 and 11.9, 8192 18.5 and 15.7, 16384 33 and 16).
+// 64 tokens 6.3 and 7.0, 4096 11.1 and 11.9, 8192 18.5 and 15.7, 16384 33 and 16;
+// 5000 x 512 17.3 and 16.4, 16384 x 512 51 and 28).
 constexpr int kWaveTokens = 4096;
-constexpr uint32_t kLow = 255;          // the expert's bits of a key
-constexpr uint32_t kMasked = kLow + 1;  // leading bits of a masked expert; a free slot is 0
 __device__ __forceinline__ uint32_t key_bits(float v) {
   const uint32_t b = __float_as_uint(v);
   return b ^ (b >> 31 ? 0xffffffffu : 0x80000000u);
@@ -268,6 +268,8 @@ __device__ __forceinline__ void load_share(const T* q, int c, int cnt, bool whol
 
 template <typename T, int KPL>
 __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
+  constexpr uint32_t kLow = 16 * KPL > 256 ? 511 : 255;  // the expert's bits of a key
+  constexpr uint32_t kMasked = kLow + 1;  // leading bits of a masked expert; a free slot is 0
   extern __shared__ double lds_keys[];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15;
   zero_counts(p);
@@ -589,7 +591,7 @@ hipError_t launch_gate(const GateArgs& args, int f32, hipStream_t st) {
   if (shares == 1) a.counts = nullptr;  // the count kernel writes them itself
   const size_t lds = a.n_group > 1 ? (size_t)4 * a.E * sizeof(double) : 0;
   const int G = a.n_group;
-  if (a.T > kWaveTokens && a.E <= 256 && G <= 16 && (G & (G - 1)) == 0 && a.k <= 16) {
+  if (a.T > kWaveTokens && a.E <= 512 && G <= 16 && (G & (G - 1)) == 0 && a.k <= 16) {
     const int lpg = 16 / G, c = (a.E / G + lpg - 1) / lpg;  // experts of a lane
     const int grid = (a.T + 15) / 16;
     auto go = [&](auto kpl) {
@@ -602,8 +604,10 @@ hipError_t launch_gate(const GateArgs& args, int f32, hipStream_t st) {
       go(std::integral_constant<int, 4>{});
     else if (c <= 8)
       go(std::integral_constant<int, 8>{});
-    else
+    else if (c <= 16)
       go(std::integral_constant<int, 16>{});
+    else
+      go(std::integral_constant<int, 32>{});
   } else {
     const int grid = (a.T + 3) / 4;
     by_keys(a.E, [&](auto c) {

@@ -68,7 +68,8 @@ def _check(z, k, bias=None, valid=None, kind="sigmoid", G=1, keep=1, pick="top2"
 # T, E, groups, kept, k: one expert, fewer than a wave, ragged, every width of a lane's share
 SHAPES = [(1, 1, 1, 1, 1), (5, 2, 1, 1, 2), (3, 5, 5, 2, 2), (37, 64, 1, 1, 6), (9, 65, 13, 4, 8),
           (130, 100, 4, 2, 7), (37, 160, 8, 3, 6), (66, 256, 8, 4, 8), (33, 256, 64, 9, 32),
-          (4, 333, 3, 3, 16), (21, 512, 16, 5, 10), (5, 1000, 8, 2, 12), (7, 1024, 1, 1, 32),
+          (4, 333, 3, 3, 16), (21, 512, 16, 5, 10), (40, 512, 1, 1, 16),
+          (40, 320, 16, 4, 9), (40, 500, 2, 1, 8), (5, 1000, 8, 2, 12), (7, 1024, 1, 1, 32),
           (6, 1024, 64, 8, 8)]
 
 
@@ -85,7 +86,8 @@ def test_gate_values(T, E, G, keep, k, kind):
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
-@pytest.mark.parametrize("E,G,keep,k", [(256, 8, 4, 8), (160, 8, 3, 6), (60, 1, 1, 4)])
+@pytest.mark.parametrize("E,G,keep,k", [(256, 8, 4, 8), (160, 8, 3, 6), (60, 1, 1, 4),
+                                        (512, 16, 5, 10), (333, 1, 1, 8)])
 def test_gate_ties(E, G, keep, k, kind):
     """Logits of few values: equal keys and equal group scores go to the lower index."""
     z = torch.round(_logits(64, E, 35, scale=1.0))
@@ -100,12 +102,12 @@ def test_gate_ties(E, G, keep, k, kind):
 def test_gate_near_ties_are_decided_by_the_values(kind):
     """Neighbouring fp32 logits, whose scores are equal in fp32, and biases
     that bring them within 1e-9 of each other, in any order."""
-    E = 128
-    base = torch.full((40, E), 0.75, device=_dev())
-    step = torch.randint(-3, 4, (40, E), generator=torch.Generator().manual_seed(37)).to(_dev())
-    z = (base.view(torch.int32) + step.int()).view(torch.float32)
-    _check(z, 8, None, None, kind)
-    _check(z, 8, _vec(E, 38, 1e-8), None, kind, 8, 3)
+    for E in (128, 400):
+        base = torch.full((40, E), 0.75, device=_dev())
+        step = torch.randint(-3, 4, (40, E), generator=torch.Generator().manual_seed(37)).to(_dev())
+        z = (base.view(torch.int32) + step.int()).view(torch.float32)
+        _check(z, 8, None, None, kind)
+        _check(z, 8, _vec(E, 38, 1e-8), None, kind, 8, 3)
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
