@@ -42,8 +42,7 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route", "beam_moe_forward",
             "beam_moe_forward_shard", "beam_moe_forward_noalloc", "beam_moe_add_rms_norm",
             "beam_moe_add_rms_norm_backward_workspace_bytes", "beam_moe_add_rms_norm_backward",
             "beam_moe_gate", "beam_moe_gate_backward", "beam_moe_mx4_quantize",
-            "beam_moe_mx4_dequantize",
-            "beam_moe_mx4_linear")
+            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear")
 
 # Scratch size of beam_moe_forward_noalloc (BEAM_MOE_NOALLOC_MAX_BYTES in the header)
 NOALLOC_MAX_BYTES = 64 << 20
@@ -607,6 +606,12 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _sizes(where, *sizes):
+    """Sizes that the library takes as 32-bit integers."""
+    if max(sizes) > 0x7fffffff:
+        raise BeamMoeError(BEAM_ERR_SHAPE, where)
+
+
 def add_rms_norm(x, norm_weight, *, stream_in=None, keep=1.0, add=1.0, norm_eps=1e-6, quant=None,
                  return_y=True, stream_out=None, stream=None):
     """The residual's addition and the RMS norm of the sum, in one pass:
@@ -628,6 +633,7 @@ def add_rms_norm(x, norm_weight, *, stream_in=None, keep=1.0, add=1.0, norm_eps=
     for t, name in ((stream_in, "stream_in"), (stream_out, "stream_out")):
         if t is not None:
             _check(t, name, (T, H), (x.dtype,), dev)
+    _sizes("beam_moe_add_rms_norm", T, H)
     cfg = BeamMoeNorm(H, _X_DTYPES[x.dtype], keep, add, norm_eps, _QUANTS[quant])
     y = q = scale = None
     with _on(dev, stream):
@@ -660,6 +666,7 @@ def add_rms_norm_backward(dy, s, norm_weight, *, d_stream_out=None, keep=1.0, ad
     _check(norm_weight, "norm_weight", (H,), _F32, dev)
     if d_stream_out is not None:
         _check(d_stream_out, "d_stream_out", (T, H), (dy.dtype,), dev)
+    _sizes("beam_moe_add_rms_norm_backward", T, H)
     cfg = BeamMoeNorm(H, _X_DTYPES[dy.dtype], keep, add, norm_eps, BEAM_QUANT_NONE)
     d_in = dw = None
     with _on(dev, stream):
@@ -733,6 +740,7 @@ def _gate_config(logits, top_k, score, n_group, topk_group, group_score, renorma
         raise ValueError(f"score {score!r} / group_score {group_score!r}: expected one of "
                          f"{tuple(_SCORES)} / {tuple(_GROUP_SCORES)}")
     _check(logits, "logits", logits.shape, _FLOATS, logits.device)
+    _sizes("beam_moe_gate", *logits.shape, top_k, n_group, topk_group)
     return BeamMoeGateConfig(logits.shape[1], n_group, topk_group, top_k, _SCORES[score],
                              _GROUP_SCORES[group_score], int(bool(renormalise)),
                              _X_DTYPES[logits.dtype], rsf)
@@ -753,6 +761,7 @@ def mx4_quantize(x, *, packed=False, stream=None):
         raise ValueError(f"x has rows of {C} values, expected a multiple of 32")
     if packed and x.shape[1] % 16:
         raise ValueError(f"x has {x.shape[1]} rows per expert, expected a multiple of 16")
+    _sizes("beam_moe_mx4_quantize", C)
     with _on(dev, stream):
         codes = torch.empty(*x.shape[:-1], C // 2, dtype=torch.uint8, device=dev)
         scales = torch.empty(*x.shape[:-1], C // 32, dtype=torch.uint8, device=dev)
@@ -773,6 +782,7 @@ def mx4_dequantize(codes, scales, *, dtype=torch.bfloat16, stream=None):
         raise ValueError(f"codes have rows of {C} values, expected a multiple of 32")
     _check(codes, "codes", codes.shape, _U8, dev)
     _check(scales, "scales", (*codes.shape[:-1], C // 32), _U8, dev)
+    _sizes("beam_moe_mx4_dequantize", C)
     with _on(dev, stream):
         out = torch.empty(*codes.shape[:-1], C, dtype=dtype, device=dev)
         _launch("beam_moe_mx4_dequantize", dev, lib().beam_moe_mx4_dequantize, _p(codes),
@@ -807,6 +817,7 @@ def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, st
         _check(out, "out", (T, N), _FLOATS, dev)
     if out_dtype not in _X_DTYPES:
         raise ValueError(f"out_dtype is {out_dtype}, expected one of {_FLOATS}")
+    _sizes("beam_moe_mx4_linear", T, N, K)
     cfg = BeamMoeLinear(N, K, fmt, _X_DTYPES[out_dtype])
     with _on(dev, stream):
         if out is None:

@@ -216,3 +216,19 @@ def test_binding_refuses_bad_tensors():
               lambda: gl.mx4_linear(xq, xs, wq, ws)):
         with pytest.raises(ValueError, match="expected a GPU"):
             f()
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """Sizes that would wrap in the library's 32-bit arguments are refused."""
+    big, bf, u8 = (1 << 32) + 4, torch.bfloat16, torch.uint8
+    rows, w = torch.empty(big, 0, dtype=bf), torch.empty(0)
+    for f in (lambda: gl.add_rms_norm(rows, w), lambda: gl.add_rms_norm_backward(rows, rows, w),
+              lambda: gl.gate(rows, top_k=1),
+              lambda: gl.gate(torch.zeros(4, 8), top_k=big),
+              lambda: gl.gate(torch.zeros(4, 8), top_k=1, n_group=big),
+              lambda: gl.gate_backward(torch.empty(big, 0), rows, torch.empty(big, 0, dtype=torch.int32)),
+              lambda: gl.mx4_linear(torch.empty(big, 0, dtype=u8), torch.empty(big, 0, dtype=u8),
+                                    torch.empty(4, 0, dtype=u8), torch.empty(4, 0, dtype=u8))):
+        with pytest.raises(gl.BeamMoeError) as e:
+            f()
+        assert e.value.status == gl.BEAM_ERR_SHAPE
