@@ -173,8 +173,8 @@ __device__ __forceinline__ const uint8_t* scalar(const uint8_t* p) {
 // group and on sums of 512), and sums are fp32. E2M1 products span 8 bits and need
 // one part. Whole E4M3 fragments, off by up to 3e-4 of a sum's magnitudes at K = 32 and
 // 4e-5 at K = 512, took half the matrix instructions: N = K = 5120, us, whole and in
-// parts, 1 token 4.9 and 5.9, 64 tokens 7.7 and 10.0, 512 tokens 21 and 36, 8192 tokens
-// with block scales 175 and 293.
+// parts, 1 token 4.9 and 5.9, 64 tokens 7.7 and 8.2, 512 tokens 21 and 36, 8192 tokens
+// with block scales 175 and 292.
 struct Parts {
   i32x8 hi, lo;
 };
@@ -216,7 +216,8 @@ __device__ __forceinline__ int swizzle(int row) {
 // same byte, so one count of bytes serves all of a lane's rows. Behind the last
 // scale of all up to 3 bytes of its own dword are read. (Loaded byte by byte where
 // they are needed, which waits for every load before them, the scales more than
-// doubled the time: 512 tokens, N = 5120, row scales, K = 5120 21 us, K = 5152 56 us.)
+// doubled the time: 512 tokens, N = 5120, row scales, E4M3 rows in one part, K = 5120
+// 21 us, K = 5152 56 us by bytes and 26 us so. In two parts, 36 and 41 us.)
 struct ScaleCut {
   uint32_t first, keep, fill;  // first byte of lane row r; the last step's bytes of the row
   int last;
@@ -244,9 +245,10 @@ __device__ __forceinline__ uint32_t last_dword(int row, int nb) {
 // added through LDS in wave order. (The same loads into registers, 16 bytes of 32
 // rows a lane pair, took 17 us for 64 tokens at N = K = 5120: each touches 32
 // lines. Through LDS a load is whole lines of 8 rows.) N = K = 5120, E4M3 rows: 1
-// token 5.9 us, 64 tokens 10.0 us (13.9 MB of weights), bound by the token rows, which
-// every workgroup reads from L2, 52 MB in all, and by taking them apart and multiplying
-// them twice, one wave a SIMD.
+// token 5.9 us, 64 tokens 8.2 us (13.9 MB of weights) by 32 x 64 workgroups, bound by
+// the token rows, which every workgroup reads from L2, and by taking them apart and
+// multiplying them twice; 1 token at N = K = 10240 15.8 us, 3.5 TB/s of weights. (All
+// figures with warm inputs: replays of a graph.)
 template <int XMODE, int TR, int FN, bool RAGGED>
 struct StreamShape {
   static constexpr int FM = TR > 32 ? TR / 32 : 1, WAVES = TR > 32 ? 4 : 8;
@@ -476,8 +478,8 @@ void stream_launch(const Mx4LinearArgs& a, hipStream_t st) {
 // scales of four stages are 16 bytes of a row and are loaded together, into one of
 // two buffers, while the four stages before them are multiplied (a load per stage,
 // 4 bytes of each row, was half of all requests to L2).
-// N = K = 5120, 8192 tokens: E4M3 rows 293 us (1.5 PF/s, 2.9 of instructions), 4-bit
-// rows 129 us (3.3 PF/s); each round of tiles starts and ends with 9 us outside its
+// N = K = 5120, 8192 tokens: E4M3 rows 292 us (1.5 PF/s, 2.9 of instructions), 4-bit
+// rows 121-129 us (3.3-3.5 PF/s); each round of tiles starts and ends with 9 us outside its
 // loop. Tiles of 128 fill LDS at
 // 50 GB/s per CU, which bounds them; rings of 160 KB and 8 waves a tile did not help
 // (1111 x 2560 x 5120, 4-bit rows: 17.3, 17.6 and 18.4 us).
@@ -901,35 +903,53 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
   return hipGetLastError();
 }
 
-// Which kernel takes a product. A CU runs one workgroup of any of them at about
-// its own rate, so the time goes by how many rounds of 256 workgroups there are.
-// Tenths of a us a round at K = 5120 with E4M3 rows:
-//   stream,  16 tokens x  32 columns   50      32 tokens x  32 columns   56
-//            16 tokens x  64 columns   65      32 tokens x  64 columns   79
-//            64 tokens x  32 columns   77      64 tokens x  64 columns  101
-//   tile,    64 tokens x 128 columns  143     128 tokens x 128 columns  205
-//           256 tokens x 256 columns  500
-// (4-bit rows: the tiles 130, 160 and 400.) Measured at N = K = 5120 around the
-// borders, us: T = 128, stream of 32 columns 14.1 and 64 x 128 tiles 14.5; T = 512,
-// 64 x 128 tiles 24.9 and 128 x 128 tiles 20.6; T = 2048, 128 x 128 tiles 57 and
-// 256 x 256 tiles 50; T = 4096, 102 and 109. At N = K = 10240: 1 token, streams of
-// 32 and 64 columns 17.0 and 15.3; 32 tokens 21.8 and 17.3.
+// Which kernel takes a product: the one whose rounds of 256 workgroups cost least. The
+// first round pays for the start and the first loads, a later one overlaps with the
+// one before it (of 64 and 128 token tiles two share a CU). Tenths of a us, first and
+// later rounds, at K = 5120 (at other K taken to be in the same proportion):
+//                            E4M3 rows   4-bit rows
+//   stream, 16 x  32          60   45     45   33
+//           16 x  64          85   70     68   60
+//           32 x  32          66   52     50   43
+//           32 x  64          95   72     72   66
+//           64 x  32         102   88     74   65
+//           64 x  64         145  125    105  100
+//   tile,   64 x 128         250  200    132  103
+//          128 x 128         355  290    155  155
+//          256 x 256         950  960    345  420
+// Measured around the borders, N = 5120, us, the kernel taken and the next best one.
+// E4M3 rows: T = 64, 32 x 64 9.0 and 64 x 32 10.3; 128, 64 x 64 14.0 and 32 x 64 16.5;
+// 256, 32 x 64 24.7 and 64 x 64 26.4; 384, 64 x 128 27.5 and 64 x 64 28.4; 512, 128 x
+// 128 36.7 and 64 x 128 39.9; 2048, 128 x 128 91.5 and 256 x 256 93.2; 3000, 256 x 256
+// 102 and 128 x 128 124; 4096, 128 x 128 161 and 256 x 256 189; 8192, 256 x 256 292 and
+// 128 x 128 314. 4-bit rows: T = 128, 64 x 64 10.4 and 64 x 128 12.9; 512, 128 x 128
+// 15.5 and 64 x 128 21.4; 2048, 256 x 256 36.3 and 128 x 128 46.3; 4096, 256 x 256 77.4
+// and 128 x 128 84.2.
 enum class Variant { kStream16, kStream16Wide, kStream32, kStream32Wide, kStream64, kStream64Wide,
                      kTile64, kTile128, kTile256 };
-Variant variant_of(int T, int N) {
+struct Cost {
+  int first, later;
+};
+Variant variant_of(int T, int N, bool mx4_rows) {
   struct {
     Variant v;
-    int bm, bn, cost;
-  } const all[] = {{Variant::kStream16, 16, 32, 50},   {Variant::kStream16Wide, 16, 64, 65},
-                   {Variant::kStream32, 32, 32, 56},   {Variant::kStream32Wide, 32, 64, 79},
-                   {Variant::kStream64, 64, 32, 77},   {Variant::kStream64Wide, 64, 64, 101},
-                   {Variant::kTile64, 64, 128, 143},   {Variant::kTile128, 128, 128, 205},
-                   {Variant::kTile256, 256, 256, 500}};
+    int bm, bn;
+    Cost e4m3, mx4;
+  } const all[] = {{Variant::kStream16, 16, 32, {60, 45}, {45, 33}},
+                   {Variant::kStream16Wide, 16, 64, {85, 70}, {68, 60}},
+                   {Variant::kStream32, 32, 32, {66, 52}, {50, 43}},
+                   {Variant::kStream32Wide, 32, 64, {95, 72}, {72, 66}},
+                   {Variant::kStream64, 64, 32, {102, 88}, {74, 65}},
+                   {Variant::kStream64Wide, 64, 64, {145, 125}, {105, 100}},
+                   {Variant::kTile64, 64, 128, {250, 200}, {132, 103}},
+                   {Variant::kTile128, 128, 128, {355, 290}, {155, 155}},
+                   {Variant::kTile256, 256, 256, {950, 960}, {345, 420}}};
   Variant best = Variant::kTile256;
   int64_t least = INT64_MAX;
   for (const auto& c : all) {
     const int64_t wgs = (int64_t)((T + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
-    const int64_t cost = (wgs + 255) / 256 * c.cost;
+    const Cost& us = mx4_rows ? c.mx4 : c.e4m3;
+    const int64_t cost = us.first + ((wgs + 255) / 256 - 1) * us.later;
     if (cost < least) {
       least = cost;
       best = c.v;
@@ -941,7 +961,7 @@ Variant variant_of(int T, int N) {
 hipError_t launch_mx4_linear(const Mx4LinearArgs& a, int x_mode, hipStream_t st) {
   auto go = [&](auto m) {
     constexpr int XMODE = decltype(m)::value;
-    switch (variant_of(a.T, a.N)) {
+    switch (variant_of(a.T, a.N, XMODE == 2)) {
       case Variant::kStream16: stream_launch<XMODE, 16, 1>(a, st); break;
       case Variant::kStream16Wide: stream_launch<XMODE, 16, 2>(a, st); break;
       case Variant::kStream32: stream_launch<XMODE, 32, 1>(a, st); break;
