@@ -1,0 +1,42 @@
+"""Routing of given logits and its gradient where values run out of fp32's
+range, stand in masked places or tie, against oracle.gate in float64. The
+tolerances are those of test_gpu_gate.py, whose checks are used."""
+
+import numpy as np
+import pytest
+import torch
+
+import group_limited_routing_amd as gl
+from test_gpu_gate import DT, _check, _dev, _grad_check, _logits, _vec
+
+pytestmark = pytest.mark.gpu
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("k", [1, 2, 8])
+def test_gradient_of_far_negative_sigmoids(k, renorm, dtype):
+    """Scores that fp32 holds as subnormals or not at all still share their sum.
+    Differences of a row's chosen logits are at most 6, so that an exponential's
+    rounded argument is 6 u off, below the 40 u that the tolerance has for it."""
+    level = torch.tensor([-80.0, -87.0, -88.0, -90.0, -100.0, -104.0, -120.0, -200.0, -600.0])
+    g = torch.Generator().manual_seed(61)
+    z = (level[:, None] - 5 * torch.rand((9, 40), generator=g)).to(DT[dtype]).to(_dev())
+    z[:, 30:] -= 1000.0
+    r = gl.gate(z, top_k=k, renormalise=renorm, routed_scaling_factor=2.5)
+    if renorm:
+        assert torch.allclose(r["topk_w"].sum(1), torch.full((9,), 2.5, device=_dev()), rtol=1e-6)
+    got = _grad_check(_vec(9 * k, 62, 1.0).view(9, k), z, r["topk_idx"], "sigmoid", renorm, 2.5)
+    if renorm and k > 1:
+        assert (got.abs().amax(1) > 1e-4).all()
+
+
+def test_gradient_of_mixed_sigmoids():
+    """One slot far above the others, positive and negative logits in one row."""
+    z = torch.tensor([[40.0, -40.0, 0.0, -100.0], [-90.0, -91.0, -120.0, -300.0],
+                      [100.0, 90.0, -100.0, 3.0], [-INF, -95.0, -95.0, -INF],
+                      [INF, 2.0, -3.0, -200.0]], device=_dev())
+    idx = torch.arange(4, dtype=torch.int32, device=_dev()).repeat(5, 1)
+    _grad_check(_vec(20, 63, 1.0).view(5, 4), z, idx, "sigmoid", True, 2.5)
