@@ -492,7 +492,9 @@ __global__ __launch_bounds__(256) void gate_backward_kernel(GateBwdArgs p) {
       zc = to_f32(zr[e]);
     }
   }
-  const bool on = zc > -INFINITY;  // a masked expert has score 0 and gradient 0
+  // a masked expert has score 0 and gradient 0, whatever arrives at its slot
+  const bool on = zc > -INFINITY;
+  if (!on) dw = 0.f;
 
   float f[KPL];
   const bool full = p.softmax && !p.renorm;

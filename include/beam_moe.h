@@ -516,7 +516,8 @@ beam_status beam_moe_gate(const beam_moe_gate_config* cfg, int32_t T, const void
  * experts is piecewise constant. fp32.
  *   d_topk_w  [T, top_k] fp32;  logits as above;  topk_idx [T, top_k] int32, as
  *   beam_moe_gate wrote it (an index outside [0, n_experts) is an empty slot:
- *   padding gets zero gradients; an index that stands twice counts twice).
+ *   padding gets zero gradients; an index that stands twice counts twice; what
+ *   d_topk_w holds at a masked expert's slot reaches nothing, NaN included).
  *   d_logits  out [T, n_experts], z_dtype. May not overlap logits.
  * cfg's n_group, topk_group and group_score are not used, but checked.
  */

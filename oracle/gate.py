@@ -61,13 +61,14 @@ def gate(z, top_k, bias=None, kind="sigmoid", n_group=1, topk_group=1, group_sco
 
 
 def gate_backward(dw, z, idx, kind="sigmoid", renormalise=True, rsf=1.0):
-    """Gradient of the logits [T, E]; slots with an index outside [0, E) are empty."""
+    """Gradient of the logits [T, E]; slots with an index outside [0, E) are empty,
+    and so are a masked expert's, whatever arrives there."""
     z, dw = np.asarray(z, dtype=np.float64), np.asarray(dw, dtype=np.float64)
     T, E = z.shape
     dz = np.zeros((T, E))
     for t in range(T):
-        f, _ = scores(z[t], kind)
-        slots = [j for j in range(idx.shape[1]) if 0 <= idx[t, j] < E]
+        f, on = scores(z[t], kind)
+        slots = [j for j in range(idx.shape[1]) if 0 <= idx[t, j] < E and on[idx[t, j]]]
         e = idx[t, slots]
         p, d = f[e], dw[t, slots]
         if renormalise:

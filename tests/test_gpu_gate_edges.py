@@ -40,3 +40,20 @@ def test_gradient_of_mixed_sigmoids():
                       [INF, 2.0, -3.0, -200.0]], device=_dev())
     idx = torch.arange(4, dtype=torch.int32, device=_dev()).repeat(5, 1)
     _grad_check(_vec(20, 63, 1.0).view(5, 4), z, idx, "sigmoid", True, 2.5)
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("junk", [float("nan"), INF, -INF])
+def test_gradient_passes_over_masked_slots(kind, renorm, junk):
+    """What arrives at a slot of a masked expert does not reach the others."""
+    z = _logits(6, 24, 64)
+    z[:, 5], z[:, 11] = -INF, float("nan")
+    idx = torch.tensor([[5, 1, 2], [3, 11, 4], [5, 11, 7], [0, 1, 5], [5, 11, -1], [11, 23, 24]],
+                       dtype=torch.int32, device=_dev())
+    dw = _vec(18, 65, 1.0).view(6, 3)
+    masked = (idx == 5) | (idx == 11) | (idx < 0) | (idx > 23)
+    clean = _grad_check(torch.where(masked, torch.zeros_like(dw), dw), z, idx, kind, renorm, 1.5)
+    got = gl.gate_backward(torch.where(masked, torch.full_like(dw, junk), dw), z, idx, score=kind,
+                           renormalise=renorm, routed_scaling_factor=1.5)
+    assert torch.equal(got, clean) and (got[4] == 0).all()
