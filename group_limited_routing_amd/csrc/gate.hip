@@ -355,7 +355,8 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
     if (lpg > 1) merge(dpp_move<0xB1>(t1, t1), dpp_move<0xB1>(t2, t2));
     if (lpg > 2) merge(dpp_move<0x4E>(t1, t1), dpp_move<0x4E>(t2, t2));
     if (lpg > 4) merge(dpp_move<0x141>(t1, t1), dpp_move<0x141>(t2, t2));
-    const float score = p.top2 && gs > 1 ? t1 + t2 : t1;
+    float score = p.top2 && gs > 1 ? t1 + t2 : t1;
+    if (!(score == score)) score = -INFINITY;  // +inf by its bias and a masked second
     int rank = 0;
     for (int g = 0; g < G; ++g) {
       const float o = __shfl(score, (lane & 48) + g * lpg);

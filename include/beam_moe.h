@@ -479,7 +479,8 @@ typedef enum beam_group_score {
  *   the top_k largest keys inside them are chosen, key descending;
  *   w = routed_scaling_factor * f, over the sum of the chosen f with
  *   renormalise.
- * Equal keys, and equal group scores, go to the lower index. Scores and keys
+ * Equal keys, and equal group scores, go to the lower index; a group score that
+ * is a NaN (a key of +inf beside one of -inf) counts as -inf. Scores and keys
  * are fp64. A logit of -inf or NaN masks its expert: score 0, chosen after
  * every other of its groups; so does a key of -inf or NaN, which keeps its
  * score. Where all chosen scores are 0, the weights are 0.

@@ -57,3 +57,22 @@ def test_gradient_passes_over_masked_slots(kind, renorm, junk):
     got = gl.gate_backward(torch.where(masked, torch.full_like(dw, junk), dw), z, idx, score=kind,
                            renormalise=renorm, routed_scaling_factor=1.5)
     assert torch.equal(got, clean) and (got[4] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_infinite_bias_in_a_masked_group(kind, dtype):
+    """A group whose two best keys are +inf and -inf has no score: it comes last,
+    in batches of any size."""
+    z = _logits(10, 96, 66, dtype)
+    bias = _vec(96, 67, 0.1)
+    bias[13] = INF
+    z[::2, 12:24] = -INF
+    z[::2, 13] = 0.5
+    for keep in (1, 2, 5):
+        with np.errstate(invalid="ignore"):
+            _check(z, 6, bias, None, kind, 8, keep, "top2")
+            _check(z, 6, bias, None, kind, 8, keep, "max")
+    bias[40] = INF
+    with np.errstate(invalid="ignore"):
+        _check(z, 6, bias, None, kind, 8, 2, "top2")
