@@ -229,7 +229,12 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs p) {
 // the first top_k + 1 keys, or the last kept group and the first dropped one, lie
 // so near each other that the fp64 keys might stand the other way, the token is
 // done over in fp64 by the whole wave (about 1% of tokens with random logits).
-// With bf16 logits and no bias the 24 bits are the logit, and equal ones are ties.
+// With bf16 logits and no bias the 24 bits are the logit, and equal ones are ties. Of
+// these, logits below 2^-20 other than 0 may share one fp64 score with any number of
+// others, 0 among them: where one is chosen, or may be hidden behind a 0 that is the
+// first not to be chosen, the token is done over too. Larger logits are 2^-29 apart or
+// more, which their scores show. (Looking for such logits in every token took bf16
+// softmax routing of 16384 x 256 from 8.7 to 12.6 us; so it takes 9.1.)
 // Weights are fp64 from the chosen logits in either case. 16384 tokens x 256
 // experts, 8 groups, top 8: 8 rounds of the fp64 maximum over a wave per token
 // took 33 us.
@@ -330,6 +335,7 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
   auto saturated = [&](float lower) {
     return p.softmax ? !(m - lower < 600.f) : !(lower < 16.f && lower > -600.f);
   };
+  const bool exact = sizeof(T) == 2 && !p.bias;
   bool near = false;
   uint32_t key[KPL];
 #pragma unroll
@@ -366,11 +372,11 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
     const float lo = row_reduce(kept ? score : INFINITY, [](float a, float b) { return fminf(a, b); });
     const float hi = row_reduce(kept ? -INFINITY : score, [](float a, float b) { return fmaxf(a, b); });
     if (!scored) {
-      near = !(lo - hi > 0x1p-28f) || saturated(hi);
+      near |= !(lo - hi > 0x1p-28f) || saturated(hi);
     } else {
       // a score is within 2^-21, and relative to itself within 2^-16 down to 1e-30
       // (its exponential's argument is rounded)
-      near = !(lo - hi > (p.bias ? 0x1p-18f * (fabsf(lo) + fabsf(hi) + 1.f) : 0x1p-15f * (lo + hi)));
+      near |= !(lo - hi > (p.bias ? 0x1p-18f * (fabsf(lo) + fabsf(hi) + 1.f) : 0x1p-15f * (lo + hi)));
       near |= !p.bias && !(lo > 1e-30f);
     }
     if (!kept) {
@@ -395,15 +401,24 @@ __global__ __launch_bounds__(256) void gate_rows_kernel(GateArgs p) {
   if (l == k - 1) after = next;
   int e = (int)(kLow - (mine & kLow));
   const float zc = l < k && live ? to_f32(zr[e]) : -INFINITY;
-  bool close = false;  // to the one after
+  bool close = false;    // to the one after
+  bool behind0 = false;  // the first key that is not chosen is 0, with others behind it
   if (l < k && after >= 2 * kMasked) {  // neither is masked
-    const bool exact = sizeof(T) == 2 && !p.bias;
     const float lo = key_value(mine & ~kLow), hi = key_value(exact ? after & ~kLow : after | kLow);
     // with a bias both keys are within 2^-20, and their sums' rounding; logits are
     // exact, but fp64 scores of logits this near could be equal
     const float tol = p.bias ? 0x1p-18f + 0x1p-21f * (fabsf(lo) + fabsf(hi)) : 0x1p-28f;
     close = !(lo - hi > tol || (exact && lo == hi));
     if (!p.bias) near |= saturated(hi);
+    // (-0, whose key lies below that of 0, shows as a tiny value too)
+    auto tiny = [](float x) { return x != 0.f && fabsf(x) < 0x1p-20f; };
+    if (exact) near |= tiny(lo) || tiny(hi);
+    behind0 = exact && l == k - 1 && hi == 0.f;
+  }
+  const uint64_t zeros = __ballot(behind0);
+  if ((zeros >> (lane & 48)) & 0xffff) {
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) near |= z[i] <= 0.f && z[i] > -0x1p-20f && __float_as_uint(z[i]) != 0u;
   }
 
   double f = 0;

@@ -76,3 +76,26 @@ def test_infinite_bias_in_a_masked_group(kind, dtype):
     bias[40] = INF
     with np.errstate(invalid="ignore"):
         _check(z, 6, bias, None, kind, 8, 2, "top2")
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,G,keep", [(64, 1, 1), (256, 8, 3), (500, 4, 2)])
+def test_ties_of_tiny_logits(E, G, keep, kind, dtype):
+    """Logits so small that their fp64 scores are equal, in twos and threes, and
+    zeros of either sign: the lower index comes first, wherever top_k cuts them."""
+    rows = []
+    for values in ([1e-30, 1e-30, 0.0], [1e-30, 0.0, 0.0], [0.0, -0.0, 0.0], [-0.0, 0.0, 1e-20],
+                   [2e-25, 2e-25, 1e-25], [-1e-30, -1e-30, -2e-30], [0.0, -1e-30, -0.0]):
+        for at in ([5, 7, 3], [9, 5, 7], [3, 5, 7], [40, 20, 60], [60, 40, 20]):
+            for ahead in (0, 2):
+                row = torch.full((E,), -2.0)
+                row[at] = torch.tensor(values)
+                row[50:50 + ahead] = 1.0
+                rows.append(row)
+    rows.append(torch.zeros(E))
+    rows.append(-torch.zeros(E))
+    z = torch.stack(rows).to(DT[dtype]).to(_dev())
+    for k in (1, 2, 3, 4, 5):
+        _check(z, k, None, None, kind, G, keep, "max")
+        _check(z, k, None, None, kind, G, keep, "top2")
