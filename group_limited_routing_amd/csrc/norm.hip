@@ -124,6 +124,8 @@ __device__ __forceinline__ Raw<T> load_unit(const T* p, int tid, int nt, int j, 
   return r;
 }
 
+__device__ __forceinline__ float load_value(const float* p) { return *p; }
+__device__ __forceinline__ float load_value(const uint16_t* p) { return bf16_bits_to_f32(*p); }
 __device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)f32_to_bf16_bits(v); }
 
@@ -175,6 +177,26 @@ __device__ __forceinline__ F block_reduce(F v, F* lds, int nwaves) {
   return s;
 }
 
+// Rows whose mean square, with eps, lies outside of [2^-40, 2^100]: there fp32 sums of
+// squares may have overflowed or vanished (rows of 1e20, of 1e-25 with eps = 0), and
+// 1 / rms may not be a normal number. Such a row's sums are done over in fp64, and it
+// goes on as s p, with p a power of two that brings it near 1, and f = 1 / (p rms); 0,
+// infinity and NaN come out as they are. (fp64 sums of every row cost the gradient of
+// 16384 x 5120 bf16 168 -> 181 us, of 65536 x 256 39 -> 47 us; so they stay at 168.5
+// and 39.)
+__device__ __forceinline__ bool fp32_range(float mean_sq) { return mean_sq > 0x1p-40f && mean_sq < 0x1p100f; }
+struct InvRms {
+  float p, f;
+};
+// 2^e as a double, |e| < 1022
+__device__ __forceinline__ double power2(int e) { return __builtin_bit_cast(double, (uint64_t)(1023 + e) << 52); }
+__device__ __forceinline__ InvRms inv_rms(double mean_sq) {
+  // mean_sq = 4^k m with m in [1, 4); p = 2^-k as far as fp32 has normal numbers
+  const int e = (int)(__builtin_bit_cast(uint64_t, mean_sq) >> 52 & 0x7ff) - 1023;
+  const int k = min(max(e >> 1, -160), 160), c = min(max(-k, -126), 127);
+  return {(float)power2(c), (float)power2(-k - c) / sqrtf((float)(mean_sq * power2(-2 * k)))};
+}
+
 // ------------------------------------------------------------------ E4M3
 // fp64 -> fp32 rounded to odd: the value cut after 24 bits, its last bit set
 // if anything was cut, so that a later rounding to few bits decides as from
@@ -208,7 +230,7 @@ __device__ __forceinline__ u32x2 e4m3x8(const float (&v)[8]) {
 // The 8-bit outputs are decided in fp64 (QUANT != 0): a code is the nearest
 // to the exact quotient, not to one with an fp32 rounding on either side of a
 // border. fp64 runs at the unpacked fp32 rate here and the kernel is bound by
-// memory. Without an 8-bit output everything is fp32.
+// memory. Without an 8-bit output everything is fp32 (see fp32_range).
 // Bound by memory where there are many rows: 8192 x 5120 bf16 with the stream's
 // update, E4M3 blocks and no bf16 output 58 us (295 MB, 5.0 TB/s; a large copy
 // reaches 5.2). Few rows wait for one row's chain of loads and two reductions:
@@ -256,10 +278,26 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
   }
   sq = block_reduce<false>(sq, lds[0], nwaves);
   A r;
-  if constexpr (QUANT)
+  if constexpr (QUANT) {
     r = 1.0 / sqrt(sq / H + (double)p.eps);
-  else
-    r = 1.0f / sqrtf(sq / H + p.eps);
+  } else {
+    const float v = sq / H + p.eps;
+    r = 1.0f / sqrtf(v);
+    if (!fp32_range(v)) {  // the same for the whole row
+      double sq2 = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sq2 += (double)s[j][u] * s[j][u];
+      __shared__ double lds2[16];
+      const InvRms ir = inv_rms(block_reduce<false>(sq2, lds2, nwaves) / H + p.eps);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s[j][u] *= ir.p;
+      r = ir.f;
+    }
+  }
 
   // s becomes s w; y = r (s w)
 #pragma unroll
@@ -361,11 +399,18 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
 // weight gradient (5.4 TB/s) and 141 us without; odd rows, 8192 x 5001 bf16, 142 us.
 // Rows over 16384 values need more registers than their threads have and spill: 512
 // x 65536 336 us (five arrays of 67 MB).
+// bf16 rows of two units are held to five waves a SIMD (96 registers), which the sums
+// over again of rare rows would take them from: 16384 x 5120 168.5 us so and 172.5
+// without, 64 x 5120 7.3 and 7.0.
+template <typename T, bool VEC, int V>
+constexpr int kBwdWaves = VEC && V == 2 && sizeof(T) == 2 ? 5 : V == 8 ? 4 : 2;
 template <typename T, bool VEC, int V, bool DW>
 __global__ __launch_bounds__(V == 8 ? 1024 : 512)
+__attribute__((amdgpu_waves_per_eu(kBwdWaves<T, VEC, V>)))
 void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
   constexpr Form F = VEC ? kVec : sizeof(T) == 2 ? kAny : kOne;
   __shared__ float lds[2][2][16];  // double buffered over rows: one barrier per row
+  __shared__ double lds2[2][2][16];
   const int nwaves = nt >> 6;
   const int per = nt == 64 ? (blockDim.x >> 6) : 1;  // rows side by side in the workgroup
   const int tid = nt == 64 ? (threadIdx.x & 63) : threadIdx.x;
@@ -418,8 +463,43 @@ void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
         gs += lds[buf][1][i];
       }
     }
-    const float r = 1.0f / sqrtf(sq / H + p.eps);
-    const float c = gs * r / H;  // mean(g n)
+    const float v = sq / H + p.eps;
+    float r = 1.0f / sqrtf(v), scale = 1.f;
+    float c = gs * r / H;  // mean(g n)
+    if (!fp32_range(v) || !(fabsf(gs) < 0x1p120f)) {  // the same for the whole row
+      // read again value by value: units would need registers that every row pays for.
+      // (All of the row's reads are behind the barrier before its first store.)
+      double sq2 = 0, gs2 = 0;
+#pragma unroll 1
+      for (int e = tid; e < H; e += nt) {
+        const double sv = load_value((const T*)p.s + off + e);
+        sq2 += sv * sv;
+        gs2 += (double)(load_value((const T*)p.dy + off + e) * p.w[e]) * sv;
+      }
+      sq2 = wave_sum(sq2);
+      gs2 = wave_sum(gs2);
+      if (nwaves > 1) {
+        if ((threadIdx.x & 63) == 0) {
+          lds2[buf][0][threadIdx.x >> 6] = sq2;
+          lds2[buf][1][threadIdx.x >> 6] = gs2;
+        }
+        __syncthreads();
+        sq2 = lds2[buf][0][0];
+        gs2 = lds2[buf][1][0];
+#pragma unroll 1
+        for (int i = 1; i < nwaves; ++i) {
+          sq2 += lds2[buf][0][i];
+          gs2 += lds2[buf][1][i];
+        }
+      }
+      const InvRms ir = inv_rms(sq2 / H + p.eps);
+      scale = ir.p;
+      r = ir.f;
+      c = (float)(gs2 * scale * r / H);
+    }
+    scale = lane_value(scale, 0);
+    r = lane_value(r, 0);
+    c = lane_value(c, 0);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       s[j].repack();
@@ -431,8 +511,8 @@ void add_rms_norm_bwd_kernel(NormBwdArgs p, int nt) {
       float a[8], b[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float n = s[j].get(u) * r, g = dy[j].get(u);
-        float ds = r * (g * w[j].get(u) - n * c);
+        const float n = s[j].get(u) * scale * r, g = dy[j].get(u);
+        float ds = r * (g * w[j].get(u) - n * c) * scale;
         ds += d[j].get(u);
         if (DW) dw[DW ? j : 0][u] += g * n;
         a[u] = p.add * ds;

@@ -398,7 +398,8 @@ typedef enum beam_quant {
  * depth-scaled residual and sandwich norm). Per row:
  *   s = keep * stream_in + add * x      (s = add * x without stream_in)
  *   y = s / sqrt(mean over hidden of s^2 + eps) * norm_weight
- * from the unrounded s, which is never read back from its stored form.
+ * from the unrounded s, which is never read back from its stored form, for
+ * rows of any finite s.
  *   x           [T, hidden], x_dtype (BEAM_F32 or BEAM_BF16).
  *   stream_in   [T, hidden], x_dtype, or NULL.
  *   norm_weight [hidden] fp32.
