@@ -314,20 +314,25 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
   }
   if constexpr (QUANT == 1) {
     // one scale per row, amax / 448; r is common to all of a row's values, so
-    // y 448 / amax|y| = (s w) 448 / amax|s w|
+    // y 448 / amax|y| = (s w) 448 / amax|s w|. An infinity or NaN among them makes
+    // the scale a NaN: no code stands for one, and the maximum passes over a NaN.
     double m = 0;
+    bool bad = false;
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const double a = fabs(s[j][u]);
         m = a > m ? a : m;
+        bad |= a != a;
       }
+    if (bad) m = INFINITY;
     m = block_reduce<true>(m, lds[1], nwaves);
     const double ym = m * r;
     const bool zero = m == 0;
     const double inv = zero ? 0.0 : 448.0 / m;
-    if (tid == 0) ((float*)p.q_scale)[row] = zero && ym == ym ? 1.0f : (float)(ym / 448.0);
+    if (tid == 0)
+      ((float*)p.q_scale)[row] = !(m < INFINITY) ? NAN : zero && ym == ym ? 1.0f : (float)(ym / 448.0);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float v[8];

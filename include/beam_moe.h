@@ -409,7 +409,8 @@ typedef enum beam_quant {
  *   q, q_scale  out with quant != BEAM_QUANT_NONE, else NULL: E4M3 codes
  *               [T, hidden] of y before its rounding to x_dtype, and
  *               BEAM_QUANT_ROW: fp32 [T], amax|y| / 448 (1 for a row of
- *               zeros), the codes nearest to y / scale;
+ *               zeros), the codes nearest to y / scale (a row with an infinity
+ *               or NaN: scale NaN);
  *               BEAM_QUANT_BLOCK (hidden a multiple of 32): E8M0 bytes
  *               [T, hidden / 32], exponent floor(log2 amax|y|) - 8 and at
  *               least -127, codes nearest to y / scale, at most 448 (a block

@@ -84,3 +84,18 @@ def test_norm_gradient_in_place_of_any_magnitude(H, dtype):
             cfg, 8, a.data_ptr(), b.data_ptr(), w.data_ptr(), None, dx.data_ptr(), None, None, None, 0,
             torch.cuda.current_stream().cuda_stream)
         assert st == gl.BEAM_OK and torch.equal(dx.nan_to_num(), ref.nan_to_num()), over
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H", [5, 64, 520, 5120])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_norm_codes_of_a_gain_that_is_not_finite(value, H, dtype):
+    """Codes with row scales: no code stands for a NaN or an infinity of y by
+    itself, so the row's scale does; of rows that a zero gain leaves alone too."""
+    x, w = _rows(4, H, DT[dtype], 38), _gain(H, 39)
+    w[H // 2] = value
+    r = gl.add_rms_norm(x, w, quant="row")
+    y = r["y"].float()
+    assert not torch.isfinite(y[:, H // 2]).any() and torch.isfinite(y[:, :H // 2]).all()
+    assert torch.isnan(r["q_scale"]).all()
+    assert torch.isnan(r["q"].float() * r["q_scale"][:, None]).all()
