@@ -741,6 +741,9 @@ def _gate_config(logits, top_k, score, n_group, topk_group, group_score, renorma
                          f"{tuple(_SCORES)} / {tuple(_GROUP_SCORES)}")
     _check(logits, "logits", logits.shape, _FLOATS, logits.device)
     _sizes("beam_moe_gate", *logits.shape, top_k, n_group, topk_group)
+    # before outputs of top_k columns are allocated; the library checks the rest
+    if not 1 <= top_k <= logits.shape[1] or n_group < 1 or topk_group < 1:
+        raise BeamMoeError(BEAM_ERR_CONFIG, "beam_moe_gate")
     return BeamMoeGateConfig(logits.shape[1], n_group, topk_group, top_k, _SCORES[score],
                              _GROUP_SCORES[group_score], int(bool(renormalise)),
                              _X_DTYPES[logits.dtype], rsf)
