@@ -99,3 +99,28 @@ def test_norm_codes_of_a_gain_that_is_not_finite(value, H, dtype):
     assert not torch.isfinite(y[:, H // 2]).any() and torch.isfinite(y[:, :H // 2]).all()
     assert torch.isnan(r["q_scale"]).all()
     assert torch.isnan(r["q"].float() * r["q_scale"][:, None]).all()
+
+
+def _steps(T, H):
+    """Additions in a row on a weight gradient: the rows of a workgroup's thread,
+    the four waves beside each other of narrow rows, a share's partials (32
+    shares) and the shares."""
+    per = 4 if H <= 512 else 1
+    groups = min(-(-T // per), 768)
+    return -(-T // (groups * per)) + (3 if per == 4 else 0) + -(-groups // 32) + 31
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(1, 1), (70, 64), (1100, 96), (3500, 72), (33, 1001), (2049, 520), (5000, 512)])
+def test_norm_weight_gradient_sums(T, H, dtype):
+    """dw within the roundings of its own sum: each addition is at most u of the
+    magnitudes' sum off, a term dy n has 48 roundings at most in n (see
+    test_gpu_norm.py) and one for the product."""
+    dy, s, w = _rows(T, H, DT[dtype], 40), _rows(T, H, DT[dtype], 41, 2.0), _gain(H, 42)
+    got = gl.add_rms_norm_backward(dy, s, w, norm_eps=1e-6)["d_norm_weight"]
+    eps = float(np.float32(1e-6))
+    n = f64(s) / np.sqrt(np.mean(f64(s) ** 2, 1, keepdims=True) + eps)
+    ref, mag = np.sum(f64(dy) * n, 0), np.sum(np.abs(f64(dy) * n), 0)
+    err = np.abs(f64(got) - ref)
+    tol = 2.0 ** -24 * (49 + _steps(T, H)) * 1.001 * mag
+    assert (err <= tol).all(), float((err / tol).max())
