@@ -203,7 +203,9 @@ __device__ __forceinline__ void for_each(F&& f) {
 // at position c ^ ((r >> 1) & 7); E2M1 64 bytes, chunk c at c ^ ((r >> 2) & 3).
 // A 16-byte read is served 16 lanes at a time, 0-3, 12-15 and 20-27 of the first
 // 32 and then the rest of them: with these keys each such group covers all 64
-// banks (c ^ (r & 7) and c ^ ((r >> 1) & 3) conflicted on every read).
+// banks (c ^ (r & 7) and c ^ ((r >> 1) & 3) conflicted on every read). Operands have no
+// conflicts by the counters; the tiles' scale dwords, 32 rows at a pitch of 16 bytes,
+// have 6 cycles each, up to 36 a wave and stage.
 template <int ROW>
 __device__ __forceinline__ int swizzle(int row) {
   return ROW == 64 ? (row >> 2) & 3 : (row >> 1) & 7;
@@ -478,11 +480,11 @@ void stream_launch(const Mx4LinearArgs& a, hipStream_t st) {
 // scales of four stages are 16 bytes of a row and are loaded together, into one of
 // two buffers, while the four stages before them are multiplied (a load per stage,
 // 4 bytes of each row, was half of all requests to L2).
-// N = K = 5120, 8192 tokens: E4M3 rows 292 us (1.5 PF/s, 2.9 of instructions), 4-bit
-// rows 121-129 us (3.3-3.5 PF/s); each round of tiles starts and ends with 9 us outside its
-// loop. Tiles of 128 fill LDS at
-// 50 GB/s per CU, which bounds them; rings of 160 KB and 8 waves a tile did not help
-// (1111 x 2560 x 5120, 4-bit rows: 17.3, 17.6 and 18.4 us).
+// N = K = 5120, 8192 tokens: E4M3 rows 292 us (1.5 PF/s, 2.9 of instructions, matrix
+// cores busy 59% of the time), 4-bit rows 121-129 us (3.3-3.5 PF/s); each round of
+// tiles starts and ends with 9 us outside its loop. Tiles of 128 with 4-bit rows fill
+// LDS at 50 GB/s per CU, which bounds them; rings of 160 KB and 8 waves a tile did not
+// help (1111 x 2560 x 5120: 17.3, 17.6 and 18.4 us).
 // Tiles that run together on one XCD (32 consecutive, dealt to the XCDs in
 // turn) cover 4 token tiles x 8 weight tiles, which share operands in its L2.
 __device__ __forceinline__ void tile_of(int b, int n_tiles, int mt, int nt, int& m, int& n) {

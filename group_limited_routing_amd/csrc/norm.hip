@@ -183,7 +183,7 @@ __device__ __forceinline__ F block_reduce(F v, F* lds, int nwaves) {
 // goes on as s p, with p a power of two that brings it near 1, and f = 1 / (p rms); 0,
 // infinity and NaN come out as they are. (fp64 sums of every row cost the gradient of
 // 16384 x 5120 bf16 168 -> 181 us, of 65536 x 256 39 -> 47 us; so they stay at 168.5
-// and 39.)
+// and 39. Rows of more than 16384 values, which spill, pay 1 to 13%.)
 __device__ __forceinline__ bool fp32_range(float mean_sq) { return mean_sq > 0x1p-40f && mean_sq < 0x1p100f; }
 struct InvRms {
   float p, f;
@@ -232,8 +232,8 @@ __device__ __forceinline__ u32x2 e4m3x8(const float (&v)[8]) {
 // border. fp64 runs at the unpacked fp32 rate here and the kernel is bound by
 // memory. Without an 8-bit output everything is fp32 (see fp32_range).
 // Bound by memory where there are many rows: 8192 x 5120 bf16 with the stream's
-// update, E4M3 blocks and no bf16 output 58 us (295 MB, 5.0 TB/s; a large copy
-// reaches 5.2). Few rows wait for one row's chain of loads and two reductions:
+// update, E4M3 blocks and no bf16 output 58-61 us on warm inputs, 66 on cold ones (295
+// MB, 4.5-5.0 TB/s; a large copy reaches 5.2; what follows is warm). Few rows wait for one row's chain of loads and two reductions:
 // 64 x 5120 with row scales and a bf16 output 5.6 us, one row 3.2 us. Narrow rows
 // with an 8-bit output are bound by fp64: 65536 x 256 45 us, 22 us without. Odd
 // rows: 8192 x 5001 83 us with row scales, 76 us without an 8-bit output.
@@ -400,10 +400,11 @@ __global__ __launch_bounds__(V == 8 ? 1024 : 512) void add_rms_norm_kernel(NormA
 // registers over all of them and writes it once (norm_dw_kernel adds the
 // partials in order: no atomics). The rows stay packed across the reduction
 // (repack), so that three of them and the partial fit in registers.
-// Bound by memory: 16384 x 5120 bf16, five arrays of 168 MB, 154 us with the
-// weight gradient (5.4 TB/s) and 141 us without; odd rows, 8192 x 5001 bf16, 142 us.
+// Bound by memory: 16384 x 5120 bf16, five arrays of 168 MB, 154-172 us with the
+// weight gradient (4.9-5.4 TB/s, one card and another) and 141-149 us without; odd
+// rows, 8192 x 5001 bf16, 142-155 us.
 // Rows over 16384 values need more registers than their threads have and spill: 512
-// x 65536 336 us (five arrays of 67 MB).
+// x 65536 373 us (five arrays of 67 MB; 343 before rare rows had sums of their own).
 // bf16 rows of two units are held to five waves a SIMD (96 registers), which the sums
 // over again of rare rows would take them from: 16384 x 5120 168.5 us so and 172.5
 // without, 64 x 5120 7.3 and 7.0.
