@@ -911,14 +911,16 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
 // later rounds, at K = 5120 (at other K taken to be in the same proportion):
 //                            E4M3 rows   4-bit rows
 //   stream, 16 x  32          60   45     45   33
-//           16 x  64          85   70     68   60
+//           16 x  64          85   70     72   60
 //           32 x  32          66   52     50   43
 //           32 x  64          95   72     72   66
-//           64 x  32         102   88     74   65
+//           64 x  32           -         70   65
 //           64 x  64         145  125    105  100
 //   tile,   64 x 128         250  200    132  103
 //          128 x 128         355  290    155  155
 //          256 x 256         950  960    345  420
+// (64 x 32 takes as many workgroups as 32 x 64 and is slower with E4M3 rows, 10.2 and
+// 9.5 a round; with 4-bit rows 33 tokens of N = 5120 take 6.2 and 6.9.)
 // Measured around the borders, N = 5120, us, the kernel taken and the next best one.
 // E4M3 rows: T = 64, 32 x 64 9.0 and 64 x 32 10.3; 128, 64 x 64 14.0 and 32 x 64 16.5;
 // 256, 32 x 64 24.7 and 64 x 64 26.4; 384, 64 x 128 27.5 and 64 x 64 28.4; 512, 128 x
@@ -938,10 +940,10 @@ Variant variant_of(int T, int N, bool mx4_rows) {
     int bm, bn;
     Cost e4m3, mx4;
   } const all[] = {{Variant::kStream16, 16, 32, {60, 45}, {45, 33}},
-                   {Variant::kStream16Wide, 16, 64, {85, 70}, {68, 60}},
+                   {Variant::kStream16Wide, 16, 64, {85, 70}, {72, 60}},
                    {Variant::kStream32, 32, 32, {66, 52}, {50, 43}},
                    {Variant::kStream32Wide, 32, 64, {95, 72}, {72, 66}},
-                   {Variant::kStream64, 64, 32, {102, 88}, {74, 65}},
+                   {Variant::kStream64, 64, 32, {0, 0}, {70, 65}},
                    {Variant::kStream64Wide, 64, 64, {145, 125}, {105, 100}},
                    {Variant::kTile64, 64, 128, {250, 200}, {132, 103}},
                    {Variant::kTile128, 128, 128, {355, 290}, {155, 155}},
@@ -951,6 +953,7 @@ Variant variant_of(int T, int N, bool mx4_rows) {
   for (const auto& c : all) {
     const int64_t wgs = (int64_t)((T + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     const Cost& us = mx4_rows ? c.mx4 : c.e4m3;
+    if (us.first == 0) continue;  // not for this format
     const int64_t cost = us.first + ((wgs + 255) / 256 - 1) * us.later;
     if (cost < least) {
       least = cost;
@@ -968,7 +971,9 @@ hipError_t launch_mx4_linear(const Mx4LinearArgs& a, int x_mode, hipStream_t st)
       case Variant::kStream16Wide: stream_launch<XMODE, 16, 2>(a, st); break;
       case Variant::kStream32: stream_launch<XMODE, 32, 1>(a, st); break;
       case Variant::kStream32Wide: stream_launch<XMODE, 32, 2>(a, st); break;
-      case Variant::kStream64: stream_launch<XMODE, 64, 1>(a, st); break;
+      case Variant::kStream64:
+        if constexpr (XMODE == 2) stream_launch<XMODE, 64, 1>(a, st);
+        break;
       case Variant::kStream64Wide: stream_launch<XMODE, 64, 2>(a, st); break;
       case Variant::kTile64: tile_launch<XMODE, 2, 1, 1, 4>(a, st); break;
       case Variant::kTile128: tile_launch<XMODE, 2, 2, 2, 2>(a, st); break;

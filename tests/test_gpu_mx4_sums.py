@@ -13,14 +13,16 @@ import pytest
 import torch
 
 import group_limited_routing_amd as gl
+import test_gpu_mx4 as product
 
 pytestmark = pytest.mark.gpu
 
 U = 2.0 ** -24
 UNIT = 2.0 ** -10
-# every kernel of the product: streams of 16, 32 and 64 tokens, both widths, and the three tiles
-SIZES = [(5, 70), (5, 16000), (20, 321), (30, 16000), (50, 700), (60, 16001), (100, 1000),
-         (250, 5121), (500, 5100), (2020, 5115)]
+# every kernel of the product with E4M3 rows: streams of 16, 32 and 64 tokens, 32 and 64
+# columns wide, and the tiles of 64, 128 and 256
+STREAMS = [(5, 70), (5, 16000), (20, 5100), (30, 16000), (50, 700), (60, 16001), (250, 5121)]
+TILES = [(384, 5121), (500, 5100), (2020, 5115), (2900, 5100)]
 
 
 def _dev():
@@ -44,8 +46,8 @@ def _any_e4m3(shape, seed):
 
 
 @pytest.mark.parametrize("fmt", ["row", "block"])
-@pytest.mark.parametrize("K", [32, 160, 512, 1120])
-@pytest.mark.parametrize("T,N", SIZES)
+@pytest.mark.parametrize("T,N,K", [(T, N, K) for T, N in STREAMS for K in (32, 160, 512, 1120)] +
+                         [(T, N, K) for T, N in TILES for K in (32, 96, 160, 384, 416, 448, 512, 544, 672, 1120)])
 def test_linear_sums_are_exact(T, N, K, fmt):
     dev = _dev()
     x = _any_e4m3((T, K), 1).float()
@@ -96,3 +98,13 @@ def test_linear_sums_in_general(T, N, K, fmt):
         # roundings of either sign: in the norm as if a few were left of each root of 2 K / 8
         if out == torch.float32:
             assert float(err.norm() / ref.norm()) <= 2 * U * adds ** 0.5
+
+
+@pytest.mark.parametrize("fmt", ["row", "block"])
+@pytest.mark.parametrize("T,N", TILES[::3])
+def test_linear_tiles_keep_to_their_rows(T, N, fmt):
+    """The tiles of 64 and 256 with E4M3 rows: a NaN scale at a row's start is its
+    own row's alone, and not a byte around the output changes."""
+    for K in (160, 416, 544, 608):
+        product.test_linear_scales_behind_a_row_stay_out(T, N, K, fmt)
+    product.test_linear_writes_its_rows_only(T, N, fmt)
