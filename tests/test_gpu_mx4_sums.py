@@ -95,7 +95,8 @@ def test_linear_sums_in_general(T, N, K, fmt):
     for out, half in ((torch.float32, U), (torch.bfloat16, 2.0 ** -8)):
         err = (gl.mx4_linear(x, xs, w, ws, out_dtype=out).double() - ref).abs()
         assert bool((err <= half * ref.abs() + adds * 2 * U * mag).all())
-        # roundings of either sign: in the norm as if a few were left of each root of 2 K / 8
+        # independent roundings of partial sums, which in the norm are no larger than the
+        # whole: they add up as the root of their number
         if out == torch.float32:
             assert float(err.norm() / ref.norm()) <= 2 * U * adds ** 0.5
 

@@ -91,7 +91,7 @@ def test_norm_gradient_in_place_of_any_magnitude(H, dtype):
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
 def test_norm_codes_of_a_gain_that_is_not_finite(value, H, dtype):
     """Codes with row scales: no code stands for a NaN or an infinity of y by
-    itself, so the row's scale does; of rows that a zero gain leaves alone too."""
+    itself, so the row's scale does."""
     x, w = _rows(4, H, DT[dtype], 38), _gain(H, 39)
     w[H // 2] = value
     r = gl.add_rms_norm(x, w, quant="row")
