@@ -34,6 +34,7 @@ BEAM_QUANT_NONE, BEAM_QUANT_ROW, BEAM_QUANT_BLOCK = 0, 1, 2
 BEAM_SCORE_SIGMOID, BEAM_SCORE_SOFTMAX = 0, 1
 BEAM_GROUP_TOP2, BEAM_GROUP_MAX = 0, 1
 BEAM_X_E4M3_ROW, BEAM_X_E4M3_BLOCK, BEAM_X_MXFP4 = 0, 1, 2
+BEAM_ACT_SILU, BEAM_ACT_GELU = 0, 1
 
 EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route", "beam_moe_forward",
             "beam_moe_forward_residual", "beam_moe_status_string", "beam_moe_profile_begin",
@@ -42,7 +43,11 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route", "beam_moe_forward",
             "beam_moe_forward_shard", "beam_moe_forward_noalloc", "beam_moe_add_rms_norm",
             "beam_moe_add_rms_norm_backward_workspace_bytes", "beam_moe_add_rms_norm_backward",
             "beam_moe_gate", "beam_moe_gate_backward", "beam_moe_mx4_quantize",
-            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear")
+            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear", "beam_moe_gated_linear",
+            "beam_moe_gated_linear_backward_workspace_bytes", "beam_moe_gated_linear_backward",
+            "beam_moe_lora_plan_bytes", "beam_moe_lora_plan", "beam_moe_lora_workspace_bytes",
+            "beam_moe_lora", "beam_moe_lora_backward_workspace_bytes", "beam_moe_lora_backward",
+            "beam_moe_dropout", "beam_moe_dropout_backward")
 
 # Scratch size of beam_moe_forward_noalloc (BEAM_MOE_NOALLOC_MAX_BYTES in the header)
 NOALLOC_MAX_BYTES = 64 << 20
@@ -120,6 +125,34 @@ class BeamMoeLinear(ctypes.Structure):
     ]
 
 
+class BeamMoeGated(ctypes.Structure):
+    _fields_ = [
+        ("hidden", ctypes.c_int32),
+        ("intermediate", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class BeamMoeLoraConfig(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_int32),
+        ("n", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
+        ("n_adapters", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class BeamMoeDropoutConfig(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_float),
+        ("keep", ctypes.c_float),
+        ("add", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 class BeamMoeError(RuntimeError):
     def __init__(self, status, where):
         self.status = status
@@ -186,8 +219,29 @@ def lib():
         L.beam_moe_mx4_quantize.argtypes = [vp, i64, i32, i32, i32, vp, vp, vp]
         L.beam_moe_mx4_dequantize.argtypes = [vp, vp, i64, i32, i32, vp, vp]
         L.beam_moe_mx4_linear.argtypes = [linp, i32, vp, vp, vp, vp, vp, vp]
+        gatedp, lorap = ctypes.POINTER(BeamMoeGated), ctypes.POINTER(BeamMoeLoraConfig)
+        dropp, u64 = ctypes.POINTER(BeamMoeDropoutConfig), ctypes.c_uint64
+        L.beam_moe_gated_linear.argtypes = [gatedp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.beam_moe_gated_linear_backward_workspace_bytes.argtypes = [gatedp, i32]
+        L.beam_moe_gated_linear_backward_workspace_bytes.restype = sz
+        L.beam_moe_gated_linear_backward.argtypes = [gatedp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
+                                                     vp, vp, vp, vp, sz, vp]
+        L.beam_moe_lora_plan_bytes.argtypes = [i32, i32]
+        L.beam_moe_lora_plan_bytes.restype = sz
+        L.beam_moe_lora_plan.argtypes = [vp, i32, i32, vp, sz, vp]
+        L.beam_moe_lora_workspace_bytes.argtypes = [lorap, i32]
+        L.beam_moe_lora_workspace_bytes.restype = sz
+        L.beam_moe_lora.argtypes = [lorap, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.beam_moe_lora_backward_workspace_bytes.argtypes = [lorap, i32]
+        L.beam_moe_lora_backward_workspace_bytes.restype = sz
+        L.beam_moe_lora_backward.argtypes = [lorap, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                             vp, sz, vp]
+        L.beam_moe_dropout.argtypes = [dropp, i64, vp, vp, u64, u64, vp, vp, vp]
+        L.beam_moe_dropout_backward.argtypes = [dropp, i64, vp, u64, u64, vp, vp, vp, vp]
         for name in ("add_rms_norm", "add_rms_norm_backward", "gate", "gate_backward",
-                     "mx4_quantize", "mx4_dequantize", "mx4_linear"):
+                     "mx4_quantize", "mx4_dequantize", "mx4_linear", "gated_linear",
+                     "gated_linear_backward", "lora_plan", "lora", "lora_backward", "dropout",
+                     "dropout_backward"):
             getattr(L, "beam_moe_" + name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -830,6 +884,248 @@ def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, st
     return out
 
 
+def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=None,
+                 return_pre=False, stream=None):
+    """The gated product of a dense MLP in one kernel: gate = x w_gate^T + add_gate,
+    up = x w_up^T + add_up, h = act(gate) * up, act "silu" or "gelu" (g Phi(g)).
+
+    x [T, H], w_gate and w_up [F, H], add_gate and add_up [T, F] (an adapter's share,
+    as from lora(); may be None), all bf16, H and F multiples of 8. Returns dict(h:
+    [T, F] bf16, gate, up: [T, F] bf16 for gated_linear_backward(), None without
+    ``return_pre``)."""
+    T, H = x.shape
+    F = w_gate.shape[0]
+    dev = x.device
+    cfg = _gated_config(x, w_gate, w_up, activation, dev)
+    for t, name in ((add_gate, "add_gate"), (add_up, "add_up")):
+        if t is not None:
+            _check(t, name, (T, F), _BF16, dev)
+    gate = up = None
+    with _on(dev, stream):
+        h = torch.empty(T, F, dtype=torch.bfloat16, device=dev)
+        if return_pre:
+            gate, up = torch.empty_like(h), torch.empty_like(h)
+        _launch("beam_moe_gated_linear", dev, lib().beam_moe_gated_linear, ctypes.byref(cfg), T,
+                _p(x), _p(w_gate), _p(w_up), _p(add_gate), _p(add_up), _p(h), _p(gate), _p(up))
+    return {"h": h, "gate": gate, "up": up}
+
+
+def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", input_grad=True,
+                          weight_grad=True, workspace=None, stream=None):
+    """Gradients of gated_linear() from its stored ``gate`` and ``up`` and the gradient
+    ``dh`` of h. Returns dict(d_gate, d_up: [T, F] bf16, also the gradients of add_gate
+    and add_up; dx: [T, H] bf16, None without ``input_grad``; d_w_gate, d_w_up: [F, H]
+    bf16, None without ``weight_grad``)."""
+    T, H = x.shape
+    F = w_gate.shape[0]
+    dev = x.device
+    cfg = _gated_config(x, w_gate, w_up, activation, dev)
+    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
+        _check(t, name, (T, F), _BF16, dev)
+    dx = dwg = dwu = None
+    with _on(dev, stream):
+        dg, du = torch.empty_like(dh), torch.empty_like(dh)
+        need = 0
+        if input_grad:
+            dx = torch.empty_like(x)
+            need = int(lib().beam_moe_gated_linear_backward_workspace_bytes(ctypes.byref(cfg), T))
+        if weight_grad:  # no rows: the sums over them are 0
+            dwg, dwu = ((torch.empty_like if T else torch.zeros_like)(w) for w in (w_gate, w_up))
+        workspace = _scratch(workspace, need, dev) if need else None
+        _launch("beam_moe_gated_linear_backward", dev, lib().beam_moe_gated_linear_backward,
+                ctypes.byref(cfg), T, _p(dh), _p(x), _p(w_gate), _p(w_up), _p(gate), _p(up), _p(dg),
+                _p(du), _p(dx), _p(dwg), _p(dwu), _p(workspace),
+                0 if workspace is None else workspace.numel())
+    return {"dx": dx, "d_w_gate": dwg, "d_w_up": dwu, "d_gate": dg, "d_up": du}
+
+
+def _gated_config(x, w_gate, w_up, activation, dev):
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation is {activation!r}, expected one of {tuple(_ACTIVATIONS)}")
+    T, H = x.shape
+    F = w_gate.shape[0]
+    _check(x, "x", (T, H), _BF16, dev)
+    _check(w_gate, "w_gate", (F, H), _BF16, dev)
+    _check(w_up, "w_up", (F, H), _BF16, dev)
+    _sizes("beam_moe_gated_linear", T, H, F)
+    # before outputs of F columns are allocated; the library checks the rest
+    if H % 8 or F % 8:
+        raise BeamMoeError(BEAM_ERR_SHAPE, "beam_moe_gated_linear")
+    return BeamMoeGated(H, F, _ACTIVATIONS[activation], BEAM_BF16)
+
+
+class LoraPlan:
+    """Which tokens of a batch use which adapter, grouped on the GPU: lora_plan()
+    makes it, lora() and lora_backward() of that batch take it. ``index`` and the
+    number of tokens and adapters stay as they were when it was made."""
+
+    __slots__ = ("buffer", "tokens", "n_adapters")
+
+    def __init__(self, buffer, tokens, n_adapters):
+        self.buffer, self.tokens, self.n_adapters = buffer, tokens, n_adapters
+
+
+def lora_plan(index, n_adapters, *, stream=None):
+    """The plan of a batch whose token t uses adapter index[t] ([T] int32; a token
+    with an index outside [0, n_adapters) uses none), for every product of the batch.
+    In a captured graph a replay groups the tokens anew, from what index then holds."""
+    T, = index.shape
+    dev = index.device
+    _check(index, "index", (T,), (torch.int32,), dev)
+    _sizes("beam_moe_lora_plan", T, n_adapters)
+    if n_adapters < 1:
+        raise BeamMoeError(BEAM_ERR_CONFIG, "beam_moe_lora_plan")
+    need = int(lib().beam_moe_lora_plan_bytes(T, n_adapters))
+    with _on(dev, stream):
+        buffer = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        _launch("beam_moe_lora_plan", dev, lib().beam_moe_lora_plan, _p(index), T, n_adapters,
+                _p(buffer), buffer.numel())
+    return LoraPlan(buffer, T, n_adapters)
+
+
+def lora(x, a, b, plan, *, scale=None, base=None, out=None, return_v=False, workspace=None,
+         stream=None):
+    """Low-rank adapters of many requests beside a projection that they share: for a
+    token with adapter i (see lora_plan()) v = a[i] x, out = base + scale[i] b[i] v;
+    without one out = base, v = 0.
+
+    x [T, K], a [E, R, K], b [E, N, R] bf16, R (8 to 128), K and N multiples of 8;
+    scale [E] fp32 (None: 1); base [T, N] bf16, such as mx4_linear()'s result (None:
+    0); ``out`` may be given, also base itself. Returns dict(out: [T, N] bf16, v: [T, R]
+    fp32 for lora_backward(), None without ``return_v``)."""
+    T, K = x.shape
+    dev = x.device
+    cfg = _lora_config("beam_moe_lora", x, a, b, plan, scale, dev)
+    N, R = cfg.n, cfg.rank
+    for t, name in ((base, "base"), (out, "out")):
+        if t is not None:
+            _check(t, name, (T, N), _BF16, dev)
+    v = None
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(T, N, dtype=torch.bfloat16, device=dev)
+        if return_v:
+            v = torch.empty(T, R, dtype=torch.float32, device=dev)
+        workspace = _scratch(workspace, int(lib().beam_moe_lora_workspace_bytes(ctypes.byref(cfg), T)),
+                             dev)
+        _launch("beam_moe_lora", dev, lib().beam_moe_lora, ctypes.byref(cfg), T, _p(x), _p(a), _p(b),
+                _p(scale), _p(plan.buffer), _p(base), _p(out), _p(v), _p(workspace),
+                workspace.numel())
+    return {"out": out, "v": v}
+
+
+def lora_backward(dy, x, v, a, b, plan, *, scale=None, base=None, dx=None, input_grad=True,
+                  weight_grad=True, workspace=None, stream=None):
+    """Gradients of lora() from its stored ``v`` and the gradient ``dy`` of out (which
+    is also base's): dv = scale[i] b[i]^T dy, dx = base + a[i]^T dv (base [T, K] bf16: the
+    gradient that reaches x through the shared projection, None: 0; ``dx`` may be
+    given, also base itself), d_a[i] and d_b[i] summed over the tokens of adapter i.
+    Returns dict(dx: [T, K] bf16, None without ``input_grad``; d_a, d_b: bf16, shapes
+    of a and b, None without ``weight_grad``)."""
+    T, K = x.shape
+    dev = x.device
+    cfg = _lora_config("beam_moe_lora_backward", x, a, b, plan, scale, dev)
+    _check(dy, "dy", (T, cfg.n), _BF16, dev)
+    if weight_grad:
+        _check(v, "v", (T, cfg.rank), _F32, dev)
+    for t, name in ((base, "base"), (dx, "dx")):
+        if t is not None:
+            _check(t, name, (T, K), _BF16, dev)
+    da = db = None
+    with _on(dev, stream):
+        if not input_grad:
+            dx = None
+        elif dx is None:
+            dx = torch.empty_like(x)
+        if weight_grad:  # no rows: the sums over them are 0
+            da, db = ((torch.empty_like if T else torch.zeros_like)(w) for w in (a, b))
+        workspace = _scratch(
+            workspace, int(lib().beam_moe_lora_backward_workspace_bytes(ctypes.byref(cfg), T)), dev)
+        if input_grad or weight_grad:
+            _launch("beam_moe_lora_backward", dev, lib().beam_moe_lora_backward, ctypes.byref(cfg), T,
+                    _p(dy), _p(x), _p(v) if weight_grad else None, _p(a), _p(b), _p(scale),
+                    _p(plan.buffer), _p(base), _p(dx), _p(da), _p(db), _p(workspace),
+                    workspace.numel())
+    return {"dx": dx, "d_a": da, "d_b": db}
+
+
+def _lora_config(where, x, a, b, plan, scale, dev):
+    T, K = x.shape
+    E, R = a.shape[:2]
+    N = b.shape[1]
+    _check(x, "x", (T, K), _BF16, dev)
+    _check(a, "a", (E, R, K), _BF16, dev)
+    _check(b, "b", (E, N, R), _BF16, dev)
+    if scale is not None:
+        _check(scale, "scale", (E,), _F32, dev)
+    if (plan.tokens, plan.n_adapters) != (T, E):
+        raise ValueError(f"plan is for {plan.tokens} tokens and {plan.n_adapters} adapters, "
+                         f"expected {T} and {E}")
+    if plan.buffer.device != dev:
+        raise ValueError(f"plan is on {plan.buffer.device}, expected {dev}")
+    _sizes(where, T, K, N, R, E)
+    # before outputs are allocated; the library checks the rest
+    if not 8 <= R <= 128 or R % 8 or E < 1:
+        raise BeamMoeError(BEAM_ERR_CONFIG, where)
+    if K < 8 or K % 8 or N < 8 or N % 8:
+        raise BeamMoeError(BEAM_ERR_SHAPE, where)
+    return BeamMoeLoraConfig(K, N, R, E, BEAM_BF16)
+
+
+def dropout(x, p, *, seed, offset=0, stream_in=None, keep=1.0, add=1.0, out=None, stream=None):
+    """Dropout with a mask that is never stored, and the stream's update with it: out =
+    keep * stream_in + add * D(x) (add * D(x) without ``stream_in``), where D(x) is 0
+    with probability p and x / (1 - p) else (p rounded to a multiple of 1 / 65536).
+
+    x, stream_in [...] bf16 or fp32. The mask depends on ``seed`` (64 bits), ``offset``
+    and the element's place in x alone (Philox4x32-10, see beam_moe.h); ``offset`` is
+    an integer of 64 bits, or a GPU tensor of one int64 that the kernel reads, so that
+    replays of a graph can draw new masks. Another ``offset`` is another mask. ``out``
+    may be given, also x or stream_in itself. Returns out."""
+    dev = x.device
+    cfg, offset, at = _dropout_config(x, "x", p, seed, offset, keep, add)
+    for t, name in ((stream_in, "stream_in"), (out, "out")):
+        if t is not None:
+            _check(t, name, x.shape, (x.dtype,), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        _launch("beam_moe_dropout", dev, lib().beam_moe_dropout, ctypes.byref(cfg), x.numel(), _p(x),
+                _p(stream_in), seed, offset, _p(at), _p(out))
+    return out
+
+
+def dropout_backward(dy, p, *, seed, offset=0, keep=1.0, add=1.0, stream_grad=False, stream=None):
+    """Gradients of dropout() with the same p, seed, offset, keep and add. Returns
+    dict(dx: add * D(dy), d_stream_in: keep * dy with ``stream_grad`` (dy itself where
+    keep == 1), else None)."""
+    dev = dy.device
+    cfg, offset, at = _dropout_config(dy, "dy", p, seed, offset, keep, add)
+    d_in = None
+    with _on(dev, stream):
+        dx = torch.empty_like(dy)
+        if stream_grad and keep != 1.0:
+            d_in = torch.empty_like(dy)
+        _launch("beam_moe_dropout_backward", dev, lib().beam_moe_dropout_backward, ctypes.byref(cfg),
+                dy.numel(), _p(dy), seed, offset, _p(at), _p(dx), _p(d_in))
+    return {"dx": dx, "d_stream_in": dy if stream_grad and d_in is None else d_in}
+
+
+def _dropout_config(x, name, p, seed, offset, keep, add):
+    """The configuration, the offset as a number, and as a tensor or None."""
+    _check(x, name, x.shape, _FLOATS, x.device)
+    at = None
+    if torch.is_tensor(offset):
+        offset, at = 0, offset
+        if at.numel() != 1:
+            raise ValueError(f"offset has {at.numel()} elements, expected one")
+        _check(at, "offset", at.shape, (torch.int64,), x.device)
+    for n, what in ((seed, "seed"), (offset, "offset")):
+        if not 0 <= n < 1 << 64:
+            raise ValueError(f"{what} is {n}, expected 64 bits without a sign")
+    return BeamMoeDropoutConfig(p, keep, add, _X_DTYPES[x.dtype]), offset, at
+
+
 def _scratch(workspace, need, device):
     """The caller's workspace if it is large enough, else a new one."""
     if workspace is None or workspace.numel() < need:
@@ -839,6 +1135,8 @@ def _scratch(workspace, need, device):
 
 
 _FLOATS, _F32, _U8 = tuple(_X_DTYPES), (torch.float32,), (torch.uint8,)
+_BF16 = (torch.bfloat16,)
+_ACTIVATIONS = {"silu": BEAM_ACT_SILU, "gelu": BEAM_ACT_GELU}
 _QUANTS = {None: BEAM_QUANT_NONE, "row": BEAM_QUANT_ROW, "block": BEAM_QUANT_BLOCK}
 _SCORES = {"sigmoid": BEAM_SCORE_SIGMOID, "softmax": BEAM_SCORE_SOFTMAX}
 _GROUP_SCORES = {"top2": BEAM_GROUP_TOP2, "max": BEAM_GROUP_MAX}

@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libbeam_moe.so")
 SOURCES = ["beam_moe.hip", "router.hip", "permute.hip", "expert_gemm.hip", "backward.hip",
-           "operators.hip", "norm.hip", "gate.hip", "mx4.hip"]
+           "operators.hip", "norm.hip", "gate.hip", "mx4.hip", "mlp.hip", "lora.hip",
+           "dropout.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

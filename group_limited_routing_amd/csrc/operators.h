@@ -1,5 +1,6 @@
 // Launchers of the operators around the MoE block: RMS norm with the
-// residual's addition, routing of given logits, MXFP4 quantisation and product.
+// residual's addition, routing of given logits, MXFP4 quantisation and product,
+// and the dense MLP's gated product, its adapters and dropout.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -88,5 +89,111 @@ struct Mx4LinearArgs {
 };
 // x_mode: 0 E4M3 with row scales, 1 E4M3 with block scales, 2 MXFP4
 hipError_t launch_mx4_linear(const Mx4LinearArgs& a, int x_mode, hipStream_t st);
+
+// ---------------------------------------------------------------- mlp.hip
+constexpr int kMlpMaxH = 65536;    // hidden
+constexpr int kMlpMaxF = 262144;   // intermediate
+
+struct GatedArgs {
+  const uint16_t* x;         // [T, H] bf16
+  const uint16_t* wg;        // [F, H]
+  const uint16_t* wu;        // [F, H]
+  const uint16_t* add_gate;  // [T, F] or null
+  const uint16_t* add_up;    // [T, F] or null
+  uint16_t* h;               // [T, F]
+  uint16_t* gate;            // [T, F] or null
+  uint16_t* up;              // [T, F] or null
+  int T, H, F;
+};
+// gelu: the activation is gelu (else silu)
+hipError_t launch_gated_linear(const GatedArgs& a, int gelu, hipStream_t st);
+
+struct GatedBwdArgs {
+  const uint16_t* dh;    // [T, F] bf16
+  const uint16_t* x;     // [T, H]
+  const uint16_t* wg;    // [F, H]
+  const uint16_t* wu;    // [F, H]
+  const uint16_t* gate;  // [T, F]
+  const uint16_t* up;    // [T, F]
+  uint16_t* d_gate;      // [T, F]
+  uint16_t* d_up;        // [T, F]
+  uint16_t* dx;          // [T, H] or null
+  uint16_t* d_wg;        // [F, H] or null (both or none)
+  uint16_t* d_wu;        // [F, H]
+  float* part;           // workspace: partial sums of dx
+  int T, H, F;
+};
+size_t gated_bwd_workspace_bytes(int T, int H, int F);
+hipError_t launch_gated_linear_backward(const GatedBwdArgs& a, int gelu, hipStream_t st);
+
+// ---------------------------------------------------------------- lora.hip
+constexpr int kLoraMaxR = 128;
+constexpr int kLoraMaxE = 1024;
+
+// A plan: int32 words. The tokens in order of their adapter, those without one
+// last (stable), cut into tiles of one adapter's tokens and, for the gradients
+// of the adapters, into longer chunks.
+constexpr int kLoraTile = 64, kLoraChunk = 512;
+struct LoraPlanLayout {
+  int tiles, chunks;  // at most
+  size_t o_order, o_tiles, o_chunks, o_first, words;
+  __host__ __device__ LoraPlanLayout(int T, int E) {
+    tiles = T / kLoraTile + (E + 1 < T ? E + 1 : T);
+    chunks = T / kLoraChunk + (E < T ? E : T);
+    o_order = 16;                       // [0] tiles, [1] chunks
+    o_tiles = o_order + (((size_t)T + 3) & ~(size_t)3);  // {adapter or -1, first, count, 0}
+    o_chunks = o_tiles + 4 * (size_t)tiles;
+    o_first = o_chunks + 4 * (size_t)chunks;             // [E + 1] first chunk of an adapter
+    words = o_first + (((size_t)E + 1 + 3) & ~(size_t)3);
+  }
+};
+hipError_t launch_lora_plan(const int32_t* index, int T, int E, int32_t* plan, hipStream_t st);
+
+struct LoraArgs {
+  const uint16_t* x;     // [T, K] bf16
+  const uint16_t* a;     // [E, R, K]
+  const uint16_t* b;     // [E, N, R]
+  const float* scale;    // [E] or null
+  const int32_t* plan;
+  const uint16_t* base;  // [T, N] or null
+  uint16_t* out;         // [T, N]
+  float* v;              // [T, R] or null
+  float* part;           // workspace
+  int T, K, N, R, E;
+};
+size_t lora_workspace_bytes(int T, int K, int N, int R, int E);
+hipError_t launch_lora(const LoraArgs& a, hipStream_t st);
+
+struct LoraBwdArgs {
+  const uint16_t* dy;    // [T, N] bf16
+  const uint16_t* x;     // [T, K]
+  const float* v;        // [T, R]
+  const uint16_t* a;     // [E, R, K]
+  const uint16_t* b;     // [E, N, R]
+  const float* scale;    // [E] or null
+  const int32_t* plan;
+  const uint16_t* base;  // [T, K] or null
+  uint16_t* dx;          // [T, K] or null
+  uint16_t* da;          // [E, R, K] or null (both or none)
+  uint16_t* db;          // [E, N, R]
+  void* workspace;
+  int T, K, N, R, E;
+};
+size_t lora_bwd_workspace_bytes(int T, int K, int N, int R, int E);
+hipError_t launch_lora_backward(const LoraBwdArgs& a, hipStream_t st);
+
+// ---------------------------------------------------------------- dropout.hip
+struct DropoutArgs {
+  const void* x;              // [n]
+  const void* stream_in;      // [n] or null
+  void* out;                  // [n]
+  void* kept_grad;            // [n] or null: keep * x
+  const int64_t* offset_dev;  // [1] or null, added to offset
+  uint64_t seed, offset;
+  int64_t n;
+  uint32_t border;            // of 65536: elements whose 16 random bits are below it are 0
+  float scale, keep, add;     // scale = 1 / (1 - border / 65536)
+};
+hipError_t launch_dropout(const DropoutArgs& a, int f32, hipStream_t st);
 
 }  // namespace beam

@@ -1,4 +1,5 @@
-// C ABI of the operators around the MoE block: argument checks and launches.
+// C ABI of the operators around the MoE block and of the dense MLP: argument checks
+// and launches.
 // See include/beam_moe.h for the contract.
 #include "operators.h"
 
@@ -58,6 +59,54 @@ beam_status check_linear(const beam_moe_linear* c, int32_t T) {
       T > kMaxT)
     return BEAM_ERR_SHAPE;
   return BEAM_OK;
+}
+
+beam_status check_gated(const beam_moe_gated* c, int32_t T) {
+  if (!c) return BEAM_ERR_NULL;
+  if (c->activation != BEAM_ACT_SILU && c->activation != BEAM_ACT_GELU) return BEAM_ERR_CONFIG;
+  if (c->dtype != BEAM_BF16) return BEAM_ERR_DTYPE;
+  if (c->hidden < 8 || c->hidden > kMlpMaxH || c->hidden % 8 != 0 || c->intermediate < 8 ||
+      c->intermediate > kMlpMaxF || c->intermediate % 8 != 0 || T < 0 || T > kMaxT)
+    return BEAM_ERR_SHAPE;
+  return BEAM_OK;
+}
+
+beam_status check_lora_plan(int32_t T, int32_t n_adapters) {
+  if (n_adapters < 1 || n_adapters > kLoraMaxE) return BEAM_ERR_CONFIG;
+  return T < 0 || T > kMaxT ? BEAM_ERR_SHAPE : BEAM_OK;
+}
+
+beam_status check_lora(const beam_moe_lora_config* c, int32_t T) {
+  if (!c) return BEAM_ERR_NULL;
+  if (c->rank < 8 || c->rank > kLoraMaxR || c->rank % 8 != 0) return BEAM_ERR_CONFIG;
+  if (c->dtype != BEAM_BF16) return BEAM_ERR_DTYPE;
+  if (c->k < 8 || c->k > 65536 || c->k % 8 != 0 || c->n < 8 || c->n > kMlpMaxF || c->n % 8 != 0)
+    return BEAM_ERR_SHAPE;
+  return check_lora_plan(T, c->n_adapters);
+}
+
+// Elements dropped of 65536, or a status
+beam_status check_dropout(const beam_moe_dropout_config* c, int64_t n) {
+  if (!c) return BEAM_ERR_NULL;
+  if (!(c->p >= 0.f && c->p <= 1.f) || !isfinite(c->keep) || !isfinite(c->add)) return BEAM_ERR_CONFIG;
+  if (!float_dtype(c->dtype)) return BEAM_ERR_DTYPE;
+  return n < 0 || n > (1LL << 40) ? BEAM_ERR_SHAPE : BEAM_OK;
+}
+
+DropoutArgs dropout_args(const beam_moe_dropout_config* c, int64_t n, const void* x, uint64_t seed,
+                         uint64_t offset, const int64_t* offset_dev) {
+  DropoutArgs a{};
+  a.x = x;
+  a.n = n;
+  a.seed = seed;
+  a.offset = offset;
+  a.offset_dev = offset_dev;
+  a.border = (uint32_t)floor((double)c->p * 65536.0 + 0.5);
+  // border 65536 keeps nothing
+  a.scale = a.border < 65536 ? (float)(65536.0 / (65536.0 - a.border)) : 0.f;
+  a.keep = c->keep;
+  a.add = c->add;
+  return a;
 }
 
 }  // namespace
@@ -196,6 +245,138 @@ beam_status beam_moe_mx4_linear(const beam_moe_linear* cfg, int32_t T, const voi
   const Mx4LinearArgs a{(const uint8_t*)x, x_scale, (const uint8_t*)w, (const uint8_t*)w_scale,
                         out, T, cfg->n, cfg->k, cfg->out_dtype == BEAM_F32};
   return launched(launch_mx4_linear(a, cfg->x_format, (hipStream_t)stream));
+}
+
+beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const void* x,
+                                  const void* w_gate, const void* w_up, const void* add_gate,
+                                  const void* add_up, void* h, void* gate, void* up, void* stream) {
+  const beam_status cs = check_gated(cfg, T);
+  if (cs != BEAM_OK) return cs;
+  if (T == 0) return BEAM_OK;
+  if (!x || !w_gate || !w_up || !h) return BEAM_ERR_NULL;
+  if (any_misaligned(x, w_gate, w_up, add_gate, add_up, h, gate, up)) return BEAM_ERR_ALIGN;
+  const GatedArgs a{(const uint16_t*)x,        (const uint16_t*)w_gate, (const uint16_t*)w_up,
+                    (const uint16_t*)add_gate, (const uint16_t*)add_up, (uint16_t*)h,
+                    (uint16_t*)gate,           (uint16_t*)up,           T,
+                    cfg->hidden,               cfg->intermediate};
+  return launched(launch_gated_linear(a, cfg->activation == BEAM_ACT_GELU, (hipStream_t)stream));
+}
+
+size_t beam_moe_gated_linear_backward_workspace_bytes(const beam_moe_gated* cfg, int32_t T) {
+  if (check_gated(cfg, T) != BEAM_OK || T == 0) return 0;
+  return gated_bwd_workspace_bytes(T, cfg->hidden, cfg->intermediate);
+}
+
+beam_status beam_moe_gated_linear_backward(const beam_moe_gated* cfg, int32_t T, const void* dh,
+                                           const void* x, const void* w_gate, const void* w_up,
+                                           const void* gate, const void* up, void* d_gate, void* d_up,
+                                           void* dx, void* d_w_gate, void* d_w_up, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  const beam_status cs = check_gated(cfg, T);
+  if (cs != BEAM_OK) return cs;
+  if (T == 0) return BEAM_OK;
+  if (!dh || !gate || !up || !d_gate || !d_up) return BEAM_ERR_NULL;
+  if (dx && (!w_gate || !w_up)) return BEAM_ERR_NULL;
+  if (!d_w_gate != !d_w_up || (d_w_gate && !x)) return BEAM_ERR_NULL;
+  const size_t need = dx ? beam_moe_gated_linear_backward_workspace_bytes(cfg, T) : 0;
+  if (need && (!workspace || workspace_bytes < need)) return BEAM_ERR_WORKSPACE;
+  if (any_misaligned(dh, x, w_gate, w_up, gate, up, d_gate, d_up, dx, d_w_gate, d_w_up, workspace))
+    return BEAM_ERR_ALIGN;
+  const GatedBwdArgs a{(const uint16_t*)dh,   (const uint16_t*)x,    (const uint16_t*)w_gate,
+                       (const uint16_t*)w_up, (const uint16_t*)gate, (const uint16_t*)up,
+                       (uint16_t*)d_gate,     (uint16_t*)d_up,       (uint16_t*)dx,
+                       (uint16_t*)d_w_gate,   (uint16_t*)d_w_up,     (float*)workspace,
+                       T,                     cfg->hidden,           cfg->intermediate};
+  return launched(launch_gated_linear_backward(a, cfg->activation == BEAM_ACT_GELU, (hipStream_t)stream));
+}
+
+size_t beam_moe_lora_plan_bytes(int32_t T, int32_t n_adapters) {
+  if (check_lora_plan(T, n_adapters) != BEAM_OK || T == 0) return 0;
+  return LoraPlanLayout(T, n_adapters).words * sizeof(int32_t);
+}
+
+beam_status beam_moe_lora_plan(const int32_t* index, int32_t T, int32_t n_adapters, void* plan,
+                               size_t plan_bytes, void* stream) {
+  const beam_status cs = check_lora_plan(T, n_adapters);
+  if (cs != BEAM_OK) return cs;
+  if (T == 0) return BEAM_OK;
+  if (!index || !plan) return BEAM_ERR_NULL;
+  if (plan_bytes < beam_moe_lora_plan_bytes(T, n_adapters)) return BEAM_ERR_WORKSPACE;
+  if (any_misaligned(index, plan)) return BEAM_ERR_ALIGN;
+  return launched(launch_lora_plan(index, T, n_adapters, (int32_t*)plan, (hipStream_t)stream));
+}
+
+size_t beam_moe_lora_workspace_bytes(const beam_moe_lora_config* cfg, int32_t T) {
+  if (check_lora(cfg, T) != BEAM_OK || T == 0) return 0;
+  return lora_workspace_bytes(T, cfg->k, cfg->n, cfg->rank, cfg->n_adapters);
+}
+
+beam_status beam_moe_lora(const beam_moe_lora_config* cfg, int32_t T, const void* x, const void* a,
+                          const void* b, const float* scale, const void* plan, const void* base,
+                          void* out, float* v, void* workspace, size_t workspace_bytes, void* stream) {
+  const beam_status cs = check_lora(cfg, T);
+  if (cs != BEAM_OK) return cs;
+  if (T == 0) return BEAM_OK;
+  if (!x || !a || !b || !plan || !out) return BEAM_ERR_NULL;
+  if (!workspace || workspace_bytes < beam_moe_lora_workspace_bytes(cfg, T)) return BEAM_ERR_WORKSPACE;
+  if (any_misaligned(x, a, b, scale, plan, base, out, v, workspace)) return BEAM_ERR_ALIGN;
+  const LoraArgs p{(const uint16_t*)x,    (const uint16_t*)a, (const uint16_t*)b, scale,
+                   (const int32_t*)plan,  (const uint16_t*)base, (uint16_t*)out,  v,
+                   (float*)workspace,     T, cfg->k, cfg->n, cfg->rank, cfg->n_adapters};
+  return launched(launch_lora(p, (hipStream_t)stream));
+}
+
+size_t beam_moe_lora_backward_workspace_bytes(const beam_moe_lora_config* cfg, int32_t T) {
+  if (check_lora(cfg, T) != BEAM_OK || T == 0) return 0;
+  return lora_bwd_workspace_bytes(T, cfg->k, cfg->n, cfg->rank, cfg->n_adapters);
+}
+
+beam_status beam_moe_lora_backward(const beam_moe_lora_config* cfg, int32_t T, const void* dy,
+                                   const void* x, const float* v, const void* a, const void* b,
+                                   const float* scale, const void* plan, const void* base, void* dx,
+                                   void* d_a, void* d_b, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  const beam_status cs = check_lora(cfg, T);
+  if (cs != BEAM_OK) return cs;
+  if (T == 0) return BEAM_OK;
+  if (!dy || !a || !b || !plan || (!dx && !d_a)) return BEAM_ERR_NULL;
+  if (!d_a != !d_b || (d_a && (!x || !v))) return BEAM_ERR_NULL;
+  if (!workspace || workspace_bytes < beam_moe_lora_backward_workspace_bytes(cfg, T))
+    return BEAM_ERR_WORKSPACE;
+  if (any_misaligned(dy, x, v, a, b, scale, plan, base, dx, d_a, d_b, workspace)) return BEAM_ERR_ALIGN;
+  const LoraBwdArgs p{(const uint16_t*)dy, (const uint16_t*)x, v, (const uint16_t*)a,
+                      (const uint16_t*)b,  scale, (const int32_t*)plan, (const uint16_t*)base,
+                      (uint16_t*)dx,       (uint16_t*)d_a, (uint16_t*)d_b, workspace,
+                      T, cfg->k, cfg->n, cfg->rank, cfg->n_adapters};
+  return launched(launch_lora_backward(p, (hipStream_t)stream));
+}
+
+beam_status beam_moe_dropout(const beam_moe_dropout_config* cfg, int64_t n, const void* x,
+                             const void* stream_in, uint64_t seed, uint64_t offset,
+                             const int64_t* offset_dev, void* out, void* stream) {
+  const beam_status cs = check_dropout(cfg, n);
+  if (cs != BEAM_OK) return cs;
+  if (n == 0) return BEAM_OK;
+  if (!x || !out) return BEAM_ERR_NULL;
+  if (any_misaligned(x, stream_in, out) || (((uintptr_t)offset_dev) & 7u)) return BEAM_ERR_ALIGN;
+  DropoutArgs a = dropout_args(cfg, n, x, seed, offset, offset_dev);
+  a.stream_in = stream_in;
+  a.out = out;
+  return launched(launch_dropout(a, cfg->dtype == BEAM_F32, (hipStream_t)stream));
+}
+
+beam_status beam_moe_dropout_backward(const beam_moe_dropout_config* cfg, int64_t n, const void* dy,
+                                      uint64_t seed, uint64_t offset, const int64_t* offset_dev,
+                                      void* dx, void* d_stream_in, void* stream) {
+  const beam_status cs = check_dropout(cfg, n);
+  if (cs != BEAM_OK) return cs;
+  if (n == 0) return BEAM_OK;
+  if (!dy || !dx) return BEAM_ERR_NULL;
+  if (any_misaligned(dy, dx, d_stream_in) || (((uintptr_t)offset_dev) & 7u)) return BEAM_ERR_ALIGN;
+  DropoutArgs a = dropout_args(cfg, n, dy, seed, offset, offset_dev);
+  a.out = dx;
+  a.kept_grad = d_stream_in;
+  return launched(launch_dropout(a, cfg->dtype == BEAM_F32, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -582,6 +582,159 @@ beam_status beam_moe_mx4_linear(const beam_moe_linear* cfg, int32_t T, const voi
                                 const void* x_scale, const void* w, const void* w_scale,
                                 void* out, void* stream);
 
+/* ---- The dense MLP: gated product, adapters, dropout ---- */
+
+typedef enum beam_activation {
+  BEAM_ACT_SILU = 0, /* g sigmoid(g) */
+  BEAM_ACT_GELU = 1  /* g Phi(g), Phi the normal distribution (no tanh) */
+} beam_activation;
+
+/*
+ * The gated product of a dense MLP (the layers without experts; also of a shared
+ * expert), both projections, the activation and the product in one kernel:
+ *   gate = x w_gate^T + add_gate;  up = x w_up^T + add_up;  h = act(gate) * up.
+ * Sums are fp32, and h is made of the unrounded gate and up.
+ *   x                [T, hidden] bf16;  w_gate, w_up [intermediate, hidden] bf16.
+ *   add_gate, add_up [T, intermediate] bf16 or NULL (the adapters' shares).
+ *   h                out [T, intermediate] bf16.
+ *   gate, up         out [T, intermediate] bf16 or NULL: what the gradient needs. May be
+ *                    the same memory as add_gate and add_up, each as its own.
+ * Supported: hidden in [8, 65536] and intermediate in [8, 262144], multiples of 8;
+ * dtype BEAM_BF16. Errors: BEAM_ERR_NULL, BEAM_ERR_CONFIG (activation),
+ * BEAM_ERR_SHAPE, BEAM_ERR_DTYPE, BEAM_ERR_ALIGN, BEAM_ERR_HIP.
+ */
+typedef struct beam_moe_gated {
+  int32_t hidden;
+  int32_t intermediate;
+  int32_t activation; /* beam_activation */
+  int32_t dtype;      /* beam_dtype */
+} beam_moe_gated;
+
+beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const void* x,
+                                  const void* w_gate, const void* w_up, const void* add_gate,
+                                  const void* add_up, void* h, void* gate, void* up, void* stream);
+
+/*
+ * Its gradient, from the stored gate and up:
+ *   d_up = dh act(gate);  d_gate = dh up act'(gate), both rounded to bf16, then
+ *   dx = d_gate w_gate + d_up w_up;  d_w_gate = d_gate^T x;  d_w_up = d_up^T x.
+ *   dh, gate, up     [T, intermediate] bf16;  x, w_gate, w_up as above (x only for the
+ *                    weights' gradients, the weights only for dx).
+ *   d_gate, d_up     out [T, intermediate] bf16 (the adapters' gradients start from
+ *                    them). May be the same memory as gate and up, or dh.
+ *   dx               out [T, hidden] bf16 or NULL; needs a workspace of
+ *                    beam_moe_gated_linear_backward_workspace_bytes(cfg, T) (0: none).
+ *   d_w_gate, d_w_up out [intermediate, hidden] bf16, or both NULL. With T == 0 they
+ *                    are left as they were.
+ * Errors as above; BEAM_ERR_WORKSPACE.
+ */
+size_t beam_moe_gated_linear_backward_workspace_bytes(const beam_moe_gated* cfg, int32_t T);
+
+beam_status beam_moe_gated_linear_backward(const beam_moe_gated* cfg, int32_t T, const void* dh,
+                                           const void* x, const void* w_gate, const void* w_up,
+                                           const void* gate, const void* up, void* d_gate, void* d_up,
+                                           void* dx, void* d_w_gate, void* d_w_up, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/*
+ * Which tokens use which adapter, for beam_moe_lora and its gradient: once for all
+ * products of a batch. The plan groups the tokens by adapter, on the GPU.
+ *   index  [T] int32: the adapter of each token; outside [0, n_adapters): none.
+ *   plan   out, beam_moe_lora_plan_bytes(T, n_adapters) bytes; for calls with the
+ *          same T and n_adapters only.
+ * Supported: n_adapters in [1, 1024] (else BEAM_ERR_CONFIG).
+ */
+size_t beam_moe_lora_plan_bytes(int32_t T, int32_t n_adapters);
+
+beam_status beam_moe_lora_plan(const int32_t* index, int32_t T, int32_t n_adapters, void* plan,
+                               size_t plan_bytes, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a projection that they share, such as
+ * beam_moe_mx4_linear's: for a token with adapter i
+ *   v = a[i] x;  out = base + scale[i] b[i] v,
+ * and for a token without one v = 0, out = base. Sums are fp32; v goes into the second
+ * product as a sum of two bf16 values (16 significant bits).
+ *   x      [T, k] bf16;  a [n_adapters, rank, k] bf16;  b [n_adapters, n, rank] bf16.
+ *   scale  [n_adapters] fp32 or NULL (1).
+ *   plan   of beam_moe_lora_plan.
+ *   base   [T, n] bf16 or NULL (0);  out [T, n] bf16. May be the same memory.
+ *   v      out [T, rank] fp32 or NULL (the gradient needs it).
+ *   workspace  beam_moe_lora_workspace_bytes(cfg, T).
+ * Supported: rank in [8, 128], k in [8, 65536], n in [8, 262144], multiples of 8; dtype
+ * BEAM_BF16. Errors: BEAM_ERR_NULL, BEAM_ERR_CONFIG (rank, n_adapters),
+ * BEAM_ERR_SHAPE, BEAM_ERR_DTYPE, BEAM_ERR_WORKSPACE, BEAM_ERR_ALIGN, BEAM_ERR_HIP.
+ */
+typedef struct beam_moe_lora_config {
+  int32_t k;
+  int32_t n;
+  int32_t rank;
+  int32_t n_adapters;
+  int32_t dtype; /* beam_dtype */
+} beam_moe_lora_config;
+
+size_t beam_moe_lora_workspace_bytes(const beam_moe_lora_config* cfg, int32_t T);
+
+beam_status beam_moe_lora(const beam_moe_lora_config* cfg, int32_t T, const void* x, const void* a,
+                          const void* b, const float* scale, const void* plan, const void* base,
+                          void* out, float* v, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradient, from the stored v (the gradient of base is dy itself):
+ *   dv = scale[i] b[i]^T dy;  dx = base + a[i]^T dv (no adapter: base);
+ *   d_a[i] = sum over the tokens of adapter i of dv x^T;  d_b[i] = scale[i] sum of
+ *   dy v^T (an adapter without tokens: zeros).
+ *   dy   [T, n] bf16;  x, a, b, scale, plan as above;  v [T, rank] fp32 (x and v only
+ *        for the adapters' gradients).
+ *   base [T, k] bf16 or NULL: gradient that reaches x on another way;  dx out [T, k]
+ *        bf16 or NULL. May be the same memory.
+ *   d_a, d_b  out, shapes of a and b, bf16, or both NULL. With T == 0 they are left as
+ *        they were.
+ *   workspace  beam_moe_lora_backward_workspace_bytes(cfg, T).
+ * Errors as above.
+ */
+size_t beam_moe_lora_backward_workspace_bytes(const beam_moe_lora_config* cfg, int32_t T);
+
+beam_status beam_moe_lora_backward(const beam_moe_lora_config* cfg, int32_t T, const void* dy,
+                                   const void* x, const float* v, const void* a, const void* b,
+                                   const float* scale, const void* plan, const void* base, void* dx,
+                                   void* d_a, void* d_b, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * Dropout with a mask that is never stored, and the stream's update with it:
+ *   out[i] = keep * stream_in[i] + add * D(x[i]) (without stream_in: add * D(x[i])),
+ *   D(x[i]) = x[i] / (1 - q) where u[i] >= 65536 q, else 0 (also for an infinity or a NaN),
+ *   q = p rounded to a multiple of 1 / 65536.
+ * u[i] are 16 bits of Philox4x32-10 with the 64-bit key `seed` and the counter
+ * (i / 8, offset), each 64 bits, low word first: the low half of word (i % 8) / 2 for
+ * even i, the high half for odd i. So the mask depends on the seed, the offset and the
+ * place of the element in the flattened tensor alone.
+ *   x, stream_in, out  [n] dtype (BEAM_F32 or BEAM_BF16), stream_in may be NULL. out
+ *              may be the same memory as either.
+ *   offset_dev [1] int64 or NULL, 8-byte aligned: added to offset when the kernel runs, so
+ *              that replays of a graph can draw new masks.
+ * Supported: p in [0, 1]; keep, add finite; n <= 2^40. Errors: BEAM_ERR_NULL,
+ * BEAM_ERR_CONFIG (p, keep, add), BEAM_ERR_SHAPE (n), BEAM_ERR_DTYPE, BEAM_ERR_ALIGN,
+ * BEAM_ERR_HIP.
+ */
+typedef struct beam_moe_dropout_config {
+  float p;
+  float keep;
+  float add;
+  int32_t dtype; /* beam_dtype */
+} beam_moe_dropout_config;
+
+beam_status beam_moe_dropout(const beam_moe_dropout_config* cfg, int64_t n, const void* x,
+                             const void* stream_in, uint64_t seed, uint64_t offset,
+                             const int64_t* offset_dev, void* out, void* stream);
+
+/* Its gradient: dx = add * D(dy), d_stream_in = keep * dy ([n] or NULL). dx may be the
+ * same memory as dy; d_stream_in may not overlap either. */
+beam_status beam_moe_dropout_backward(const beam_moe_dropout_config* cfg, int64_t n, const void* dy,
+                                      uint64_t seed, uint64_t offset, const int64_t* offset_dev,
+                                      void* dx, void* d_stream_in, void* stream);
+
 /* Static, NUL-terminated description of a status code; never NULL. */
 const char* beam_moe_status_string(int32_t status);
 

@@ -42,3 +42,4 @@ from . import residual  # noqa: F401
 from . import backward  # noqa: F401
 from . import norm  # noqa: F401
 from . import gate  # noqa: F401
+from . import mlp  # noqa: F401
