@@ -43,7 +43,8 @@ EXPORTED = ("beam_moe_workspace_bytes", "beam_moe_route", "beam_moe_forward",
             "beam_moe_forward_shard", "beam_moe_forward_noalloc", "beam_moe_add_rms_norm",
             "beam_moe_add_rms_norm_backward_workspace_bytes", "beam_moe_add_rms_norm_backward",
             "beam_moe_gate", "beam_moe_gate_backward", "beam_moe_mx4_quantize",
-            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear", "beam_moe_gated_linear",
+            "beam_moe_mx4_dequantize", "beam_moe_mx4_linear", "beam_moe_gated_linear_workspace_bytes",
+            "beam_moe_gated_linear",
             "beam_moe_gated_linear_backward_workspace_bytes", "beam_moe_gated_linear_backward",
             "beam_moe_lora_plan_bytes", "beam_moe_lora_plan", "beam_moe_lora_workspace_bytes",
             "beam_moe_lora", "beam_moe_lora_backward_workspace_bytes", "beam_moe_lora_backward",
@@ -221,7 +222,9 @@ def lib():
         L.beam_moe_mx4_linear.argtypes = [linp, i32, vp, vp, vp, vp, vp, vp]
         gatedp, lorap = ctypes.POINTER(BeamMoeGated), ctypes.POINTER(BeamMoeLoraConfig)
         dropp, u64 = ctypes.POINTER(BeamMoeDropoutConfig), ctypes.c_uint64
-        L.beam_moe_gated_linear.argtypes = [gatedp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.beam_moe_gated_linear_workspace_bytes.argtypes = [gatedp, i32]
+        L.beam_moe_gated_linear_workspace_bytes.restype = sz
+        L.beam_moe_gated_linear.argtypes = [gatedp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.beam_moe_gated_linear_backward_workspace_bytes.argtypes = [gatedp, i32]
         L.beam_moe_gated_linear_backward_workspace_bytes.restype = sz
         L.beam_moe_gated_linear_backward.argtypes = [gatedp, i32, vp, vp, vp, vp, vp, vp, vp, vp,
@@ -885,7 +888,7 @@ def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, st
 
 
 def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=None,
-                 return_pre=False, stream=None):
+                 return_pre=False, workspace=None, stream=None):
     """The gated product of a dense MLP in one kernel: gate = x w_gate^T + add_gate,
     up = x w_up^T + add_up, h = act(gate) * up, act "silu" or "gelu" (g Phi(g)).
 
@@ -905,8 +908,11 @@ def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=No
         h = torch.empty(T, F, dtype=torch.bfloat16, device=dev)
         if return_pre:
             gate, up = torch.empty_like(h), torch.empty_like(h)
+        need = int(lib().beam_moe_gated_linear_workspace_bytes(ctypes.byref(cfg), T))
+        workspace = _scratch(workspace, need, dev) if need else None
         _launch("beam_moe_gated_linear", dev, lib().beam_moe_gated_linear, ctypes.byref(cfg), T,
-                _p(x), _p(w_gate), _p(w_up), _p(add_gate), _p(add_up), _p(h), _p(gate), _p(up))
+                _p(x), _p(w_gate), _p(w_up), _p(add_gate), _p(add_up), _p(h), _p(gate), _p(up),
+                _p(workspace), 0 if workspace is None else workspace.numel())
     return {"h": h, "gate": gate, "up": up}
 
 
@@ -926,9 +932,10 @@ def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", i
     with _on(dev, stream):
         dg, du = torch.empty_like(dh), torch.empty_like(dh)
         need = 0
+        if input_grad or weight_grad:
+            need = int(lib().beam_moe_gated_linear_backward_workspace_bytes(ctypes.byref(cfg), T))
         if input_grad:
             dx = torch.empty_like(x)
-            need = int(lib().beam_moe_gated_linear_backward_workspace_bytes(ctypes.byref(cfg), T))
         if weight_grad:  # no rows: the sums over them are 0
             dwg, dwu = ((torch.empty_like if T else torch.zeros_like)(w) for w in (w_gate, w_up))
         workspace = _scratch(workspace, need, dev) if need else None

@@ -103,8 +103,10 @@ struct GatedArgs {
   uint16_t* h;               // [T, F]
   uint16_t* gate;            // [T, F] or null
   uint16_t* up;              // [T, F] or null
+  float* part;               // workspace: sums over parts of H
   int T, H, F;
 };
+size_t gated_workspace_bytes(int T, int H, int F);
 // gelu: the activation is gelu (else silu)
 hipError_t launch_gated_linear(const GatedArgs& a, int gelu, hipStream_t st);
 
@@ -120,7 +122,7 @@ struct GatedBwdArgs {
   uint16_t* dx;          // [T, H] or null
   uint16_t* d_wg;        // [F, H] or null (both or none)
   uint16_t* d_wu;        // [F, H]
-  float* part;           // workspace: partial sums of dx
+  float* part;           // workspace: sums over parts of a product's reduction
   int T, H, F;
 };
 size_t gated_bwd_workspace_bytes(int T, int H, int F);

@@ -247,18 +247,26 @@ beam_status beam_moe_mx4_linear(const beam_moe_linear* cfg, int32_t T, const voi
   return launched(launch_mx4_linear(a, cfg->x_format, (hipStream_t)stream));
 }
 
+size_t beam_moe_gated_linear_workspace_bytes(const beam_moe_gated* cfg, int32_t T) {
+  if (check_gated(cfg, T) != BEAM_OK || T == 0) return 0;
+  return gated_workspace_bytes(T, cfg->hidden, cfg->intermediate);
+}
+
 beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const void* x,
                                   const void* w_gate, const void* w_up, const void* add_gate,
-                                  const void* add_up, void* h, void* gate, void* up, void* stream) {
+                                  const void* add_up, void* h, void* gate, void* up, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
   const beam_status cs = check_gated(cfg, T);
   if (cs != BEAM_OK) return cs;
   if (T == 0) return BEAM_OK;
   if (!x || !w_gate || !w_up || !h) return BEAM_ERR_NULL;
-  if (any_misaligned(x, w_gate, w_up, add_gate, add_up, h, gate, up)) return BEAM_ERR_ALIGN;
+  const size_t need = beam_moe_gated_linear_workspace_bytes(cfg, T);
+  if (need && (!workspace || workspace_bytes < need)) return BEAM_ERR_WORKSPACE;
+  if (any_misaligned(x, w_gate, w_up, add_gate, add_up, h, gate, up, workspace)) return BEAM_ERR_ALIGN;
   const GatedArgs a{(const uint16_t*)x,        (const uint16_t*)w_gate, (const uint16_t*)w_up,
                     (const uint16_t*)add_gate, (const uint16_t*)add_up, (uint16_t*)h,
-                    (uint16_t*)gate,           (uint16_t*)up,           T,
-                    cfg->hidden,               cfg->intermediate};
+                    (uint16_t*)gate,           (uint16_t*)up,           (float*)workspace,
+                    T,                         cfg->hidden,             cfg->intermediate};
   return launched(launch_gated_linear(a, cfg->activation == BEAM_ACT_GELU, (hipStream_t)stream));
 }
 
@@ -278,7 +286,7 @@ beam_status beam_moe_gated_linear_backward(const beam_moe_gated* cfg, int32_t T,
   if (!dh || !gate || !up || !d_gate || !d_up) return BEAM_ERR_NULL;
   if (dx && (!w_gate || !w_up)) return BEAM_ERR_NULL;
   if (!d_w_gate != !d_w_up || (d_w_gate && !x)) return BEAM_ERR_NULL;
-  const size_t need = dx ? beam_moe_gated_linear_backward_workspace_bytes(cfg, T) : 0;
+  const size_t need = dx || d_w_gate ? beam_moe_gated_linear_backward_workspace_bytes(cfg, T) : 0;
   if (need && (!workspace || workspace_bytes < need)) return BEAM_ERR_WORKSPACE;
   if (any_misaligned(dh, x, w_gate, w_up, gate, up, d_gate, d_up, dx, d_w_gate, d_w_up, workspace))
     return BEAM_ERR_ALIGN;

@@ -599,9 +599,10 @@ typedef enum beam_activation {
  *   h                out [T, intermediate] bf16.
  *   gate, up         out [T, intermediate] bf16 or NULL: what the gradient needs. May be
  *                    the same memory as add_gate and add_up, each as its own.
+ *   workspace        beam_moe_gated_linear_workspace_bytes(cfg, T) (0: none).
  * Supported: hidden in [8, 65536] and intermediate in [8, 262144], multiples of 8;
  * dtype BEAM_BF16. Errors: BEAM_ERR_NULL, BEAM_ERR_CONFIG (activation),
- * BEAM_ERR_SHAPE, BEAM_ERR_DTYPE, BEAM_ERR_ALIGN, BEAM_ERR_HIP.
+ * BEAM_ERR_SHAPE, BEAM_ERR_DTYPE, BEAM_ERR_WORKSPACE, BEAM_ERR_ALIGN, BEAM_ERR_HIP.
  */
 typedef struct beam_moe_gated {
   int32_t hidden;
@@ -610,9 +611,12 @@ typedef struct beam_moe_gated {
   int32_t dtype;      /* beam_dtype */
 } beam_moe_gated;
 
+size_t beam_moe_gated_linear_workspace_bytes(const beam_moe_gated* cfg, int32_t T);
+
 beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const void* x,
                                   const void* w_gate, const void* w_up, const void* add_gate,
-                                  const void* add_up, void* h, void* gate, void* up, void* stream);
+                                  const void* add_up, void* h, void* gate, void* up, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * Its gradient, from the stored gate and up:
@@ -622,11 +626,12 @@ beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const vo
  *                    weights' gradients, the weights only for dx).
  *   d_gate, d_up     out [T, intermediate] bf16 (the adapters' gradients start from
  *                    them). May be the same memory as gate and up, or dh.
- *   dx               out [T, hidden] bf16 or NULL; needs a workspace of
- *                    beam_moe_gated_linear_backward_workspace_bytes(cfg, T) (0: none).
+ *   dx               out [T, hidden] bf16 or NULL.
  *   d_w_gate, d_w_up out [intermediate, hidden] bf16, or both NULL. With T == 0 they
  *                    are left as they were.
- * Errors as above; BEAM_ERR_WORKSPACE.
+ *   workspace        beam_moe_gated_linear_backward_workspace_bytes(cfg, T) (0: none), for
+ *                    dx and the weights' gradients.
+ * Errors as above.
  */
 size_t beam_moe_gated_linear_backward_workspace_bytes(const beam_moe_gated* cfg, int32_t T);
 

@@ -24,11 +24,11 @@ def L():
 GATED = dict(hidden=512, intermediate=264, activation=0, dtype=gl.BEAM_BF16)
 
 
-def _gated(L, T=8, cfg=GATED, **over):
-    p = dict(x=FAKE, wg=FAKE, wu=FAKE, ag=FAKE, au=FAKE, h=FAKE, g=FAKE, u=FAKE)
+def _gated(L, T=8, cfg=GATED, ws_bytes=HUGE, **over):
+    p = dict(x=FAKE, wg=FAKE, wu=FAKE, ag=FAKE, au=FAKE, h=FAKE, g=FAKE, u=FAKE, ws=FAKE)
     p.update(over)
     c = ctypes.byref(gl.BeamMoeGated(**cfg)) if cfg else None
-    return L.beam_moe_gated_linear(c, T, *p.values(), None)
+    return L.beam_moe_gated_linear(c, T, *p.values(), ws_bytes, None)
 
 
 def _gated_bwd(L, T=8, cfg=GATED, ws_bytes=HUGE, **over):
@@ -52,19 +52,24 @@ def test_gated_checks(L):
         assert call(L, T=0, x=None) == gl.BEAM_OK
     for name in ("x", "wg", "wu", "h"):
         assert _gated(L, **{name: None}) == gl.BEAM_ERR_NULL, name
-    for name in ("x", "wg", "wu", "ag", "au", "h", "g", "u"):
+    for name in ("x", "wg", "wu", "ag", "au", "h", "g", "u", "ws"):
         assert _gated(L, **{name: FAKE + 8}) == gl.BEAM_ERR_ALIGN, name
     for name in ("dh", "g", "u", "dg", "du", "wg", "wu", "x", "dwg", "dwu"):
         assert _gated_bwd(L, **{name: None}) == gl.BEAM_ERR_NULL, name
     for name in ("dh", "x", "wg", "wu", "g", "u", "dg", "du", "dx", "dwg", "dwu", "ws"):
         assert _gated_bwd(L, **{name: FAKE + 8}) == gl.BEAM_ERR_ALIGN, name
-    for T in (1, 8, 100, 4096):
-        c = ctypes.byref(gl.BeamMoeGated(**GATED))
-        need = L.beam_moe_gated_linear_backward_workspace_bytes(c, T)
-        if need:
-            assert _gated_bwd(L, T=T, ws=None) == gl.BEAM_ERR_WORKSPACE
-            assert _gated_bwd(L, T=T, ws_bytes=need - 1) == gl.BEAM_ERR_WORKSPACE
-    assert L.beam_moe_gated_linear_backward_workspace_bytes(None, 8) == 0
+    c = gl.BeamMoeGated(**dict(GATED, hidden=4096))
+    for call, size in ((_gated, L.beam_moe_gated_linear_workspace_bytes),
+                       (_gated_bwd, L.beam_moe_gated_linear_backward_workspace_bytes)):
+        assert size(None, 8) == 0 and size(ctypes.byref(c), -1) == 0 and size(ctypes.byref(c), 0) == 0
+        seen = 0
+        for T in (1, 8, 100, 4096):
+            need = size(ctypes.byref(c), T)
+            if need:
+                seen += 1
+                assert call(L, T=T, cfg=dict(GATED, hidden=4096), ws=None) == gl.BEAM_ERR_WORKSPACE
+                assert call(L, T=T, cfg=dict(GATED, hidden=4096), ws_bytes=need - 1) == gl.BEAM_ERR_WORKSPACE
+        assert seen
 
 
 LORA = dict(k=512, n=264, rank=16, n_adapters=5, dtype=gl.BEAM_BF16)

@@ -218,7 +218,7 @@ def test_activation_tails():
             assert (err <= rel * np.abs(ref) + 2.0 ** -100).all(), (act, g, _f(got), ref)
 
 
-@pytest.mark.parametrize("T,H,F", [(1, 72, 40), (30, 520, 136), (77, 328, 264), (150, 72, 136), (300, 200, 264)])
+@pytest.mark.parametrize("T,H,F", [(1, 72, 40), (30, 520, 136), (77, 328, 264), (150, 72, 136), (300, 200, 264), (40, 4104, 72)])
 def test_writes_stay_inside(T, H, F):
     """Exactly sized outputs between canaries, through the C ABI."""
     dev, L = _dev(), gl.lib()
@@ -226,9 +226,12 @@ def test_writes_stay_inside(T, H, F):
     cfg = gl.BeamMoeGated(H, F, 0, gl.BEAM_BF16)
     bufs = {n: Guarded(2 * T * F, dev, n) for n in ("h", "gate", "up", "dg", "du")}
     ptr = {n: g.view.data_ptr() for n, g in bufs.items()}
+    need = L.beam_moe_gated_linear_workspace_bytes(ctypes.byref(cfg), T)
+    fws = Guarded(max(need, 256), dev, "forward workspace")
     st = L.beam_moe_gated_linear(ctypes.byref(cfg), T, x.data_ptr(), wg.data_ptr(), wu.data_ptr(), None, None,
-                                 ptr["h"], ptr["gate"], ptr["up"], None)
+                                 ptr["h"], ptr["gate"], ptr["up"], fws.view.data_ptr(), need, None)
     assert st == gl.BEAM_OK
+    fneed = need
     need = L.beam_moe_gated_linear_backward_workspace_bytes(ctypes.byref(cfg), T)
     ws = Guarded(max(need, 256), dev, "workspace")
     out = {"dx": Guarded(2 * T * H, dev, "dx"), "dwg": Guarded(2 * F * H, dev, "dwg"),
@@ -237,7 +240,7 @@ def test_writes_stay_inside(T, H, F):
         ctypes.byref(cfg), T, ptr["h"], x.data_ptr(), wg.data_ptr(), wu.data_ptr(), ptr["gate"], ptr["up"],
         ptr["dg"], ptr["du"], *(g.view.data_ptr() for g in out.values()), ws.view.data_ptr(), need, None)
     assert st == gl.BEAM_OK
-    for g in [*bufs.values(), *out.values(), ws]:
+    for g in [*bufs.values(), *out.values(), ws, fws]:
         g.check()
     fw = gl.gated_linear(x, wg, wu, return_pre=True)
     assert torch.equal(bufs["h"].tensor((T, F), torch.bfloat16), fw["h"])
@@ -251,7 +254,8 @@ def test_writes_stay_inside(T, H, F):
     bref = gl.gated_linear_backward(dh, x, wg, wu, ref["gate"], ref["up"])
     h = torch.empty_like(ag)
     assert L.beam_moe_gated_linear(ctypes.byref(cfg), T, x.data_ptr(), wg.data_ptr(), wu.data_ptr(), ag.data_ptr(),
-                                   au.data_ptr(), h.data_ptr(), ag.data_ptr(), au.data_ptr(), None) == gl.BEAM_OK
+                                   au.data_ptr(), h.data_ptr(), ag.data_ptr(), au.data_ptr(), fws.view.data_ptr(),
+                                   fneed, None) == gl.BEAM_OK
     assert torch.equal(ag, ref["gate"]) and torch.equal(au, ref["up"]) and torch.equal(h, ref["h"])
     assert L.beam_moe_gated_linear_backward(
         ctypes.byref(cfg), T, dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), ag.data_ptr(),
