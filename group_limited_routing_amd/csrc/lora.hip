@@ -19,8 +19,9 @@ constexpr int kPlanWaves = 16;
 __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_t* __restrict__ index, int T,
                                                                     int E, int32_t* __restrict__ plan) {
   __shared__ int32_t part[kPlanWaves][kLoraMaxE + 1];
-  __shared__ int32_t start[kLoraMaxE + 2], tile0[kLoraMaxE + 2], chunk0[kLoraMaxE + 2];
+  __shared__ int32_t start[kLoraMaxE + 2], tile0[kLoraMaxE + 2], chunk0[kLoraMaxE + 2], padded0[kLoraMaxE + 2];
   const LoraPlanLayout at(T, E);
+  const int chunk = at.chunk;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, G = E + 1;
   const int per = ((T + kPlanWaves - 1) / kPlanWaves + 63) & ~63;
   const int t0 = min(wave * per, T), t1 = min(t0 + per, T);
@@ -32,34 +33,38 @@ __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_
   };
   for (int t = t0 + lane; t < t1; t += 64) atomicAdd(&part[wave][group(t)], 1);
   __syncthreads();
-  if (wave == 0) {  // exclusive scans of the groups' tokens, tiles and chunks
-    int s = 0, ts = 0, cs = 0;
+  if (wave == 0) {  // exclusive scans of the groups' tokens, tiles, chunks, slots and padded tokens
+    int total[5] = {};
     for (int g0 = 0; g0 < G; g0 += 64) {
       const int g = g0 + lane;
       int n = 0;
       if (g < G)
         for (int w = 0; w < kPlanWaves; ++w) n += part[w][g];
-      const int nt = (n + kLoraTile - 1) / kLoraTile, nc = g < E ? (n + kLoraChunk - 1) / kLoraChunk : 0;
-      int a = n, b = nt, c = nc;
-      for (int d = 1; d < 64; d <<= 1) {
-        const int oa = __shfl_up(a, d), ob = __shfl_up(b, d), oc = __shfl_up(c, d);
-        if (lane >= d) a += oa, b += ob, c += oc;
+      const int nc = g < E ? (n + chunk - 1) / chunk : 0;
+      const int own[5] = {n, (n + kLoraTile - 1) / kLoraTile, nc, nc > 1 ? nc : 0, g < E ? (n + 31) & ~31 : 0};
+      int before[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        int v = own[i];
+        for (int d = 1; d < 64; d <<= 1) {
+          const int o = __shfl_up(v, d);
+          if (lane >= d) v += o;
+        }
+        before[i] = total[i] + v - own[i];
+        total[i] += __shfl(v, 63);
       }
       if (g < G) {
-        start[g] = s + a - n;
-        tile0[g] = ts + b - nt;
-        chunk0[g] = cs + c - nc;
+        start[g] = before[0];
+        tile0[g] = before[1];
+        chunk0[g] = before[2];
+        padded0[g] = before[4];
+        if (g < E) plan[at.o_slot + g] = nc > 1 ? before[3] : -1;
       }
-      s += __shfl(a, 63);
-      ts += __shfl(b, 63);
-      cs += __shfl(c, 63);
     }
     if (lane == 0) {
-      start[G] = s;
-      tile0[G] = ts;
-      chunk0[G] = cs;
-      plan[0] = ts;
-      plan[1] = cs;
+      start[G] = total[0];
+      plan[0] = total[1];
+      plan[1] = total[2];
     }
   }
   __syncthreads();
@@ -79,8 +84,8 @@ __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_
     for (int j = tid; j * kLoraTile < n; j += 64 * kPlanWaves)
       tiles[tile0[g] + j] = make_int4(e, s + j * kLoraTile, min(kLoraTile, n - j * kLoraTile), 0);
     if (g < E)
-      for (int j = tid; j * kLoraChunk < n; j += 64 * kPlanWaves)
-        chunks[chunk0[g] + j] = make_int4(e, s + j * kLoraChunk, min(kLoraChunk, n - j * kLoraChunk), 0);
+      for (int j = tid; j * chunk < n; j += 64 * kPlanWaves)
+        chunks[chunk0[g] + j] = make_int4(e, s + j * chunk, min(chunk, n - j * chunk), padded0[g] + j * chunk);
   }
   __syncthreads();
   int32_t* order = plan + at.o_order;
@@ -100,69 +105,483 @@ __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_
   }
 }
 
-__device__ __forceinline__ float bf(const uint16_t* p, size_t i) { return bf16_bits_to_f32(p[i]); }
+__device__ __forceinline__ int4 tile_at(const int32_t* plan, const LoraPlanLayout& at, int i) {
+  return reinterpret_cast<const int4*>(plan + at.o_tiles)[i];
+}
+__device__ __forceinline__ int4 chunk_at(const int32_t* plan, const LoraPlanLayout& at, int i) {
+  return reinterpret_cast<const int4*>(plan + at.o_chunks)[i];
+}
 
-// ------------------------------------------------------------------ simple kernels
-// v[t, r] = f sum over k of x[t, k] m[e][r * rs + k * ks]; a workgroup per token tile
-// and r, a wave per token in turn.
-__global__ __launch_bounds__(256) void lora_in_kernel(const uint16_t* x, const uint16_t* m, const float* scale,
-                                                      const int32_t* plan, int T, int E, int R, int K,
-                                                      int rs, int ks, float* v) {
+// v as the sum of two bf16 values, 16 significant bits; beyond the largest bf16 number,
+// and for NaN, the first alone.
+__device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
+  hi = f32_to_bf16_bits(v);
+  const float rest = v - bf16_bits_to_f32(hi);
+  lo = (hi & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_bits(rest);
+}
+
+// ------------------------------------------------------------------ into the rank
+// part[ks][position][r] = sum over a part of k of x[t, k] m[e][r, k]: a workgroup per
+// tile of tokens and part of k, its waves take 128 values of k in turn, and the four
+// sums are added through LDS. MFMA rows are r, columns tokens; both operands go from
+// memory into registers, 64 bytes of a row at a time.
+template <int RB, int TB>
+__device__ __forceinline__ void rank_sums(const uint16_t* x, const uint16_t* m, const int32_t* order, int count,
+                                          int R, int K, int first, int step, f32x4 (&acc)[TB][RB]) {
+  const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const uint16_t* xr[TB];
+  const uint16_t* mr[RB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) xr[b] = x + (size_t)order[min(b * 16 + l, count - 1)] * K + g * 8;
+#pragma unroll
+  for (int b = 0; b < RB; ++b) mr[b] = m + (size_t)min(b * 16 + l, R - 1) * K + g * 8;
+  for (int k0 = first * 128; k0 < K; k0 += step * 128) {
+    u32x4 xf[4][TB], mf[4][RB];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k = k0 + s * 32;
+      const bool in = k + g * 8 < K;  // K is a multiple of 8
+#pragma unroll
+      for (int b = 0; b < TB; ++b) xf[s][b] = in ? ld16(xr[b] + k) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int b = 0; b < RB; ++b) mf[s][b] = in ? ld16(mr[b] + k) : u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int b = 0; b < TB; ++b)
+#pragma unroll
+        for (int q = 0; q < RB; ++q)
+          acc[b][q] = mfma_bf16(as_bf16x8(mf[s][q]), as_bf16x8(xf[s][b]), acc[b][q]);
+  }
+}
+
+template <int RB>
+__global__ __launch_bounds__(256) void lora_in_kernel(const uint16_t* __restrict__ x,
+                                                      const uint16_t* __restrict__ m,
+                                                      const int32_t* __restrict__ plan, int T, int E, int R,
+                                                      int K, float* __restrict__ part) {
+  __shared__ f32x4 sums[4][4][RB][64];
   const LoraPlanLayout at(T, E);
   if ((int)blockIdx.x >= plan[0]) return;
-  const int4 tile = reinterpret_cast<const int4*>(plan + at.o_tiles)[blockIdx.x];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = blockIdx.y;
-  for (int i = wave; i < tile.z; i += 4) {
-    const int t = plan[at.o_order + tile.y + i];
-    float s = 0.f;
-    if (tile.x >= 0)
-      for (int k = lane; k < K; k += 64)
-        s += bf(x, (size_t)t * K + k) * bf(m, (size_t)tile.x * R * K + (size_t)r * rs + (size_t)k * ks);
-    s = wave_sum(s);
-    if (lane == 0) v[(size_t)t * R + r] = tile.x >= 0 && scale ? s * scale[tile.x] : s;
+  const int4 tile = tile_at(plan, at, blockIdx.x);
+  if (tile.x < 0) return;  // no adapter: nothing reads these sums
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int32_t* order = plan + at.o_order + tile.y;
+  const uint16_t* me = m + (size_t)tile.x * R * K;
+  const int first = blockIdx.y * 4 + wave, step = gridDim.y * 4, tb = (tile.z + 15) / 16;
+  auto run = [&](auto n) {
+    constexpr int TB = decltype(n)::value;
+    f32x4 acc[TB][RB] = {};
+    rank_sums<RB, TB>(x, me, order, tile.z, R, K, first, step, acc);
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int q = 0; q < RB; ++q) sums[wave][b][q][lane] = acc[b][q];
+  };
+  if (tb == 1)
+    run(std::integral_constant<int, 1>{});
+  else if (tb == 2)
+    run(std::integral_constant<int, 2>{});
+  else
+    run(std::integral_constant<int, 4>{});
+  __syncthreads();
+  // lane (token l, rows 4 g ..): 4 consecutive values of r
+  for (int i = wave; i < tb * RB; i += 4) {
+    const int b = i / RB, q = i % RB, t = b * 16 + (lane & 15), r = q * 16 + (lane >> 4) * 4;
+    f32x4 s = sums[0][b][q][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) s += sums[w][b][q][lane];
+    if (t < tile.z && r < R)
+      *reinterpret_cast<f32x4*>(part + ((size_t)blockIdx.y * T + tile.y + t) * R + r) = s;
   }
 }
 
-// out[t, n] = base[t, n] + f sum over r of v[t, r] m[e][n * ns + r * rs]
-__global__ __launch_bounds__(256) void lora_out_kernel(const float* v, const uint16_t* m, const float* scale,
-                                                       const int32_t* plan, int T, int E, int R, int N, int ns,
-                                                       int rs, const uint16_t* base, uint16_t* out) {
+// ------------------------------------------------------------------ out of the rank
+// out[t, n] = base[t, n] + sum over r of f v[t, r] m[e][n, r], v the sum of `parts` rows in
+// their order. MFMA rows are n, columns tokens, and the reduction runs over the first
+// and then the second parts of f v. Fragment j of a wave's 64 columns takes rows n =
+// 16 (i / 4) + 4 j + i % 4, so that a lane ends with 16 consecutive columns of a token.
+template <int RB>
+__global__ __launch_bounds__(256) void lora_out_kernel(const float* __restrict__ part, int parts,
+                                                       const uint16_t* __restrict__ m,
+                                                       const float* __restrict__ scale,
+                                                       const int32_t* __restrict__ plan, int T, int E, int R,
+                                                       int N, int width, const uint16_t* base, uint16_t* out,
+                                                       float* __restrict__ v) {
+  constexpr int PITCH = RB * 32 + 8;  // values of a token in LDS: hi, lo, padding
+  __shared__ __attribute__((aligned(16))) uint16_t vs[64 * PITCH];
+  __shared__ int32_t tokens[64];
   const LoraPlanLayout at(T, E);
   if ((int)blockIdx.x >= plan[0]) return;
-  const int4 tile = reinterpret_cast<const int4*>(plan + at.o_tiles)[blockIdx.x];
-  const int n = blockIdx.y * 256 + threadIdx.x;
-  if (n >= N) return;
-  for (int i = 0; i < tile.z; ++i) {
-    const int t = plan[at.o_order + tile.y + i];
-    float s = 0.f;
-    if (tile.x >= 0) {
-      for (int r = 0; r < R; ++r)
-        s += v[(size_t)t * R + r] * bf(m, (size_t)tile.x * R * N + (size_t)n * ns + (size_t)r * rs);
-      if (scale) s *= scale[tile.x];
+  const int4 tile = tile_at(plan, at, blockIdx.x);
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.y * width, n1 = min(N, n0 + width);
+  if (tid < 64) tokens[tid] = plan[at.o_order + tile.y + min(tid, tile.z - 1)];
+  const bool live = tile.x >= 0;
+  if (!live) {  // these keep their base
+    __syncthreads();
+    if (v && blockIdx.y == 0)
+      for (int i = tid; i < tile.z * R; i += 256) v[(size_t)tokens[i / R] * R + i % R] = 0.f;
+    if (base == out) return;
+    const int chunks = (n1 - n0) / 8;
+    for (int i = tid; i < tile.z * chunks; i += 256) {
+      const size_t o = (size_t)tokens[i / chunks] * N + n0 + i % chunks * 8;
+      st16(out + o, base ? ld16(base + o) : u32x4{0, 0, 0, 0});
     }
-    const size_t o = (size_t)t * N + n;
-    out[o] = (uint16_t)f32_to_bf16_bits(base ? s + bf(base, o) : s);
+    return;
+  }
+  const float f = scale ? scale[tile.x] : 1.f;
+  const int r4 = R / 4;
+  if (v && blockIdx.y == 0) __syncthreads();  // tokens
+  for (int i = tid; i < tile.z * r4; i += 256) {
+    const int t = i / r4, r = i % r4 * 4;
+    f32x4 s{};
+    for (int p = 0; p < parts; ++p)
+      s += *reinterpret_cast<const f32x4*>(part + ((size_t)p * T + tile.y + t) * R + r);
+    if (v && blockIdx.y == 0) *reinterpret_cast<f32x4*>(v + (size_t)tokens[t] * R + r) = s;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t hi, lo;
+      split(s[q] * f, hi, lo);
+      vs[t * PITCH + r + q] = (uint16_t)hi;
+      vs[t * PITCH + R + r + q] = (uint16_t)lo;
+    }
+  }
+  __syncthreads();
+  const uint16_t* me = m + (size_t)tile.x * R * N;
+  const int steps = (2 * R + 31) / 32, tb = (tile.z + 15) / 16;
+  for (int nb = n0 + wave * 64; nb < n1; nb += 256) {
+    f32x4 acc[4][4] = {};
+#pragma unroll
+    for (int s = 0; s < RB; ++s) {  // steps <= RB
+      if (s >= steps) break;
+      const int kk = s * 32 + g * 8;
+      const bool in = kk < 2 * R;
+      const int r = kk < R ? kk : kk - R;
+      u32x4 mf[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = min(nb + 16 * (l / 4) + 4 * j + l % 4, N - 1);
+        mf[j] = in ? ld16(me + (size_t)n * R + r) : u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (b >= tb) break;
+        // tokens past the tile's last one repeat it, and are not stored
+        const u32x4 vf = in ? ld16(vs + min(b * 16 + l, tile.z - 1) * PITCH + kk) : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[b][j] = mfma_bf16(as_bf16x8(mf[j]), as_bf16x8(vf), acc[b][j]);
+      }
+    }
+    const int n = nb + 16 * g;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int t = b * 16 + l;
+      if (t >= tile.z) continue;
+      const size_t o = (size_t)tokens[t] * N + n;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (n + 8 * half >= N) continue;
+        u32x4 d{0, 0, 0, 0};
+        if (base) d = ld16(base + o + 8 * half);
+        u32x4 w;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = 2 * half + q / 2, e = q % 2 * 2;
+          w[q] = pack_bf16x2(acc[b][j][e] + __uint_as_float(d[q] << 16),
+                             acc[b][j][e + 1] + __uint_as_float(d[q] & 0xffff0000u));
+        }
+        st16(out + o + 8 * half, w);
+      }
+    }
   }
 }
 
-// d[e][r * rs + c * cs] = f sum over the adapter's tokens of v[t, r] x[t, c]
-__global__ __launch_bounds__(256) void lora_grad_kernel(const float* v, const uint16_t* x, const float* scale,
-                                                        const int32_t* plan, int T, int E, int R, int C, int rs,
-                                                        int cs, uint16_t* d) {
-  const LoraPlanLayout at(T, E);
-  const int e = blockIdx.z, r = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= C) return;
-  float s = 0.f;
-  for (int j = plan[at.o_first + e]; j < plan[at.o_first + e + 1]; ++j) {
-    const int4 ch = reinterpret_cast<const int4*>(plan + at.o_chunks)[j];
-    for (int i = 0; i < ch.z; ++i) {
-      const int t = plan[at.o_order + ch.y + i];
-      s += v[(size_t)t * R + r] * bf(x, (size_t)t * C + c);
+// ------------------------------------------------------------------ gradients
+// a [E, R, K] -> [E, K, R] and b [E, N, R] -> [E, R, N], 64 x 64 blocks through LDS.
+__global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ a,
+                                                             const uint16_t* __restrict__ b, int E, int R, int K,
+                                                             int N, uint16_t* __restrict__ at,
+                                                             uint16_t* __restrict__ bt) {
+  __shared__ uint16_t tile[64][72];
+  const int rb = (R + 63) / 64, kb = (K + 63) / 64, nb = (N + 63) / 64;
+  int i = blockIdx.x;
+  const bool of_a = i < rb * kb;
+  if (!of_a) i -= rb * kb;
+  const int rows = of_a ? R : N, cols = of_a ? K : R, cb = of_a ? kb : rb;
+  const uint16_t* src = (of_a ? a : b) + (size_t)blockIdx.y * rows * cols;
+  uint16_t* dst = (of_a ? at : bt) + (size_t)blockIdx.y * rows * cols;
+  const int r0 = i / cb * 64, c0 = i % cb * 64;
+  for (int q = threadIdx.x; q < 512; q += 256) {
+    const int r = r0 + q / 8, c = c0 + q % 8 * 8;
+    if (r < rows && c < cols) {
+      const u32x4 v = ld16(src + (size_t)r * cols + c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        tile[q % 8 * 8 + 2 * e][q / 8] = (uint16_t)v[e];
+        tile[q % 8 * 8 + 2 * e + 1][q / 8] = (uint16_t)(v[e] >> 16);
+      }
     }
   }
-  if (scale) s *= scale[e];
-  d[(size_t)e * R * C + (size_t)r * rs + (size_t)c * cs] = (uint16_t)f32_to_bf16_bits(s);
+  __syncthreads();
+  for (int q = threadIdx.x; q < 512; q += 256) {
+    const int c = c0 + q / 8, r = r0 + q % 8 * 8;
+    if (c < cols && r < rows) st16(dst + (size_t)c * rows + r, ld16(&tile[q / 8][q % 8 * 8]));
+  }
 }
+
+// dv = f times the sum of its parts, in the tokens' order, and, for the adapters'
+// gradients, dv and f v as operands: two bf16 parts, a row of padded positions for each
+// r. A workgroup per 64 positions of a chunk (those past its last token: zeros).
+__global__ __launch_bounds__(256) void lora_operands_kernel(const float* part, int parts, const float* v,
+                                                            const float* scale, const int32_t* __restrict__ plan,
+                                                            int T, int E, int R, float* dv, uint16_t* dvt,
+                                                            uint16_t* vt) {
+  extern __shared__ uint32_t pairs[];  // [R][66]: hi in the low half, lo
+  const LoraPlanLayout at(T, E);
+  const int per = at.chunk / 64, c = blockIdx.x / per;
+  if (c >= plan[1]) return;
+  const int4 chunk = chunk_at(plan, at, c);
+  const int p0 = blockIdx.x % per * 64;
+  if (p0 >= chunk.z) return;
+  const int count = min(64, chunk.z - p0), padded = (count + 31) & ~31;
+  const float f = scale ? scale[chunk.x] : 1.f;
+  const int which = blockIdx.y;  // 0: dv, 1: v
+  for (int i = threadIdx.x; i < 64 * (R / 4); i += 256) {
+    const int t = i / (R / 4), r = i % (R / 4) * 4;
+    f32x4 s{};
+    if (t < count) {
+      const int pos = chunk.y + p0 + t;
+      if (which == 0) {
+        for (int p = 0; p < parts; ++p)
+          s += *reinterpret_cast<const f32x4*>(part + ((size_t)p * T + pos) * R + r);
+        s *= f;
+        *reinterpret_cast<f32x4*>(dv + (size_t)pos * R + r) = s;
+      } else {
+        s = *reinterpret_cast<const f32x4*>(v + (size_t)plan[at.o_order + pos] * R + r) * f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t hi, lo;
+      split(s[q], hi, lo);
+      pairs[(r + q) * 66 + t] = hi | lo << 16;
+    }
+  }
+  __syncthreads();
+  uint16_t* to = which == 0 ? dvt : vt;
+  if (!to) return;
+  for (int i = threadIdx.x; i < R * 8; i += 256) {
+    const int r = i / 8, t = i % 8 * 8;
+    if (t >= padded) continue;
+    u32x4 hi, lo;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t x = pairs[r * 66 + t + 2 * q], y = pairs[r * 66 + t + 2 * q + 1];
+      hi[q] = (x & 0xffffu) | y << 16;
+      lo[q] = x >> 16 | (y & 0xffff0000u);
+    }
+    uint16_t* row = to + (size_t)r * at.padded + chunk.w + p0 + t;
+    st16(row, hi);
+    st16(row + (size_t)R * at.padded, lo);
+  }
+}
+
+struct LoraGradArgs {
+  const uint16_t* op[2];  // operands [2, R, padded]: dv for d_a, f v for d_b
+  const uint16_t* rows[2];  // x [T, K], dy [T, N]
+  uint16_t* out[2];       // d_a [E, R, K], d_b [E, N, R]
+  float* part[2];         // [slots, R, C]
+  const int32_t* plan;
+  int T, E, R, C[2];
+};
+
+// sum over a chunk's tokens of op[t, r] rows[t, c] for 64 values of r and 128 columns a
+// wave. MFMA rows are r, columns c, the reduction runs over 32 tokens. Lane (l, g) loads
+// columns 8 l .. + 7 of tokens 8 g .. + 7, whole 256-byte runs of a row, and turns them in
+// its registers into fragment j of column 8 l + j, whose reduction values are its 8 tokens.
+template <int RB>
+__global__ __launch_bounds__(256) void lora_grad_kernel(LoraGradArgs p) {
+  __shared__ __attribute__((aligned(16))) int32_t tokens[512];
+  const LoraPlanLayout at(p.T, p.E);
+  const int wgs0 = (p.C[0] + 511) / 512;
+  const int which = (int)blockIdx.x >= wgs0;
+  if ((int)blockIdx.y >= p.plan[1]) return;
+  const int4 chunk = chunk_at(p.plan, at, blockIdx.y);
+  const int C = which ? p.C[1] : p.C[0], R = p.R;
+  const uint16_t* rows = which ? p.rows[1] : p.rows[0];
+  const uint16_t* op = which ? p.op[1] : p.op[0];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int c0 = ((blockIdx.x - (which ? wgs0 : 0)) * 4 + wave) * 128 + l * 8, c = min(c0, C - 8);
+  const int r0 = blockIdx.z * (RB * 16);
+  const size_t lo = (size_t)R * at.padded;
+  const uint16_t* ops[RB];
+#pragma unroll
+  for (int q = 0; q < RB; ++q)
+    ops[q] = op + (size_t)min(r0 + q * 16 + l, R - 1) * at.padded + chunk.w + g * 8;
+  f32x4 acc[RB][8] = {};
+  for (int p0 = 0; p0 < chunk.z; p0 += 512) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 512; i += 256)
+      tokens[i] = p.plan[at.o_order + chunk.y + min(p0 + i, chunk.z - 1)];
+    __syncthreads();
+    const int n = min(512, chunk.z - p0);
+    for (int s = 0; s < n; s += 32) {
+      u32x4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = ld16(rows + (size_t)tokens[s + g * 8 + i] * C + c);
+      u32x4 a[RB][2];
+#pragma unroll
+      for (int q = 0; q < RB; ++q) {
+        a[q][0] = ld16(ops[q] + p0 + s);
+        a[q][1] = ld16(ops[q] + lo + p0 + s);
+      }
+      if (s + 32 > n) {  // tokens past the chunk's last one: zeros on both sides
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (s + g * 8 + i >= n) x[i] = u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u32x4 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int q = 0; q < RB; ++q) {
+          acc[q][j] = mfma_bf16(as_bf16x8(a[q][0]), as_bf16x8(f), acc[q][j]);
+          acc[q][j] = mfma_bf16(as_bf16x8(a[q][1]), as_bf16x8(f), acc[q][j]);
+        }
+      }
+    }
+  }
+  if (c0 >= C) return;
+  const int slot = p.plan[at.o_slot + chunk.x];
+#pragma unroll
+  for (int q = 0; q < RB; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + q * 16 + g * 4 + i;
+      if (r >= R) continue;
+      if (slot >= 0) {  // one of several chunks: added by lora_grad_sum_kernel
+        float* to = (which ? p.part[1] : p.part[0]) +
+                    ((size_t)(slot + blockIdx.y - p.plan[at.o_first + chunk.x]) * R + r) * C + c0;
+        *reinterpret_cast<f32x4*>(to) = f32x4{acc[q][0][i], acc[q][1][i], acc[q][2][i], acc[q][3][i]};
+        *reinterpret_cast<f32x4*>(to + 4) = f32x4{acc[q][4][i], acc[q][5][i], acc[q][6][i], acc[q][7][i]};
+      } else if (!which) {
+        st16(p.out[0] + ((size_t)chunk.x * R + r) * C + c0,
+             u32x4{pack_bf16x2(acc[q][0][i], acc[q][1][i]), pack_bf16x2(acc[q][2][i], acc[q][3][i]),
+                   pack_bf16x2(acc[q][4][i], acc[q][5][i]), pack_bf16x2(acc[q][6][i], acc[q][7][i])});
+      }
+    }
+  if (slot < 0 && which) {  // [N, R]: 4 consecutive values of r of a column
+#pragma unroll
+    for (int q = 0; q < RB; ++q)
+      if (r0 + q * 16 + g * 4 < R)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<u32x2*>(p.out[1] + ((size_t)chunk.x * C + c0 + j) * R + r0 + q * 16 + g * 4) =
+              u32x2{pack_bf16x2(acc[q][j][0], acc[q][j][1]), pack_bf16x2(acc[q][j][2], acc[q][j][3])};
+  }
+}
+
+// The sums of adapters with several chunks, in their order, and zeros for those without
+// tokens: 8 values a thread.
+__global__ __launch_bounds__(256) void lora_grad_sum_kernel(LoraGradArgs p) {
+  const LoraPlanLayout at(p.T, p.E);
+  const int e = blockIdx.y;
+  const int first = p.plan[at.o_first + e], n = p.plan[at.o_first + e + 1] - first;
+  if (n == 1) return;
+  const int slot = p.plan[at.o_slot + e], R = p.R;
+  int i = blockIdx.x * 256 + threadIdx.x;
+  const int n0 = R * (p.C[0] / 8), n1 = (R / 8) * p.C[1];
+  if (i >= n0 + n1) return;
+  const bool which = i >= n0;
+  if (which) i -= n0;
+  const int C = which ? p.C[1] : p.C[0];
+  float s[8] = {};
+  for (int j = 0; j < n; ++j) {
+    const float* from = (which ? p.part[1] : p.part[0]) + (size_t)(slot + j) * R * C;
+    if (which) {  // column i % C, rows 8 (i / C) ..
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] += from[(size_t)(i / C * 8 + q) * C + i % C];
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(from + (size_t)i * 8),
+                  b = *reinterpret_cast<const f32x4*>(from + (size_t)i * 8 + 4);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        s[q] += a[q];
+        s[4 + q] += b[q];
+      }
+    }
+  }
+  uint16_t* to = which ? p.out[1] + ((size_t)e * C + i % C) * R + i / C * 8 : p.out[0] + (size_t)e * R * C + (size_t)i * 8;
+  st16(to, u32x4{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])});
+}
+
+// Parts of a reduction over k: enough workgroups for the chip, at least 128 values of k for
+// each of a workgroup's waves.
+int parts_of(int tiles, int K) {
+  const int most = std::max(1, (K + 511) / 512);
+  return std::min({most, 8, std::max(1, 640 / tiles)});
+}
+
+template <typename F>
+void with_rank(int R, F f) {
+  if (R <= 16)
+    f(std::integral_constant<int, 1>{});
+  else if (R <= 32)
+    f(std::integral_constant<int, 2>{});
+  else if (R <= 64)
+    f(std::integral_constant<int, 4>{});
+  else
+    f(std::integral_constant<int, 8>{});
+}
+
+void into_rank(const uint16_t* x, const uint16_t* m, const int32_t* plan, int T, int E, int R, int K, float* part,
+               hipStream_t st) {
+  const int tiles = LoraPlanLayout(T, E).tiles;
+  with_rank(R, [&](auto rb) {
+    lora_in_kernel<decltype(rb)::value><<<dim3(tiles, parts_of(tiles, K)), 256, 0, st>>>(x, m, plan, T, E, R, K, part);
+  });
+}
+
+void out_of_rank(const float* part, int parts, const uint16_t* m, const float* scale, const int32_t* plan, int T,
+                 int E, int R, int N, const uint16_t* base, uint16_t* out, float* v, hipStream_t st) {
+  const int tiles = LoraPlanLayout(T, E).tiles;
+  // columns of a workgroup: the more, the less often the tile's parts are added
+  const int width = tiles * ((N + 1023) / 1024) >= 512 ? 1024 : tiles * ((N + 511) / 512) >= 512 ? 512 : 256;
+  with_rank(R, [&](auto rb) {
+    lora_out_kernel<decltype(rb)::value><<<dim3(tiles, (N + width - 1) / width), 256, 0, st>>>(
+        part, parts, m, scale, plan, T, E, R, N, width, base, out, v);
+  });
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Workspace of the backward pass
+struct LoraBwdSpace {
+  size_t at, bt, part, dv, dvt, vt, part_a, part_b, bytes;
+  LoraBwdSpace(int T, int K, int N, int R, int E) {
+    const LoraPlanLayout l(T, E);
+    size_t o = 0;
+    auto take = [&](size_t n) {
+      const size_t was = o;
+      o += up256(n);
+      return was;
+    };
+    at = take((size_t)E * R * K * 2);
+    bt = take((size_t)E * R * N * 2);
+    part = take((size_t)parts_of(l.tiles, N) * T * R * 4);
+    dv = take((size_t)T * R * 4);
+    dvt = take((size_t)l.padded * R * 4);
+    vt = take((size_t)l.padded * R * 4);
+    part_a = take((size_t)l.slots * R * K * 4);
+    part_b = take((size_t)l.slots * R * N * 4);
+    bytes = o;
+  }
+};
 
 }  // namespace
 
@@ -171,32 +590,43 @@ hipError_t launch_lora_plan(const int32_t* index, int T, int E, int32_t* plan, h
   return hipGetLastError();
 }
 
-size_t lora_workspace_bytes(int T, int K, int N, int R, int E) { return (size_t)T * R * sizeof(float); }
+size_t lora_workspace_bytes(int T, int K, int N, int R, int E) {
+  return (size_t)parts_of(LoraPlanLayout(T, E).tiles, K) * T * R * sizeof(float);
+}
 
 hipError_t launch_lora(const LoraArgs& p, hipStream_t st) {
-  const LoraPlanLayout at(p.T, p.E);
-  float* v = p.v ? p.v : p.part;
-  lora_in_kernel<<<dim3(at.tiles, p.R), 256, 0, st>>>(p.x, p.a, nullptr, p.plan, p.T, p.E, p.R, p.K, p.K, 1, v);
-  lora_out_kernel<<<dim3(at.tiles, (p.N + 255) / 256), 256, 0, st>>>(v, p.b, p.scale, p.plan, p.T, p.E, p.R,
-                                                                     p.N, p.R, 1, p.base, p.out);
+  into_rank(p.x, p.a, p.plan, p.T, p.E, p.R, p.K, p.part, st);
+  out_of_rank(p.part, parts_of(LoraPlanLayout(p.T, p.E).tiles, p.K), p.b, p.scale, p.plan, p.T, p.E, p.R, p.N, p.base,
+              p.out, p.v, st);
   return hipGetLastError();
 }
 
-size_t lora_bwd_workspace_bytes(int T, int K, int N, int R, int E) { return (size_t)T * R * sizeof(float); }
+size_t lora_bwd_workspace_bytes(int T, int K, int N, int R, int E) { return LoraBwdSpace(T, K, N, R, E).bytes; }
 
 hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
-  const LoraPlanLayout at(p.T, p.E);
-  float* dv = (float*)p.workspace;
-  lora_in_kernel<<<dim3(at.tiles, p.R), 256, 0, st>>>(p.dy, p.b, p.scale, p.plan, p.T, p.E, p.R, p.N, 1, p.R,
-                                                      dv);
-  if (p.dx)
-    lora_out_kernel<<<dim3(at.tiles, (p.K + 255) / 256), 256, 0, st>>>(dv, p.a, nullptr, p.plan, p.T, p.E, p.R,
-                                                                       p.K, 1, p.K, p.base, p.dx);
+  const LoraPlanLayout l(p.T, p.E);
+  const LoraBwdSpace w(p.T, p.K, p.N, p.R, p.E);
+  uint8_t* ws = (uint8_t*)p.workspace;
+  uint16_t *at = (uint16_t*)(ws + w.at), *bt = (uint16_t*)(ws + w.bt);
+  float *part = (float*)(ws + w.part), *dv = (float*)(ws + w.dv);
+  uint16_t *dvt = (uint16_t*)(ws + w.dvt), *vt = (uint16_t*)(ws + w.vt);
+  const int blocks = (p.R + 63) / 64 * ((p.K + 63) / 64 + (p.N + 63) / 64);
+  lora_transpose_kernel<<<dim3(blocks, p.E), 256, 0, st>>>(p.a, p.b, p.E, p.R, p.K, p.N, at, bt);
+  into_rank(p.dy, bt, p.plan, p.T, p.E, p.R, p.N, part, st);
+  lora_operands_kernel<<<dim3(l.chunks * (l.chunk / 64), p.da ? 2 : 1), 256, p.R * 66 * 4, st>>>(
+      part, parts_of(l.tiles, p.N), p.v, p.scale, p.plan, p.T, p.E, p.R, dv, p.da ? dvt : nullptr, vt);
+  if (p.dx) out_of_rank(dv, 1, at, nullptr, p.plan, p.T, p.E, p.R, p.K, p.base, p.dx, nullptr, st);
   if (p.da) {
-    lora_grad_kernel<<<dim3((p.K + 255) / 256, p.R, p.E), 256, 0, st>>>(dv, p.x, nullptr, p.plan, p.T, p.E, p.R,
-                                                                        p.K, p.K, 1, p.da);
-    lora_grad_kernel<<<dim3((p.N + 255) / 256, p.R, p.E), 256, 0, st>>>(p.v, p.dy, p.scale, p.plan, p.T, p.E,
-                                                                        p.R, p.N, 1, p.R, p.db);
+    const LoraGradArgs a{{dvt, vt}, {p.x, p.dy}, {p.da, p.db},
+                         {(float*)(ws + w.part_a), (float*)(ws + w.part_b)}, p.plan, p.T, p.E, p.R, {p.K, p.N}};
+    const int wgs = (p.K + 511) / 512 + (p.N + 511) / 512;
+    if (p.R <= 16)
+      lora_grad_kernel<1><<<dim3(wgs, l.chunks), 256, 0, st>>>(a);
+    else if (p.R <= 32)
+      lora_grad_kernel<2><<<dim3(wgs, l.chunks), 256, 0, st>>>(a);
+    else
+      lora_grad_kernel<4><<<dim3(wgs, l.chunks, (p.R + 63) / 64), 256, 0, st>>>(a);
+    lora_grad_sum_kernel<<<dim3((p.R * (p.K + p.N) / 8 + 255) / 256, p.E), 256, 0, st>>>(a);
   }
   return hipGetLastError();
 }

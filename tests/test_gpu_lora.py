@@ -156,16 +156,26 @@ def test_plan(T, E, how):
     up4 = lambda n: (n + 3) // 4 * 4
     order = plan[16:16 + T]
     assert np.array_equal(order, np.argsort(g, kind="stable"))
-    for at, limit, size, groups, n in ((16 + up4(T), T // 64 + min(E + 1, T), 64, E + 1, plan[0]),
-                                       (16 + up4(T) + 4 * (T // 64 + min(E + 1, T)), T // 512 + min(E, T), 512, E,
-                                        plan[1])):
-        want, first = [], 0
-        for e in range(groups):
-            c = int((g == e).sum())
-            want += [(e if e < E else -1, first + j, min(size, c - j), 0) for j in range(0, c, size)]
-            first += c
+    used = min(E, T)
+    tiles, chunks = 16 + up4(T), 16 + up4(T) + 4 * (T // 64 + min(E + 1, T))
+    padded = first = 0
+    want_tiles, want_chunks, firsts, slots = [], [], [], []
+    for e in range(E + 1):
+        c = int((g == e).sum())
+        want_tiles += [(e if e < E else -1, first + j, min(64, c - j), 0) for j in range(0, c, 64)]
+        if e < E:
+            firsts.append(len(want_chunks))
+            slots.append(sum(n for n in map(int, np.diff(firsts)) if n > 1) if c > 512 else -1)
+            want_chunks += [(e, first + j, min(512, c - j), padded + j) for j in range(0, c, 512)]
+            padded += (c + 31) // 32 * 32
+        first += c
+    for at, limit, n, want in ((tiles, T // 64 + min(E + 1, T), plan[0], want_tiles),
+                               (chunks, T // 512 + used, plan[1], want_chunks)):
         assert n == len(want) <= limit
         assert np.array_equal(plan[at:at + 4 * n].reshape(n, 4), np.array(want).reshape(n, 4))
+    at = chunks + 4 * (T // 512 + used)
+    assert plan[at:at + E + 1].tolist() == firsts + [len(want_chunks)]
+    assert plan[at + up4(E + 1):at + up4(E + 1) + E].tolist() == slots
 
 
 def test_rows_do_not_touch_each_other():
