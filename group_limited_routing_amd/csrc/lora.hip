@@ -5,6 +5,7 @@
 // the dense MLP and the experts.
 #include "common.h"
 #include "operators.h"
+#include "tile.h"
 #include "wave.h"
 
 #include <algorithm>
@@ -13,11 +14,12 @@ namespace beam {
 namespace {
 
 constexpr int kPlanWaves = 16;
+constexpr int kMaxParts = 8;  // of a reduction over k
 
 // One workgroup: counts of each wave's part of the tokens, offsets by a scan over
 // the adapters, then each wave places its part in order, so the order is stable.
 __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_t* __restrict__ index, int T,
-                                                                    int E, int32_t* __restrict__ plan) {
+                                                                    int E, int32_t* plan) {
   __shared__ int32_t part[kPlanWaves][kLoraMaxE + 1];
   __shared__ int32_t start[kLoraMaxE + 2], tile0[kLoraMaxE + 2], chunk0[kLoraMaxE + 2], padded0[kLoraMaxE + 2];
   const LoraPlanLayout at(T, E);
@@ -82,13 +84,13 @@ __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_
   for (int g = 0; g < G; ++g) {
     const int s = start[g], n = start[g + 1] - s, e = g < E ? g : -1;
     for (int j = tid; j * kLoraTile < n; j += 64 * kPlanWaves)
-      tiles[tile0[g] + j] = make_int4(e, s + j * kLoraTile, min(kLoraTile, n - j * kLoraTile), 0);
+      tiles[tile0[g] + j] = make_int4(e, s + j * kLoraTile, min(kLoraTile, n - j * kLoraTile), padded0[g] + j * kLoraTile);
     if (g < E)
       for (int j = tid; j * chunk < n; j += 64 * kPlanWaves)
         chunks[chunk0[g] + j] = make_int4(e, s + j * chunk, min(chunk, n - j * chunk), padded0[g] + j * chunk);
   }
   __syncthreads();
-  int32_t* order = plan + at.o_order;
+  int32_t *order = plan + at.o_order, *tokens = plan + at.o_tokens;
   for (int t = t0; t < t1; t += 64) {
     const bool live = t + lane < t1;
     const int g = live ? group(t + lane) : -1;
@@ -99,9 +101,19 @@ __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_
       int base = 0;
       if (lane == lead) base = atomicAdd(&part[wave][lg], __popcll(same));
       base = __shfl(base, lead);
-      if (live && g == lg) order[base + __popcll(same & ((1ull << lane) - 1))] = t + lane;
+      if (live && g == lg) {
+        const int pos = base + __popcll(same & ((1ull << lane) - 1));
+        order[pos] = t + lane;
+        tokens[(size_t)tile0[lg] * kLoraTile + pos - start[lg]] = t + lane;
+      }
       left &= ~same;
     }
+  }
+  __syncthreads();
+  for (int g = tid; g < G; g += 64 * kPlanWaves) {
+    const int n = start[g + 1] - start[g];
+    int32_t* end = tokens + (size_t)tile0[g] * kLoraTile + n;
+    for (int i = n; i % kLoraTile != 0; ++i) *end++ = tokens[(size_t)tile0[g] * kLoraTile + n - 1];
   }
 }
 
@@ -110,6 +122,27 @@ __device__ __forceinline__ int4 tile_at(const int32_t* plan, const LoraPlanLayou
 }
 __device__ __forceinline__ int4 chunk_at(const int32_t* plan, const LoraPlanLayout& at, int i) {
   return reinterpret_cast<const int4*>(plan + at.o_chunks)[i];
+}
+
+// A launch of `parts` workgroups for each of `tiles` tiles, dealt so that a tile's are on one
+// XCD (workgroups go to the 8 XCDs in turn) and run one after the other: each XCD then
+// works on rows of its own, whose pages its address translation holds. (With a tile's parts on
+// several XCDs, 8192 x 5120 in 2 parts took 36 us, so 23.)
+int grid_of(int tiles, int parts) { return (tiles + 7) / 8 * 8 * parts; }
+__device__ __forceinline__ void place(int parts, int& tile, int& part) {
+  const int q = blockIdx.x >> 3;
+  part = q % parts;
+  tile = q / parts * 8 + (blockIdx.x & 7);
+}
+
+// The tokens of a tile that are this lane's MFMA columns. What a tile's work
+// begins with, its record and its tokens, stands at places that the workgroup's number
+// gives, and is read at once: each read after another costs a microsecond.
+__device__ __forceinline__ void tile_tokens(const int32_t* plan, const LoraPlanLayout& at, int tile,
+                                            int (&tokens)[4]) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    tokens[b] = plan[at.o_tokens + (size_t)tile * kLoraTile + b * 16 + (threadIdx.x & 15)];
 }
 
 // v as the sum of two bf16 values, 16 significant bits; beyond the largest bf16 number,
@@ -126,54 +159,62 @@ __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
 // sums are added through LDS. MFMA rows are r, columns tokens; both operands go from
 // memory into registers, 64 bytes of a row at a time.
 template <int RB, int TB>
-__device__ __forceinline__ void rank_sums(const uint16_t* x, const uint16_t* m, const int32_t* order, int count,
-                                          int R, int K, int first, int step, f32x4 (&acc)[TB][RB]) {
+__device__ __forceinline__ void rank_sums(const uint16_t* x, const uint16_t* m, const int (&tokens)[4], int R, int K, int first, int step, f32x4 (&acc)[TB][RB]) {
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const uint16_t* xr[TB];
   const uint16_t* mr[RB];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) xr[b] = x + (size_t)order[min(b * 16 + l, count - 1)] * K + g * 8;
+  for (int b = 0; b < TB; ++b) xr[b] = x + (size_t)tokens[b] * K + g * 8;
 #pragma unroll
   for (int b = 0; b < RB; ++b) mr[b] = m + (size_t)min(b * 16 + l, R - 1) * K + g * 8;
-  for (int k0 = first * 128; k0 < K; k0 += step * 128) {
-    u32x4 xf[4][TB], mf[4][RB];
+  constexpr int S = TB * RB > 8 ? 2 : 4;  // steps of 32 whose loads go out together
+  auto group = [&](int k0, auto end) {
+    u32x4 xf[S][TB], mf[S][RB];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < S; ++s) {
       const int k = k0 + s * 32;
-      const bool in = k + g * 8 < K;  // K is a multiple of 8
+      // past the end (K is a multiple of 8) zeros, from an address: a load that some lanes
+      // leave out would be a branch of its own
+      const bool in = !decltype(end)::value || k + g * 8 < K;
 #pragma unroll
-      for (int b = 0; b < TB; ++b) xf[s][b] = in ? ld16(xr[b] + k) : u32x4{0, 0, 0, 0};
+      for (int b = 0; b < TB; ++b) xf[s][b] = ld16(in ? (const void*)(xr[b] + k) : (const void*)kZeros);
 #pragma unroll
-      for (int b = 0; b < RB; ++b) mf[s][b] = in ? ld16(mr[b] + k) : u32x4{0, 0, 0, 0};
+      for (int b = 0; b < RB; ++b) mf[s][b] = ld16(in ? (const void*)(mr[b] + k) : (const void*)kZeros);
     }
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
       for (int b = 0; b < TB; ++b)
 #pragma unroll
         for (int q = 0; q < RB; ++q)
           acc[b][q] = mfma_bf16(as_bf16x8(mf[s][q]), as_bf16x8(xf[s][b]), acc[b][q]);
-  }
+  };
+  int k0 = first * S * 32;
+  for (; k0 + S * 32 <= K; k0 += step * S * 32) group(k0, std::false_type{});
+  if (k0 < K) group(k0, std::true_type{});
 }
 
 template <int RB>
-__global__ __launch_bounds__(256) void lora_in_kernel(const uint16_t* __restrict__ x,
+__global__ __launch_bounds__(256, RB <= 2 ? 4 : RB <= 4 ? 2 : 1) void lora_in_kernel(const uint16_t* __restrict__ x,
                                                       const uint16_t* __restrict__ m,
-                                                      const int32_t* __restrict__ plan, int T, int E, int R,
-                                                      int K, float* __restrict__ part) {
+                                                      const int32_t* __restrict__ plan, int parts, int T,
+                                                      int E, int R, int K, float* __restrict__ part) {
   __shared__ f32x4 sums[4][4][RB][64];
   const LoraPlanLayout at(T, E);
-  if ((int)blockIdx.x >= plan[0]) return;
-  const int4 tile = tile_at(plan, at, blockIdx.x);
-  if (tile.x < 0) return;  // no adapter: nothing reads these sums
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int32_t* order = plan + at.o_order + tile.y;
+  int number, mine;
+  place(parts, number, mine);
+  if (number >= at.tiles) return;
+  const int4 tile = tile_at(plan, at, number);
+  int tokens[4];
+  tile_tokens(plan, at, number, tokens);
+  if (number >= plan[0] || tile.x < 0) return;  // no adapter: nothing reads these sums
   const uint16_t* me = m + (size_t)tile.x * R * K;
-  const int first = blockIdx.y * 4 + wave, step = gridDim.y * 4, tb = (tile.z + 15) / 16;
+  const int step = parts * 4, first = mine * 4 + wave, tb = (tile.z + 15) / 16;
   auto run = [&](auto n) {
     constexpr int TB = decltype(n)::value;
     f32x4 acc[TB][RB] = {};
-    rank_sums<RB, TB>(x, me, order, tile.z, R, K, first, step, acc);
+    rank_sums<RB, TB>(x, me, tokens, R, K, first, step, acc);
 #pragma unroll
     for (int b = 0; b < TB; ++b)
 #pragma unroll
@@ -193,53 +234,73 @@ __global__ __launch_bounds__(256) void lora_in_kernel(const uint16_t* __restrict
 #pragma unroll
     for (int w = 1; w < 4; ++w) s += sums[w][b][q][lane];
     if (t < tile.z && r < R)
-      *reinterpret_cast<f32x4*>(part + ((size_t)blockIdx.y * T + tile.y + t) * R + r) = s;
+      *reinterpret_cast<f32x4*>(part + ((size_t)mine * T + tile.y + t) * R + r) = s;
   }
 }
 
 // ------------------------------------------------------------------ out of the rank
 // out[t, n] = base[t, n] + sum over r of f v[t, r] m[e][n, r], v the sum of `parts` rows in
 // their order. MFMA rows are n, columns tokens, and the reduction runs over the first
-// and then the second parts of f v. Fragment j of a wave's 64 columns takes rows n =
-// 16 (i / 4) + 4 j + i % 4, so that a lane ends with 16 consecutive columns of a token.
-template <int RB>
-__global__ __launch_bounds__(256) void lora_out_kernel(const float* __restrict__ part, int parts,
-                                                       const uint16_t* __restrict__ m,
-                                                       const float* __restrict__ scale,
-                                                       const int32_t* __restrict__ plan, int T, int E, int R,
-                                                       int N, int width, const uint16_t* base, uint16_t* out,
-                                                       float* __restrict__ v) {
-  constexpr int PITCH = RB * 32 + 8;  // values of a token in LDS: hi, lo, padding
-  __shared__ __attribute__((aligned(16))) uint16_t vs[64 * PITCH];
-  __shared__ int32_t tokens[64];
-  const LoraPlanLayout at(T, E);
-  if ((int)blockIdx.x >= plan[0]) return;
-  const int4 tile = tile_at(plan, at, blockIdx.x);
+// and then the second parts of f v. Fragments (i, j) of a wave's 64 columns take rows n =
+// 32 i + 8 (m / 4) + 4 j + m % 4, so that a lane ends with two runs of 8 columns of a token,
+// and four lanes have 64 bytes of a row.
+struct LoraOutArgs {
+  const float* part;     // [parts, T, R]
+  const uint16_t* m;     // [E, N, R]
+  const float* scale;    // [E] or null
+  const int32_t* plan;
+  const uint16_t* base;  // [T, N] or null
+  uint16_t* out;         // [T, N]
+  float* v;              // [T, R] or null
+  int parts, T, E, R, N, width;
+};
+
+template <int RB, int TB, bool BASE>
+__device__ __forceinline__ void rank_out(const LoraOutArgs& p, const int4& tile, const int (&tokens)[4],
+                                         const int32_t* all_tokens, int n0, uint16_t* vs) {
+  constexpr int PITCH = RB * 32 + 8;  // values of a token in LDS: hi, lo, zeros, padding
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, l = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.y * width, n1 = min(N, n0 + width);
-  if (tid < 64) tokens[tid] = plan[at.o_order + tile.y + min(tid, tile.z - 1)];
-  const bool live = tile.x >= 0;
-  if (!live) {  // these keep their base
-    __syncthreads();
-    if (v && blockIdx.y == 0)
-      for (int i = tid; i < tile.z * R; i += 256) v[(size_t)tokens[i / R] * R + i % R] = 0.f;
-    if (base == out) return;
-    const int chunks = (n1 - n0) / 8;
-    for (int i = tid; i < tile.z * chunks; i += 256) {
-      const size_t o = (size_t)tokens[i / chunks] * N + n0 + i % chunks * 8;
-      st16(out + o, base ? ld16(base + o) : u32x4{0, 0, 0, 0});
+  const int R = p.R, N = p.N, count = tile.z, n1 = min(N, n0 + p.width);
+  const uint16_t* m = p.m + (size_t)tile.x * R * N;
+  size_t row[TB];
+#pragma unroll
+  for (int b = 0; b < TB; ++b) row[b] = (size_t)tokens[b] * N;
+  // Every load is made, of what is there: columns past the end and tokens past the tile's
+  // last one repeat others and are not stored. The next columns' loads go out before the
+  // stores, so that waiting for them is not waiting for the stores.
+  u32x4 mf[RB][2][2], d[TB][2];
+  auto load = [&](int nb) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (BASE)
+#pragma unroll
+        for (int b = 0; b < TB; ++b) d[b][i] = ld16(p.base + row[b] + min(nb + 32 * i + 8 * g, N - 8));
+#pragma unroll
+      for (int s = 0; s < RB; ++s) {
+        const int kk = s * 32 + g * 8, r = kk < R ? kk : kk - R;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint16_t* from = m + (size_t)min(nb + 32 * i + 8 * (l / 4) + 4 * j + l % 4, N - 1) * R + r;
+          mf[s][i][j] = ld16(kk < 2 * R ? (const void*)from : (const void*)kZeros);
+        }
+      }
     }
-    return;
-  }
-  const float f = scale ? scale[tile.x] : 1.f;
+  };
+  int nb = n0 + wave * 64;
+  load(min(nb, N - 8));
+  const float f = p.scale ? p.scale[tile.x] : 1.f;
   const int r4 = R / 4;
-  if (v && blockIdx.y == 0) __syncthreads();  // tokens
-  for (int i = tid; i < tile.z * r4; i += 256) {
+  for (int i = tid; i < count * r4; i += 256) {
     const int t = i / r4, r = i % r4 * 4;
-    f32x4 s{};
-    for (int p = 0; p < parts; ++p)
-      s += *reinterpret_cast<const f32x4*>(part + ((size_t)p * T + tile.y + t) * R + r);
-    if (v && blockIdx.y == 0) *reinterpret_cast<f32x4*>(v + (size_t)tokens[t] * R + r) = s;
+    const float* from = p.part + (size_t)(tile.y + t) * R + r;
+    f32x4 w[kMaxParts], s{};
+#pragma unroll
+    for (int q = 0; q < kMaxParts; ++q)
+      w[q] = *reinterpret_cast<const f32x4*>(from + (size_t)min(q, p.parts - 1) * p.T * R);
+#pragma unroll
+    for (int q = 0; q < kMaxParts; ++q)
+      if (q < p.parts) s += w[q];
+    if (p.v && n0 == 0) *reinterpret_cast<f32x4*>(p.v + (size_t)all_tokens[t] * R + r) = s;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t hi, lo;
@@ -248,54 +309,84 @@ __global__ __launch_bounds__(256) void lora_out_kernel(const float* __restrict__
       vs[t * PITCH + R + r + q] = (uint16_t)lo;
     }
   }
+  const int rest = RB * 32 - 2 * R;  // of a token's row
+  for (int i = tid; i < count * rest; i += 256) vs[i / rest * PITCH + 2 * R + i % rest] = 0;
   __syncthreads();
-  const uint16_t* me = m + (size_t)tile.x * R * N;
-  const int steps = (2 * R + 31) / 32, tb = (tile.z + 15) / 16;
-  for (int nb = n0 + wave * 64; nb < n1; nb += 256) {
-    f32x4 acc[4][4] = {};
+  for (; nb < n1; nb += 256) {
+    u32x4 w[TB][2];
 #pragma unroll
-    for (int s = 0; s < RB; ++s) {  // steps <= RB
-      if (s >= steps) break;
-      const int kk = s * 32 + g * 8;
-      const bool in = kk < 2 * R;
-      const int r = kk < R ? kk : kk - R;
-      u32x4 mf[4];
+    for (int b = 0; b < TB; ++b) {
+      f32x4 acc[2][2] = {};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = min(nb + 16 * (l / 4) + 4 * j + l % 4, N - 1);
-        mf[j] = in ? ld16(me + (size_t)n * R + r) : u32x4{0, 0, 0, 0};
+      for (int s = 0; s < RB; ++s) {  // behind the 2 R values of a token its row of vs holds zeros
+        const u32x4 vf = ld16(vs + min(b * 16 + l, count - 1) * PITCH + s * 32 + g * 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(as_bf16x8(mf[s][i][j]), as_bf16x8(vf), acc[i][j]);
       }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        if (b >= tb) break;
-        // tokens past the tile's last one repeat it, and are not stored
-        const u32x4 vf = in ? ld16(vs + min(b * 16 + l, tile.z - 1) * PITCH + kk) : u32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[b][j] = mfma_bf16(as_bf16x8(mf[j]), as_bf16x8(vf), acc[b][j]);
-      }
-    }
-    const int n = nb + 16 * g;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int t = b * 16 + l;
-      if (t >= tile.z) continue;
-      const size_t o = (size_t)tokens[t] * N + n;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (n + 8 * half >= N) continue;
-        u32x4 d{0, 0, 0, 0};
-        if (base) d = ld16(base + o + 8 * half);
-        u32x4 w;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int j = 2 * half + q / 2, e = q % 2 * 2;
-          w[q] = pack_bf16x2(acc[b][j][e] + __uint_as_float(d[q] << 16),
-                             acc[b][j][e + 1] + __uint_as_float(d[q] & 0xffff0000u));
+          float lo = acc[i][q / 2][q % 2 * 2], hi = acc[i][q / 2][q % 2 * 2 + 1];
+          if constexpr (BASE) {
+            lo += __uint_as_float(d[b][i][q] << 16);
+            hi += __uint_as_float(d[b][i][q] & 0xffff0000u);
+          }
+          w[b][i][q] = pack_bf16x2(lo, hi);
         }
-        st16(out + o + 8 * half, w);
-      }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (nb + 256 < n1) load(nb + 256);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = nb + 32 * i + 8 * g;
+        if (b * 16 + l < count && n < N) st16(p.out + row[b] + n, w[b][i]);
+      }
   }
+}
+
+template <int RB>
+__global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_out_kernel(LoraOutArgs p) {
+  __shared__ __attribute__((aligned(16))) uint16_t vs[64 * (RB * 32 + 8)];
+  const LoraPlanLayout at(p.T, p.E);
+  int number, n0;
+  place((p.N + p.width - 1) / p.width, number, n0);
+  n0 *= p.width;
+  if (number >= at.tiles) return;
+  const int4 tile = tile_at(p.plan, at, number);
+  int tokens[4];
+  tile_tokens(p.plan, at, number, tokens);
+  if (number >= p.plan[0]) return;
+  const int32_t* all = p.plan + at.o_tokens + (size_t)number * kLoraTile;
+  if (tile.x < 0) {  // these keep their base
+    if (p.v && n0 == 0)
+      for (int i = threadIdx.x; i < tile.z * p.R; i += 256) p.v[(size_t)all[i / p.R] * p.R + i % p.R] = 0.f;
+    if (p.base == p.out) return;
+    const int chunks = (min(p.N, n0 + p.width) - n0) / 8;
+    for (int i = threadIdx.x; i < tile.z * chunks; i += 256) {
+      const size_t o = (size_t)all[i / chunks] * p.N + n0 + i % chunks * 8;
+      st16(p.out + o, p.base ? ld16(p.base + o) : u32x4{0, 0, 0, 0});
+    }
+    return;
+  }
+  auto run = [&](auto tb) {
+    constexpr int TB = decltype(tb)::value;
+    if (p.base)
+      rank_out<RB, TB, true>(p, tile, tokens, all, n0, vs);
+    else
+      rank_out<RB, TB, false>(p, tile, tokens, all, n0, vs);
+  };
+  if (tile.z <= 16)
+    run(std::integral_constant<int, 1>{});
+  else if (tile.z <= 32)
+    run(std::integral_constant<int, 2>{});
+  else
+    run(std::integral_constant<int, 4>{});
 }
 
 // ------------------------------------------------------------------ gradients
@@ -333,29 +424,32 @@ __global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __r
 
 // dv = f times the sum of its parts, in the tokens' order, and, for the adapters'
 // gradients, dv and f v as operands: two bf16 parts, a row of padded positions for each
-// r. A workgroup per 64 positions of a chunk (those past its last token: zeros).
+// r. A workgroup per tile (positions past its last token: zeros).
 __global__ __launch_bounds__(256) void lora_operands_kernel(const float* part, int parts, const float* v,
                                                             const float* scale, const int32_t* __restrict__ plan,
                                                             int T, int E, int R, float* dv, uint16_t* dvt,
                                                             uint16_t* vt) {
   extern __shared__ uint32_t pairs[];  // [R][66]: hi in the low half, lo
   const LoraPlanLayout at(T, E);
-  const int per = at.chunk / 64, c = blockIdx.x / per;
-  if (c >= plan[1]) return;
-  const int4 chunk = chunk_at(plan, at, c);
-  const int p0 = blockIdx.x % per * 64;
-  if (p0 >= chunk.z) return;
-  const int count = min(64, chunk.z - p0), padded = (count + 31) & ~31;
-  const float f = scale ? scale[chunk.x] : 1.f;
+  if ((int)blockIdx.x >= plan[0]) return;
+  const int4 tile = tile_at(plan, at, blockIdx.x);
+  if (tile.x < 0) return;
+  const int count = tile.z, padded = (count + 31) & ~31;
+  const float f = scale ? scale[tile.x] : 1.f;
   const int which = blockIdx.y;  // 0: dv, 1: v
   for (int i = threadIdx.x; i < 64 * (R / 4); i += 256) {
     const int t = i / (R / 4), r = i % (R / 4) * 4;
     f32x4 s{};
     if (t < count) {
-      const int pos = chunk.y + p0 + t;
+      const int pos = tile.y + t;
       if (which == 0) {
-        for (int p = 0; p < parts; ++p)
-          s += *reinterpret_cast<const f32x4*>(part + ((size_t)p * T + pos) * R + r);
+        f32x4 w[kMaxParts];
+#pragma unroll
+        for (int p = 0; p < kMaxParts; ++p)
+          w[p] = *reinterpret_cast<const f32x4*>(part + ((size_t)min(p, parts - 1) * T + pos) * R + r);
+#pragma unroll
+        for (int p = 0; p < kMaxParts; ++p)
+          if (p < parts) s += w[p];
         s *= f;
         *reinterpret_cast<f32x4*>(dv + (size_t)pos * R + r) = s;
       } else {
@@ -382,7 +476,7 @@ __global__ __launch_bounds__(256) void lora_operands_kernel(const float* part, i
       hi[q] = (x & 0xffffu) | y << 16;
       lo[q] = x >> 16 | (y & 0xffff0000u);
     }
-    uint16_t* row = to + (size_t)r * at.padded + chunk.w + p0 + t;
+    uint16_t* row = to + (size_t)r * at.padded + tile.w + t;
     st16(row, hi);
     st16(row + (size_t)R * at.padded, lo);
   }
@@ -397,24 +491,28 @@ struct LoraGradArgs {
   int T, E, R, C[2];
 };
 
-// sum over a chunk's tokens of op[t, r] rows[t, c] for 64 values of r and 128 columns a
-// wave. MFMA rows are r, columns c, the reduction runs over 32 tokens. Lane (l, g) loads
-// columns 8 l .. + 7 of tokens 8 g .. + 7, whole 256-byte runs of a row, and turns them in
-// its registers into fragment j of column 8 l + j, whose reduction values are its 8 tokens.
+// sum over a chunk's tokens of op[t, r] rows[t, c] for 16 RB values of r and 128 columns:
+// the four waves take 32 tokens in turn, and their sums are added through LDS. MFMA rows
+// are r, columns c, the reduction runs over 32 tokens. Lane (l, g) loads columns 8 l .. + 7
+// of tokens 8 g .. + 7, whole 256-byte runs of a row, and turns them in its registers into
+// fragment j of column 8 l + j, whose reduction values are its 8 tokens.
 template <int RB>
-__global__ __launch_bounds__(256) void lora_grad_kernel(LoraGradArgs p) {
+__global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
   __shared__ __attribute__((aligned(16))) int32_t tokens[512];
+  __shared__ f32x4 sums[2][RB][8][64];
   const LoraPlanLayout at(p.T, p.E);
-  const int wgs0 = (p.C[0] + 511) / 512;
-  const int which = (int)blockIdx.x >= wgs0;
-  if ((int)blockIdx.y >= p.plan[1]) return;
-  const int4 chunk = chunk_at(p.plan, at, blockIdx.y);
+  const int wgs0 = (p.C[0] + 127) / 128;
+  int number, block;
+  place(wgs0 + (p.C[1] + 127) / 128, number, block);
+  const int which = block >= wgs0;
+  if (number >= at.chunks || number >= p.plan[1]) return;
+  const int4 chunk = chunk_at(p.plan, at, number);
   const int C = which ? p.C[1] : p.C[0], R = p.R;
   const uint16_t* rows = which ? p.rows[1] : p.rows[0];
   const uint16_t* op = which ? p.op[1] : p.op[0];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  const int c0 = ((blockIdx.x - (which ? wgs0 : 0)) * 4 + wave) * 128 + l * 8, c = min(c0, C - 8);
-  const int r0 = blockIdx.z * (RB * 16);
+  const int c0 = (block - (which ? wgs0 : 0)) * 128 + l * 8, c = min(c0, C - 8);
+  const int r0 = blockIdx.y * (RB * 16);
   const size_t lo = (size_t)R * at.padded;
   const uint16_t* ops[RB];
 #pragma unroll
@@ -427,16 +525,22 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(LoraGradArgs p) {
       tokens[i] = p.plan[at.o_order + chunk.y + min(p0 + i, chunk.z - 1)];
     __syncthreads();
     const int n = min(512, chunk.z - p0);
-    for (int s = 0; s < n; s += 32) {
-      u32x4 x[8];
+    u32x4 ahead[8];  // the wave's next rows are in flight while these are multiplied
+    auto load = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = ld16(rows + (size_t)tokens[s + g * 8 + i] * C + c);
-      u32x4 a[RB][2];
+      for (int i = 0; i < 8; ++i) ahead[i] = ld16(rows + (size_t)tokens[s + g * 8 + i] * C + c);
+    };
+    if (wave * 32 < n) load(wave * 32);
+    for (int s = wave * 32; s < n; s += 128) {
+      u32x4 x[8], a[RB][2];
 #pragma unroll
       for (int q = 0; q < RB; ++q) {
         a[q][0] = ld16(ops[q] + p0 + s);
         a[q][1] = ld16(ops[q] + lo + p0 + s);
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = ahead[i];
+      if (s + 128 < n) load(s + 128);
       if (s + 32 > n) {  // tokens past the chunk's last one: zeros on both sides
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -456,6 +560,23 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(LoraGradArgs p) {
       }
     }
   }
+  // waves 2 and 3 onto 0 and 1, then 1 onto 0
+#pragma unroll
+  for (int half = 2; half >= 1; half /= 2) {
+    __syncthreads();
+    if (wave >= half && wave < 2 * half)
+#pragma unroll
+      for (int q = 0; q < RB; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[wave - half][q][j][lane] = acc[q][j];
+    __syncthreads();
+    if (wave < half)
+#pragma unroll
+      for (int q = 0; q < RB; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[q][j] += sums[wave][q][j][lane];
+  }
+  if (wave > 0) return;
   if (c0 >= C) return;
   const int slot = p.plan[at.o_slot + chunk.x];
 #pragma unroll
@@ -466,7 +587,7 @@ __global__ __launch_bounds__(256) void lora_grad_kernel(LoraGradArgs p) {
       if (r >= R) continue;
       if (slot >= 0) {  // one of several chunks: added by lora_grad_sum_kernel
         float* to = (which ? p.part[1] : p.part[0]) +
-                    ((size_t)(slot + blockIdx.y - p.plan[at.o_first + chunk.x]) * R + r) * C + c0;
+                    ((size_t)(slot + number - p.plan[at.o_first + chunk.x]) * R + r) * C + c0;
         *reinterpret_cast<f32x4*>(to) = f32x4{acc[q][0][i], acc[q][1][i], acc[q][2][i], acc[q][3][i]};
         *reinterpret_cast<f32x4*>(to + 4) = f32x4{acc[q][4][i], acc[q][5][i], acc[q][6][i], acc[q][7][i]};
       } else if (!which) {
@@ -520,11 +641,12 @@ __global__ __launch_bounds__(256) void lora_grad_sum_kernel(LoraGradArgs p) {
   st16(to, u32x4{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7])});
 }
 
-// Parts of a reduction over k: enough workgroups for the chip, at least 128 values of k for
-// each of a workgroup's waves.
+// Parts of a reduction over k: a power of two (5 parts of 8192 x 5120 took 25 us, 4 took
+// 22), as long as the chip holds all workgroups at once and every wave has 128 values of k.
 int parts_of(int tiles, int K) {
-  const int most = std::max(1, (K + 511) / 512);
-  return std::min({most, 8, std::max(1, 640 / tiles)});
+  int p = 1;
+  while (2 * p <= kMaxParts && 2 * p * tiles <= 700 && 2 * p * 512 <= K + 511) p *= 2;
+  return p;
 }
 
 template <typename F>
@@ -543,18 +665,18 @@ void into_rank(const uint16_t* x, const uint16_t* m, const int32_t* plan, int T,
                hipStream_t st) {
   const int tiles = LoraPlanLayout(T, E).tiles;
   with_rank(R, [&](auto rb) {
-    lora_in_kernel<decltype(rb)::value><<<dim3(tiles, parts_of(tiles, K)), 256, 0, st>>>(x, m, plan, T, E, R, K, part);
+    const int parts = parts_of(tiles, K);
+    lora_in_kernel<decltype(rb)::value><<<grid_of(tiles, parts), 256, 0, st>>>(x, m, plan, parts, T, E, R, K, part);
   });
 }
 
-void out_of_rank(const float* part, int parts, const uint16_t* m, const float* scale, const int32_t* plan, int T,
-                 int E, int R, int N, const uint16_t* base, uint16_t* out, float* v, hipStream_t st) {
-  const int tiles = LoraPlanLayout(T, E).tiles;
+void out_of_rank(LoraOutArgs a, hipStream_t st) {
+  const int tiles = LoraPlanLayout(a.T, a.E).tiles;
   // columns of a workgroup: the more, the less often the tile's parts are added
-  const int width = tiles * ((N + 1023) / 1024) >= 512 ? 1024 : tiles * ((N + 511) / 512) >= 512 ? 512 : 256;
-  with_rank(R, [&](auto rb) {
-    lora_out_kernel<decltype(rb)::value><<<dim3(tiles, (N + width - 1) / width), 256, 0, st>>>(
-        part, parts, m, scale, plan, T, E, R, N, width, base, out, v);
+  a.width = 256;
+  while (a.width < 1024 && tiles * ((a.N + 2 * a.width - 1) / (2 * a.width)) >= 1100) a.width *= 2;
+  with_rank(a.R, [&](auto rb) {
+    lora_out_kernel<decltype(rb)::value><<<grid_of(tiles, (a.N + a.width - 1) / a.width), 256, 0, st>>>(a);
   });
 }
 
@@ -596,8 +718,9 @@ size_t lora_workspace_bytes(int T, int K, int N, int R, int E) {
 
 hipError_t launch_lora(const LoraArgs& p, hipStream_t st) {
   into_rank(p.x, p.a, p.plan, p.T, p.E, p.R, p.K, p.part, st);
-  out_of_rank(p.part, parts_of(LoraPlanLayout(p.T, p.E).tiles, p.K), p.b, p.scale, p.plan, p.T, p.E, p.R, p.N, p.base,
-              p.out, p.v, st);
+  out_of_rank({p.part, p.b, p.scale, p.plan, p.base, p.out, p.v, parts_of(LoraPlanLayout(p.T, p.E).tiles, p.K), p.T, p.E,
+               p.R, p.N, 0},
+              st);
   return hipGetLastError();
 }
 
@@ -613,19 +736,19 @@ hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
   const int blocks = (p.R + 63) / 64 * ((p.K + 63) / 64 + (p.N + 63) / 64);
   lora_transpose_kernel<<<dim3(blocks, p.E), 256, 0, st>>>(p.a, p.b, p.E, p.R, p.K, p.N, at, bt);
   into_rank(p.dy, bt, p.plan, p.T, p.E, p.R, p.N, part, st);
-  lora_operands_kernel<<<dim3(l.chunks * (l.chunk / 64), p.da ? 2 : 1), 256, p.R * 66 * 4, st>>>(
+  lora_operands_kernel<<<dim3(l.tiles, p.da ? 2 : 1), 256, p.R * 66 * 4, st>>>(
       part, parts_of(l.tiles, p.N), p.v, p.scale, p.plan, p.T, p.E, p.R, dv, p.da ? dvt : nullptr, vt);
-  if (p.dx) out_of_rank(dv, 1, at, nullptr, p.plan, p.T, p.E, p.R, p.K, p.base, p.dx, nullptr, st);
+  if (p.dx) out_of_rank({dv, at, nullptr, p.plan, p.base, p.dx, nullptr, 1, p.T, p.E, p.R, p.K, 0}, st);
   if (p.da) {
     const LoraGradArgs a{{dvt, vt}, {p.x, p.dy}, {p.da, p.db},
                          {(float*)(ws + w.part_a), (float*)(ws + w.part_b)}, p.plan, p.T, p.E, p.R, {p.K, p.N}};
-    const int wgs = (p.K + 511) / 512 + (p.N + 511) / 512;
+    const int wgs = (p.K + 127) / 128 + (p.N + 127) / 128;
     if (p.R <= 16)
-      lora_grad_kernel<1><<<dim3(wgs, l.chunks), 256, 0, st>>>(a);
+      lora_grad_kernel<1><<<grid_of(l.chunks, wgs), 256, 0, st>>>(a);
     else if (p.R <= 32)
-      lora_grad_kernel<2><<<dim3(wgs, l.chunks), 256, 0, st>>>(a);
+      lora_grad_kernel<2><<<grid_of(l.chunks, wgs), 256, 0, st>>>(a);
     else
-      lora_grad_kernel<4><<<dim3(wgs, l.chunks, (p.R + 63) / 64), 256, 0, st>>>(a);
+      lora_grad_kernel<4><<<dim3(grid_of(l.chunks, wgs), (p.R + 63) / 64), 256, 0, st>>>(a);
     lora_grad_sum_kernel<<<dim3((p.R * (p.K + p.N) / 8 + 255) / 256, p.E), 256, 0, st>>>(a);
   }
   return hipGetLastError();

@@ -137,22 +137,23 @@ constexpr int kLoraMaxE = 1024;
 // of the adapters, into longer chunks.
 constexpr int kLoraTile = 64;
 struct LoraPlanLayout {
-  int chunk;          // tokens of a chunk: at most 64 chunks of one adapter's tokens
+  int chunk;          // tokens of a chunk: at most 64 chunks of one adapter's tokens, or 1024
   int tiles, chunks;  // at most
   int slots;          // chunks, at most, of adapters that have more than one
   int padded;         // tokens, at most, with every adapter's rounded up to 32
-  size_t o_order, o_tiles, o_chunks, o_first, o_slot, words;
+  size_t o_order, o_tiles, o_tokens, o_chunks, o_first, o_slot, words;
   __host__ __device__ LoraPlanLayout(int T, int E) {
     const int used = E < T ? E : T;
-    chunk = T <= 32768 ? 512 : (T / 64 + 511) & ~511;
+    chunk = T <= 64 * 1024 ? 1024 : (T / 64 + 511) & ~511;
     tiles = T / kLoraTile + (E + 1 < T ? E + 1 : T);
     chunks = T / chunk + used;
     slots = 2 * (T / chunk);  // n > chunk tokens make at most 2 n / chunk chunks
     padded = (T + 31 * used + 31) & ~31;
     auto up4 = [](size_t n) { return (n + 3) & ~(size_t)3; };
     o_order = 16;                           // [0] tiles, [1] chunks
-    o_tiles = o_order + up4(T);             // {adapter or -1, first, count, 0}
-    o_chunks = o_tiles + 4 * (size_t)tiles; // {adapter, first, count, first of the padded order}
+    o_tiles = o_order + up4(T);             // {adapter or -1, first, count, first of the padded order}
+    o_tokens = o_tiles + 4 * (size_t)tiles; // [tiles, 64], the last one repeated
+    o_chunks = o_tokens + kLoraTile * (size_t)tiles;  // as the tiles
     o_first = o_chunks + 4 * (size_t)chunks;  // [E + 1] first chunk of an adapter
     o_slot = o_first + up4((size_t)E + 1);    // [E] first slot of an adapter with several chunks
     words = o_slot + up4(E);

@@ -105,7 +105,7 @@ def test_lora(T, K, N, R, E, how):
     _check(p, _index(T, E, how, 11), p["scale"], p["base"], p["dbase"])
 
 
-@pytest.mark.parametrize("T,R", [(1, 8), (600, 16), (1100, 64), (129, 112)])
+@pytest.mark.parametrize("T,R", [(1, 8), (600, 16), (1100, 64), (129, 112), (2100, 24), (4200, 8)])
 def test_lora_one_adapter(T, R):
     """Training of one adapter: more tokens than a tile and than a chunk; without scale,
     base or the gradient's base."""
@@ -144,7 +144,7 @@ def test_lora_larger():
                                      (5000, 1024, "mixed"), (20000, 9, "runs"), (9000, 1, "one"), (700, 4, "none")])
 def test_plan(T, E, how):
     """The tokens in order of their adapter, stable, those without one last; tiles of at
-    most 64 and chunks of at most 512 tokens of one adapter."""
+    most 64 and chunks of at most 1024 tokens of one adapter."""
     index = _index(T, E, how, 14)
     need = gl.lib().beam_moe_lora_plan_bytes(T, E)
     buf = Guarded(need, _dev(), "plan")
@@ -157,23 +157,28 @@ def test_plan(T, E, how):
     order = plan[16:16 + T]
     assert np.array_equal(order, np.argsort(g, kind="stable"))
     used = min(E, T)
-    tiles, chunks = 16 + up4(T), 16 + up4(T) + 4 * (T // 64 + min(E + 1, T))
+    most = T // 64 + min(E + 1, T)
+    tiles = 16 + up4(T)
+    tokens, chunks = tiles + 4 * most, tiles + 68 * most
     padded = first = 0
     want_tiles, want_chunks, firsts, slots = [], [], [], []
     for e in range(E + 1):
         c = int((g == e).sum())
-        want_tiles += [(e if e < E else -1, first + j, min(64, c - j), 0) for j in range(0, c, 64)]
+        want_tiles += [(e if e < E else -1, first + j, min(64, c - j), padded + j) for j in range(0, c, 64)]
         if e < E:
             firsts.append(len(want_chunks))
-            slots.append(sum(n for n in map(int, np.diff(firsts)) if n > 1) if c > 512 else -1)
-            want_chunks += [(e, first + j, min(512, c - j), padded + j) for j in range(0, c, 512)]
+            slots.append(sum(n for n in map(int, np.diff(firsts)) if n > 1) if c > 1024 else -1)
+            want_chunks += [(e, first + j, min(1024, c - j), padded + j) for j in range(0, c, 1024)]
             padded += (c + 31) // 32 * 32
         first += c
-    for at, limit, n, want in ((tiles, T // 64 + min(E + 1, T), plan[0], want_tiles),
-                               (chunks, T // 512 + used, plan[1], want_chunks)):
+    for at, limit, n, want in ((tiles, most, plan[0], want_tiles),
+                               (chunks, T // 1024 + used, plan[1], want_chunks)):
         assert n == len(want) <= limit
         assert np.array_equal(plan[at:at + 4 * n].reshape(n, 4), np.array(want).reshape(n, 4))
-    at = chunks + 4 * (T // 512 + used)
+    for i, (_, first, c, _) in enumerate(want_tiles):
+        row = plan[tokens + 64 * i:tokens + 64 * i + 64]
+        assert np.array_equal(row, order[np.minimum(np.arange(first, first + 64), first + c - 1)])
+    at = chunks + 4 * (T // 1024 + used)
     assert plan[at:at + E + 1].tolist() == firsts + [len(want_chunks)]
     assert plan[at + up4(E + 1):at + up4(E + 1) + E].tolist() == slots
 
