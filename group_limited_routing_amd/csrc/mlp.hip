@@ -7,6 +7,8 @@
 #include "operators.h"
 #include "tile.h"
 
+#include <algorithm>
+
 namespace beam {
 namespace {
 
@@ -103,8 +105,9 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
 template <Mode MODE, int FM, int FN, int WM, int WN>
 struct Tile {
   static constexpr int WAVES = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
-  static constexpr int KS = 64, NS = 2;                            // values of k in a stage, stages
+  static constexpr int KS = 64;  // values of k in a stage
   static constexpr int X_BYTES = BM * 2 * KS, STAGE = (BM + BN) * 2 * KS;
+  static constexpr int NS = BM == 64 ? 3 : 2;  // stages: what 160 KB hold
   static constexpr int COLS = MODE == kGated ? FN * 16 : FN * 32;  // of the output, a wave's
   static constexpr int TN = COLS * WN;                             // and the tile's
   static constexpr int STAGING = 32 * COLS * 2;                    // 32 rows of a wave's output
@@ -349,7 +352,7 @@ void tile_kernel(TileArgs p) {
         for (int j = 0; j < FN; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            st16(to + ((wm * FM + i) * 32 + r) * BN + j * 32 + 8 * q,
+            if (t.m0 + (wm * FM + i) * 32 + r < p.M) st16(to + ((wm * FM + i) * 32 + r) * BN + j * 32 + 8 * q,
                  u32x4{__float_as_uint(acc[i][j][4 * q]), __float_as_uint(acc[i][j][4 * q + 1]),
                        __float_as_uint(acc[i][j][4 * q + 2]), __float_as_uint(acc[i][j][4 * q + 3])});
       continue;
@@ -426,26 +429,35 @@ void tile_kernel(TileArgs p) {
 // The tiles that were cut along k: the sum of a tile's parts, in their order, and what
 // tile_kernel does with a sum. 8 columns a thread.
 template <Mode MODE, int BM, int BN, bool GELU>
-__global__ __launch_bounds__(256) void finish_kernel(TileArgs p) {
+__global__ __launch_bounds__(64) void finish_kernel(TileArgs p) {
   constexpr int TN = MODE == kGated ? BN / 2 : BN, PROBLEMS = MODE == kWeights ? 2 : 1;
   const int mtt = (p.M + BM - 1) / BM, ntt = (p.N + TN - 1) / TN;
   int mi, ni;
   tile_of(p.whole + blockIdx.x, PROBLEMS * mtt * ntt, PROBLEMS * mtt, ntt, mi, ni);
   const bool problem = MODE == kWeights && mi >= mtt;
-  const int at = blockIdx.y * 256 + threadIdx.x, row = at / (TN / 8), c = at % (TN / 8) * 8;
+  const int at = blockIdx.y * 64 + threadIdx.x, row = at / (TN / 8), c = at % (TN / 8) * 8;
   const int m = (problem ? mi - mtt : mi) * BM + row, n = ni * TN + c;
-  if (m >= p.M || n >= p.N) return;
+  if (row >= BM || m >= p.M || n >= p.N) return;
   const float* from = p.part + (size_t)blockIdx.x * p.splits * (BM * BN) + row * BN;
   auto sum8 = [&](int col, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-      const u32x4 a = ld16(from + (size_t)s * (BM * BN) + col), b = ld16(from + (size_t)s * (BM * BN) + col + 4);
+    for (int s = 0; s < p.splits; s += 4) {  // four parts' loads at a time
+      u32x4 a[4], b[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += __uint_as_float(a[i]);
-        v[4 + i] += __uint_as_float(b[i]);
+      for (int e = 0; e < 4; ++e) {
+        const float* at = from + (size_t)min(s + e, p.splits - 1) * (BM * BN) + col;
+        a[e] = ld16(at);
+        b[e] = ld16(at + 4);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (s + e < p.splits)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[i] += __uint_as_float(a[e][i]);
+            v[4 + i] += __uint_as_float(b[e][i]);
+          }
     }
   };
   auto add8 = [](const uint16_t* q, float (&v)[8]) {
@@ -522,7 +534,7 @@ void tile_launch(const TileArgs& a, const Cut& c, int gelu, hipStream_t st) {
     tile_kernel<MODE, FM, FN, WM, WN, R, G><<<grid, 64 * S::WAVES, 0, st>>>(t);
     if (c.splits > 1)
       finish_kernel<MODE, S::BM, S::BN, G>
-          <<<dim3((c.items - c.whole) / c.splits, S::BM * S::TN / 2048), 256, 0, st>>>(t);
+          <<<dim3((c.items - c.whole) / c.splits, (std::min(S::BM, a.M) * S::TN + 511) / 512), 64, 0, st>>>(t);
   };
   auto with = [&](auto rc) {
     if constexpr (MODE == kGated) {
