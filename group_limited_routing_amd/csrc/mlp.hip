@@ -12,20 +12,43 @@
 namespace beam {
 namespace {
 
-// act(g), and its derivative in d. gelu by erfc, which keeps its relative accuracy
-// where 1 + erf cancels (g below -3).
+// The normal distribution Phi(g) = erfc(-g / sqrt 2) / 2, and e^(-g^2 / 2) in e, with a
+// relative accuracy of 4 (g^2 + 16) 2^-24, also where Phi is small. e^(x^2) erfc(x) = t P(t)
+// with t = 1 / (1 + 0.35 x); P of degree 9 is a Chebyshev fit over all x >= 0, within 5e-8 of the
+// quotient. About 20 instructions; erfcf, whose ranges are branches, took 150, and 15 us of
+// an output of 1111 x 5000.
+__device__ __forceinline__ float normal_cdf(float g, float& e) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(g), 0.35f * 0.70710678118654752f, 1.0f));
+  e = __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
+  float p = 0.0393733224f;
+  p = fmaf(p, t, -0.167890257f);
+  p = fmaf(p, t, 0.210833749f);
+  p = fmaf(p, t, -0.0772500421f);
+  p = fmaf(p, t, 0.136077123f);
+  p = fmaf(p, t, 0.116022718f);
+  p = fmaf(p, t, 0.162620229f);
+  p = fmaf(p, t, 0.185278087f);
+  p = fmaf(p, t, 0.197468678f);
+  p = fmaf(p, t, 0.197466345f);
+  const float tail = 0.5f * e * (p * t);
+  return g < 0.f ? tail : 1.0f - tail;
+}
+
+// act(g), and its derivative in d.
 template <bool GELU>
 __device__ __forceinline__ float activation(float g) {
+  float e;
   if constexpr (GELU)
-    return 0.5f * g * erfcf(g * -0.70710678118654752f);
+    return g * normal_cdf(g, e);
   else
     return silu_f32(g);
 }
 template <bool GELU>
 __device__ __forceinline__ float activation(float g, float& d) {
   if constexpr (GELU) {
-    const float p = 0.5f * erfcf(g * -0.70710678118654752f);
-    d = p + g * 0.39894228040143268f * __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
+    float e;
+    const float p = normal_cdf(g, e);
+    d = p + g * 0.39894228040143268f * e;
     return g * p;
   } else {
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
@@ -107,7 +130,7 @@ struct Tile {
   static constexpr int WAVES = WM * WN, BM = 32 * FM * WM, BN = 32 * FN * WN;
   static constexpr int KS = 64;  // values of k in a stage
   static constexpr int X_BYTES = BM * 2 * KS, STAGE = (BM + BN) * 2 * KS;
-  static constexpr int NS = BM == 64 ? 3 : 2;  // stages: what 160 KB hold
+  static constexpr int NS = BM == 64 && MODE == kGated ? 3 : 2;  // stages: what LDS holds
   static constexpr int COLS = MODE == kGated ? FN * 16 : FN * 32;  // of the output, a wave's
   static constexpr int TN = COLS * WN;                             // and the tile's
   static constexpr int STAGING = 32 * COLS * 2;                    // 32 rows of a wave's output
@@ -115,10 +138,9 @@ struct Tile {
   static constexpr int PER_CU = LDS <= 80 * 1024 ? 2 : 1;          // workgroups
 };
 
+// The work of workgroup `block` of `blocks`, in `smem`.
 template <Mode MODE, int FM, int FN, int WM, int WN, bool RAGGED, bool GELU>
-__global__ __launch_bounds__(64 * WM * WN)
-    __attribute__((amdgpu_waves_per_eu(Tile<MODE, FM, FN, WM, WN>::PER_CU * WM * WN / 4)))
-void tile_kernel(TileArgs p) {
+__device__ __forceinline__ void tile_work(const TileArgs& p, int block, int blocks, uint8_t* smem) {
   using S = Tile<MODE, FM, FN, WM, WN>;
   constexpr bool XA = MODE == kWeights, WA = MODE != kGated;  // across
   constexpr int BM = S::BM, BN = S::BN, NS = S::NS, WAVES = S::WAVES, TN = S::TN;
@@ -126,7 +148,6 @@ void tile_kernel(TileArgs p) {
   constexpr int XU = S::X_BYTES / 1024, WU = BN * ROW / 1024, PER = (XU + WU) / WAVES;
   static_assert(XU % WAVES == 0 && WU % WAVES == 0, "a load is of one operand for every wave");
   static_assert((!XA || BM >= 128) && (!WA || BN >= 128), "four 64-byte chunks in a row of k");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[S::LDS];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN, r = lane & 31, h = lane >> 5;
@@ -161,7 +182,7 @@ void tile_kernel(TileArgs p) {
   uint32_t src[PER];
   int srck[RAGGED ? PER : 1];  // first value of k of the lane's chunk in a stage
   const uint8_t *x0, *x1, *w0, *w1;  // the tile's first elements
-  int load_item = blockIdx.x, load_k, load_end;  // the stage that the next loads are of
+  int load_item = block, load_k, load_end;  // the stage that the next loads are of
   // The lane anew, as a value that no loop knows: what an item computes from it once is not
   // kept in registers across the stages.
   auto fresh_lane = [&] {
@@ -204,7 +225,7 @@ void tile_kernel(TileArgs p) {
   auto advance = [&]() {
     if (++load_k < load_end) return;
     // behind the last item its stages are loaded again, which nothing reads
-    if (load_item + (int)gridDim.x < p.items) load_item += gridDim.x;
+    if (load_item + blocks < p.items) load_item += blocks;
     seek();
   };
   auto issue_one = [&](int slot, auto qc) {  // load q of the stage into a slot
@@ -282,7 +303,7 @@ void tile_kernel(TileArgs p) {
   };
   // loads of a stage that go beside half 1 of the stage NS before it; the others beside
   // half 0 of the next one
-  constexpr int TURN = (HALVES - 1) * SLOTS, WINDOW = HALVES * SLOTS * (MODE == kWeights ? 5 : 3) / 8;
+  constexpr int TURN = (HALVES - 1) * SLOTS, WINDOW = HALVES * SLOTS * (MODE == kGated ? 3 : 4) / 8;
   constexpr int FIRST = (SLOTS * PER + WINDOW - 1) / WINDOW < PER ? (SLOTS * PER + WINDOW - 1) / WINDOW : PER;
   auto issue_some = [&](int slot, auto from, auto to) {
     constexpr int A = decltype(from)::value, B = decltype(to)::value;
@@ -307,7 +328,7 @@ void tile_kernel(TileArgs p) {
   asm volatile("" ::: "memory");
   for_each<READS>([&](auto q) { read_one(smem, j0, q); });
   int slot = 0, before = (NS - 1) * S::STAGE;  // of this stage, and of the one before it
-  for (int item = blockIdx.x; item < p.items; item += gridDim.x) {
+  for (int item = block; item < p.items; item += blocks) {
     const Item t = item_of(item);
     clear();
     for (int s = 0; s < t.nk; ++s) {
@@ -321,7 +342,6 @@ void tile_kernel(TileArgs p) {
           barrier_only();
           asm volatile("" ::: "memory");
         }
-        acc[I][N] = mfma32(wr[J % 2][N], xr[J % 2][I], acc[I][N]);
         constexpr int R0 = M < WITHIN ? M * READS / WITHIN : READS;
         constexpr int R1 = M < WITHIN ? (M + 1) * READS / WITHIN : READS;
         for_each<R1 - R0>([&](auto e) {
@@ -336,6 +356,7 @@ void tile_kernel(TileArgs p) {
         constexpr int A = (O * PER + WINDOW - 1) / WINDOW, B = ((O + 1) * PER + WINDOW - 1) / WINDOW;
         issue_some(T >= TURN ? slot : before, std::integral_constant<int, A < PER ? A : PER>{},
                    std::integral_constant<int, B < PER ? B : PER>{});
+        acc[I][N] = mfma32(wr[J % 2][N], xr[J % 2][I], acc[I][N]);
         __builtin_amdgcn_sched_barrier(0);
       });
       before = slot;
@@ -366,6 +387,20 @@ void tile_kernel(TileArgs p) {
     const int c0 = t.n0 + wn * COLS;
     const int row_l = lane / L, ch_l = lane % L;
     const bool col_in = c0 + ch_l * 8 < p.N;
+    // what is added to a fragment is loaded during the one before it (what lies outside: other
+    // values, which are not stored)
+    constexpr int G = 32 / RS;
+    u32x4 gate_add[G], up_add[G];
+    auto fetch = [&](int i) {
+      const int c = min(c0 + ch_l * 8, p.N - 8);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const size_t at = (size_t)min(t.m0 + (wm * FM + i) * 32 + g * RS + row_l, p.M - 1) * p.N + c;
+        if (p.add_gate) gate_add[g] = ld16(p.add_gate + at);
+        if (p.add_up) up_add[g] = ld16(p.add_up + at);
+      }
+    };
+    if constexpr (MODE == kGated) fetch(0);
     for_each<FM>([&](auto ic) {
       constexpr int I = decltype(ic)::value;
       const int mb = t.m0 + (wm * FM + I) * 32;
@@ -391,14 +426,10 @@ void tile_kernel(TileArgs p) {
         settle();
       };
       if constexpr (MODE == kGated) {
-        auto add = [&](const uint16_t* from, auto which) {  // onto gate (0) or up (1)
+        auto add = [&](const u32x4 (&from)[G], auto which) {  // onto gate (0) or up (1)
           constexpr int W = decltype(which)::value;
 #pragma unroll
-          for (int g = 0; g < 32 / RS; ++g) {
-            const int row = g * RS + row_l;
-            if (mb + row < p.M && col_in)
-              st16(chunk(row, ch_l), ld16(from + (size_t)(mb + row) * p.N + c0 + ch_l * 8));
-          }
+          for (int g = 0; g < G; ++g) st16(chunk(g * RS + row_l, ch_l), from[g]);
           settle();
 #pragma unroll
           for (int j = 0; j < COLS / 32; ++j)
@@ -413,8 +444,9 @@ void tile_kernel(TileArgs p) {
             }
           settle();
         };
-        if (p.add_gate) add(p.add_gate, j0);
-        if (p.add_up) add(p.add_up, j1);
+        if (p.add_gate) add(gate_add, j0);
+        if (p.add_up) add(up_add, j1);
+        if constexpr (I + 1 < FM) fetch(I + 1);
         put(p.out[0], [&](int j, int i) { return activation<GELU>(acc[I][2 * j][i]) * acc[I][2 * j + 1][i]; });
         if (p.out[1]) put(p.out[1], [&](int j, int i) { return acc[I][2 * j][i]; });
         if (p.out[2]) put(p.out[2], [&](int j, int i) { return acc[I][2 * j + 1][i]; });
@@ -424,6 +456,30 @@ void tile_kernel(TileArgs p) {
     });
   }
   wait_vmcnt<0>();  // no load is in flight when the workgroup's LDS is given away
+}
+
+template <Mode MODE, int FM, int FN, int WM, int WN, bool RAGGED, bool GELU>
+__global__ __launch_bounds__(64 * WM * WN)
+    __attribute__((amdgpu_waves_per_eu(Tile<MODE, FM, FN, WM, WN>::PER_CU * WM * WN / 4)))
+void tile_kernel(TileArgs p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[Tile<MODE, FM, FN, WM, WN>::LDS];
+  tile_work<MODE, FM, FN, WM, WN, RAGGED, GELU>(p, blockIdx.x, gridDim.x, smem);
+}
+
+// Both products of the gradient in one launch, which do not wait for each other: the first
+// `first` workgroups have dx, the others the weights' gradients. FM x FN of dx, 2 FN x FN or
+// as much of the others' waves.
+template <int FM, int FN, int GM, int WM, int WN, bool RAGGED>
+__global__ __launch_bounds__(64 * WM * WN)
+    __attribute__((amdgpu_waves_per_eu(Tile<kWeights, GM, FN, WM, WN>::PER_CU * WM * WN / 4)))
+void gradients_kernel(TileArgs in, TileArgs weights, int first) {
+  using A = Tile<kInput, FM, FN, WM, WN>;
+  using B = Tile<kWeights, GM, FN, WM, WN>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[A::LDS > B::LDS ? A::LDS : B::LDS];
+  if ((int)blockIdx.x < first)
+    tile_work<kInput, FM, FN, WM, WN, RAGGED, false>(in, blockIdx.x, first, smem);
+  else
+    tile_work<kWeights, GM, FN, WM, WN, RAGGED, false>(weights, blockIdx.x - first, gridDim.x - first, smem);
 }
 
 // The tiles that were cut along k: the sum of a tile's parts, in their order, and what
@@ -521,20 +577,32 @@ Cut cut_for(int M, int N, int K, int stage_ns) {
                 S::BM * S::BN * 4, stage_ns);
 }
 
+TileArgs with_cut(TileArgs a, const Cut& c) {
+  a.whole = c.whole;
+  a.items = c.items;
+  a.splits = c.splits;
+  return a;
+}
+template <Mode MODE, int FM, int FN, int WM, int WN>
+int grid_of(const Cut& c) {
+  return std::min(c.items, 256 * Tile<MODE, FM, FN, WM, WN>::PER_CU);
+}
+template <Mode MODE, int FM, int FN, int WM, int WN, bool GELU>
+void finish(const TileArgs& t, hipStream_t st) {
+  using S = Tile<MODE, FM, FN, WM, WN>;
+  if (t.splits > 1)
+    finish_kernel<MODE, S::BM, S::BN, GELU>
+        <<<dim3((t.items - t.whole) / t.splits, (std::min(S::BM, t.M) * S::TN + 511) / 512), 64, 0, st>>>(t);
+}
+
 template <Mode MODE, int FM, int FN, int WM, int WN>
 void tile_launch(const TileArgs& a, const Cut& c, int gelu, hipStream_t st) {
   using S = Tile<MODE, FM, FN, WM, WN>;
-  TileArgs t = a;
-  t.whole = c.whole;
-  t.items = c.items;
-  t.splits = c.splits;
-  const int grid = c.items < 256 * S::PER_CU ? c.items : 256 * S::PER_CU;
+  const TileArgs t = with_cut(a, c);
   auto go = [&](auto rc, auto gc) {
     constexpr bool R = decltype(rc)::value, G = decltype(gc)::value;
-    tile_kernel<MODE, FM, FN, WM, WN, R, G><<<grid, 64 * S::WAVES, 0, st>>>(t);
-    if (c.splits > 1)
-      finish_kernel<MODE, S::BM, S::BN, G>
-          <<<dim3((c.items - c.whole) / c.splits, (std::min(S::BM, a.M) * S::TN + 511) / 512), 64, 0, st>>>(t);
+    tile_kernel<MODE, FM, FN, WM, WN, R, G><<<grid_of<MODE, FM, FN, WM, WN>(c), 64 * S::WAVES, 0, st>>>(t);
+    finish<MODE, FM, FN, WM, WN, G>(t, st);
   };
   auto with = [&](auto rc) {
     if constexpr (MODE == kGated) {
@@ -549,25 +617,135 @@ void tile_launch(const TileArgs& a, const Cut& c, int gelu, hipStream_t st) {
 }
 
 // Tiles of 256 x 256, 128 x 128 and 64 x 128 (columns of w): the one whose cut costs least.
-template <Mode MODE>
-size_t product(const TileArgs* a, int M, int N, int K, int gelu, hipStream_t st) {
-  Cut c[3] = {cut_for<MODE, 4, 2, 2, 4>(M, N, K, 1650), cut_for<MODE, 2, 2, 2, 2>(M, N, K, 1000), {}};
-  c[2].cost = INT64_MAX;
-  if constexpr (MODE != kWeights) c[2] = cut_for<MODE, 1, 2, 2, 2>(M, N, K, 800);
-  int best = 0;
-  for (int i = 1; i < 3; ++i)
-    if (c[i].cost < c[best].cost) best = i;
-  if (!a) {
-    const int floats[3] = {256 * 256, 128 * 128, 64 * 128};
-    return c[best].splits > 1 ? (size_t)(c[best].items - c[best].whole) * floats[best] * sizeof(float) : 0;
+// A stage of a full round takes 1.6, 1.1 and 0.75 us (8192 x 5120 x 10240 by one tile alone:
+// 1.29, 1.76 and 2.37 ms).
+constexpr size_t kTileFloats[3] = {256 * 256, 128 * 128, 64 * 128};
+struct Choice {
+  int tile;
+  Cut cut;
+  size_t part_bytes() const {
+    return cut.splits > 1 ? (cut.items - cut.whole) * kTileFloats[tile] * sizeof(float) : 0;
   }
-  if (best == 0)
-    tile_launch<MODE, 4, 2, 2, 4>(*a, c[0], gelu, st);
-  else if (best == 1)
-    tile_launch<MODE, 2, 2, 2, 2>(*a, c[1], gelu, st);
+};
+template <Mode MODE>
+Choice choose(int M, int N, int K) {
+  Choice best{0, cut_for<MODE, 4, 2, 2, 4>(M, N, K, 1600)};
+  const Cut c = cut_for<MODE, 2, 2, 2, 2>(M, N, K, 1100);
+  if (c.cost < best.cut.cost) best = {1, c};
+  if constexpr (MODE != kWeights) {  // a row of k has at least 128 columns
+    const Cut d = cut_for<MODE, 1, 2, 2, 2>(M, N, K, 750);
+    if (d.cost < best.cut.cost) best = {2, d};
+  }
+  return best;
+}
+template <Mode MODE>
+void product(const TileArgs& a, int gelu, hipStream_t st) {
+  const Choice c = choose<MODE>(a.M, a.N, a.K);
+  if (c.tile == 0)
+    tile_launch<MODE, 4, 2, 2, 4>(a, c.cut, gelu, st);
+  else if (c.tile == 1)
+    tile_launch<MODE, 2, 2, 2, 2>(a, c.cut, gelu, st);
   else if constexpr (MODE != kWeights)
-    tile_launch<MODE, 1, 2, 2, 2>(*a, c[2], gelu, st);
-  return 0;
+    tile_launch<MODE, 1, 2, 2, 2>(a, c.cut, gelu, st);
+}
+
+template <int FM, int GM, int WM, int WN>
+void gradients_launch(const TileArgs& in, const Cut& ci, const TileArgs& weights, const Cut& cw, hipStream_t st) {
+  const TileArgs a = with_cut(in, ci), b = with_cut(weights, cw);
+  const int first = grid_of<kInput, FM, 2, WM, WN>(ci), grid = first + grid_of<kWeights, GM, 2, WM, WN>(cw);
+  if (a.K % 64 != 0 || b.K % 64 != 0)
+    gradients_kernel<FM, 2, GM, WM, WN, true><<<grid, 64 * WM * WN, 0, st>>>(a, b, first);
+  else
+    gradients_kernel<FM, 2, GM, WM, WN, false><<<grid, 64 * WM * WN, 0, st>>>(a, b, first);
+  finish<kInput, FM, 2, WM, WN, false>(a, st);
+  finish<kWeights, GM, 2, WM, WN, false>(b, st);
+}
+// Both products in one launch where their tiles have as many waves, else one after the other.
+void gradients(const TileArgs& in, const TileArgs& weights, hipStream_t st) {
+  const Choice i = choose<kInput>(in.M, in.N, in.K), w = choose<kWeights>(weights.M, weights.N, weights.K);
+  if (i.tile == 0 && w.tile == 0)
+    gradients_launch<4, 4, 2, 4>(in, i.cut, weights, w.cut, st);
+  else if (i.tile == 1 && w.tile == 1)
+    gradients_launch<2, 2, 2, 2>(in, i.cut, weights, w.cut, st);
+  else if (i.tile == 2 && w.tile == 1)
+    gradients_launch<1, 2, 2, 2>(in, i.cut, weights, w.cut, st);
+  else {
+    product<kInput>(in, 0, st);
+    product<kWeights>(weights, 0, st);
+  }
+}
+
+// ------------------------------------------------------------------ few tokens
+// Up to 16 tokens: the weights' stream is all there is. A workgroup takes 16 columns of h,
+// its 8 waves 128 values of k in turn, straight into registers (16 rows of w_gate, of
+// w_up and the tokens, 256 bytes of a row at a time), and the waves' sums are added
+// through LDS in their order: no second kernel. MFMA rows are the weights', columns the
+// tokens.
+// 5120 x 2560, 1 token 13 us (52 MB of weights; by tiles, whose cut needs a second kernel, 20),
+// 16 tokens 16 us. Every workgroup reads all tokens, so wide outputs of many tokens go to
+// the tiles: 5120 x 10240, 1 token 37 us (39), 16 tokens 44 us (39).
+constexpr int kFewTokens = 16, kFewWaves = 8;
+bool few_tokens(int T, int F) { return T <= kFewTokens && (int64_t)T * F <= 81920; }
+
+template <bool GELU>
+__global__ __launch_bounds__(64 * kFewWaves) void gated_few_kernel(GatedArgs p) {
+  __shared__ f32x4 sums[kFewWaves][2][64];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
+  const int f0 = blockIdx.x * 16;
+  const size_t row = (size_t)min(f0 + l, p.F - 1) * p.H + g * 8;
+  const uint16_t *gr = p.wg + row, *ur = p.wu + row, *xr = p.x + (size_t)min(l, p.T - 1) * p.H + g * 8;
+  f32x4 gate{}, up{};
+  auto group = [&](int k0, auto end) {
+    u32x4 x[4], a[4], b[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k = k0 + s * 32;
+      const bool in = !decltype(end)::value || k + g * 8 < p.H;  // H is a multiple of 8
+      a[s] = ld16(in ? (const void*)(gr + k) : (const void*)kZeros);
+      b[s] = ld16(in ? (const void*)(ur + k) : (const void*)kZeros);
+      x[s] = ld16(in ? (const void*)(xr + k) : (const void*)kZeros);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      gate = mfma_bf16(as_bf16x8(a[s]), as_bf16x8(x[s]), gate);
+      up = mfma_bf16(as_bf16x8(b[s]), as_bf16x8(x[s]), up);
+    }
+  };
+  int k0 = wave * 128;
+  for (; k0 + 128 <= p.H; k0 += kFewWaves * 128) group(k0, std::false_type{});
+  if (k0 < p.H) group(k0, std::true_type{});
+  sums[wave][0][lane] = gate;
+  sums[wave][1][lane] = up;
+  __syncthreads();
+  // lane (token l, columns 4 g .. + 3)
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 1; w < kFewWaves; ++w) {
+    gate += sums[w][0][lane];
+    up += sums[w][1][lane];
+  }
+  const int f = f0 + 4 * g;
+  if (l >= p.T || f >= p.F) return;
+  const size_t at = (size_t)l * p.F + f;
+  auto add = [&](const uint16_t* from, f32x4& to) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(from + at);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      to[2 * e] += __uint_as_float(v[e] << 16);
+      to[2 * e + 1] += __uint_as_float(v[e] & 0xffff0000u);
+    }
+  };
+  auto put = [&](uint16_t* to, const f32x4& v) {
+    *reinterpret_cast<u32x2*>(to + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  };
+  if (p.add_gate) add(p.add_gate, gate);
+  if (p.add_up) add(p.add_up, up);
+  f32x4 h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = activation<GELU>(gate[e]) * up[e];
+  put(p.h, h);
+  if (p.gate) put(p.gate, gate);
+  if (p.up) put(p.up, up);
 }
 
 // d_up = dh act(gate), d_gate = dh up act'(gate), 8 values a thread. Rounded to bf16,
@@ -599,9 +777,19 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedBwdArgs p) {
 
 }  // namespace
 
-size_t gated_workspace_bytes(int T, int H, int F) { return product<kGated>(nullptr, T, F, H, 0, nullptr); }
+size_t gated_workspace_bytes(int T, int H, int F) {
+  return few_tokens(T, F) ? 0 : choose<kGated>(T, F, H).part_bytes();
+}
 
 hipError_t launch_gated_linear(const GatedArgs& a, int gelu, hipStream_t st) {
+  if (few_tokens(a.T, a.F)) {
+    const int grid = (a.F + 15) / 16;
+    if (gelu)
+      gated_few_kernel<true><<<grid, 64 * kFewWaves, 0, st>>>(a);
+    else
+      gated_few_kernel<false><<<grid, 64 * kFewWaves, 0, st>>>(a);
+    return hipGetLastError();
+  }
   TileArgs t{};
   t.x[0] = (const uint8_t*)a.x;
   t.w[0] = (const uint8_t*)a.wg;
@@ -616,45 +804,47 @@ hipError_t launch_gated_linear(const GatedArgs& a, int gelu, hipStream_t st) {
   t.out[1] = a.gate;
   t.out[2] = a.up;
   t.part = a.part;
-  product<kGated>(&t, a.T, a.F, a.H, gelu, st);
+  product<kGated>(t, gelu, st);
   return hipGetLastError();
 }
 
+// dx's parts, then the weights'
 size_t gated_bwd_workspace_bytes(int T, int H, int F) {
-  const size_t in = product<kInput>(nullptr, T, H, F, 0, nullptr), w = product<kWeights>(nullptr, F, H, T, 0, nullptr);
-  return in > w ? in : w;
+  return choose<kInput>(T, H, F).part_bytes() + choose<kWeights>(F, H, T).part_bytes();
 }
 
 hipError_t launch_gated_linear_backward(const GatedBwdArgs& a, int gelu, hipStream_t st) {
   const int64_t n8 = (int64_t)a.T * a.F / 8;
-  const unsigned grid = (unsigned)((n8 + 255) / 256 < (1 << 20) ? (n8 + 255) / 256 : 1 << 20);
+  const unsigned grid = (unsigned)std::min<int64_t>((n8 + 255) / 256, 1 << 20);
   if (gelu)
     gated_grad_kernel<true><<<grid, 256, 0, st>>>(a);
   else
     gated_grad_kernel<false><<<grid, 256, 0, st>>>(a);
-  TileArgs t{};
-  t.x[0] = (const uint8_t*)a.d_gate;
-  t.x[1] = (const uint8_t*)a.d_up;
-  t.ldx = 2 * (int64_t)a.F;
-  t.ldw = 2 * (int64_t)a.H;
-  t.N = a.H;
-  t.part = a.part;
-  if (a.dx) {
-    t.w[0] = (const uint8_t*)a.wg;
-    t.w[1] = (const uint8_t*)a.wu;
-    t.M = a.T;
-    t.K = a.F;
-    t.out[0] = a.dx;
-    product<kInput>(&t, a.T, a.H, a.F, 0, st);
-  }
-  if (a.d_wg) {
-    t.w[0] = t.w[1] = (const uint8_t*)a.x;
-    t.M = a.F;
-    t.K = a.T;
-    t.out[0] = a.d_wg;
-    t.out[1] = a.d_wu;
-    product<kWeights>(&t, a.F, a.H, a.T, 0, st);
-  }
+  TileArgs in{};
+  in.x[0] = (const uint8_t*)a.d_gate;
+  in.x[1] = (const uint8_t*)a.d_up;
+  in.ldx = 2 * (int64_t)a.F;
+  in.ldw = 2 * (int64_t)a.H;
+  in.N = a.H;
+  TileArgs weights = in;
+  in.w[0] = (const uint8_t*)a.wg;
+  in.w[1] = (const uint8_t*)a.wu;
+  in.M = a.T;
+  in.K = a.F;
+  in.out[0] = a.dx;
+  in.part = a.part;
+  weights.w[0] = weights.w[1] = (const uint8_t*)a.x;
+  weights.M = a.F;
+  weights.K = a.T;
+  weights.out[0] = a.d_wg;
+  weights.out[1] = a.d_wu;
+  weights.part = a.part + choose<kInput>(a.T, a.H, a.F).part_bytes() / sizeof(float);
+  if (a.dx && a.d_wg)
+    gradients(in, weights, st);
+  else if (a.dx)
+    product<kInput>(in, 0, st);
+  else if (a.d_wg)
+    product<kWeights>(weights, 0, st);
   return hipGetLastError();
 }
 
