@@ -145,6 +145,33 @@ __device__ __forceinline__ void tile_tokens(const int32_t* plan, const LoraPlanL
     tokens[b] = plan[at.o_tokens + (size_t)tile * kLoraTile + b * 16 + (threadIdx.x & 15)];
 }
 
+// f(i, sum over the parts, in their order, of the 4 values at from(i)) for this thread's i of
+// `count`; parts is 1, 2, 4 or 8, all of an i's loads go out together.
+template <typename From, typename F>
+__device__ __forceinline__ void each_sum(int count, int parts, size_t pitch, From from, F f) {
+  auto go = [&](auto pc) {
+    constexpr int P = decltype(pc)::value;
+    for (int i = threadIdx.x; i < count; i += 256) {
+      const float* at = from(i);
+      f32x4 w[P];
+#pragma unroll
+      for (int q = 0; q < P; ++q) w[q] = *reinterpret_cast<const f32x4*>(at + q * pitch);
+      f32x4 s = w[0];
+#pragma unroll
+      for (int q = 1; q < P; ++q) s += w[q];
+      f(i, s);
+    }
+  };
+  if (parts == 1)
+    go(std::integral_constant<int, 1>{});
+  else if (parts == 2)
+    go(std::integral_constant<int, 2>{});
+  else if (parts == 4)
+    go(std::integral_constant<int, 4>{});
+  else
+    go(std::integral_constant<int, kMaxParts>{});
+}
+
 // v as the sum of two bf16 values, 16 significant bits; beyond the largest bf16 number,
 // and for NaN, the first alone.
 __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
@@ -290,25 +317,24 @@ __device__ __forceinline__ void rank_out(const LoraOutArgs& p, const int4& tile,
   load(min(nb, N - 8));
   const float f = p.scale ? p.scale[tile.x] : 1.f;
   const int r4 = R / 4;
-  for (int i = tid; i < count * r4; i += 256) {
-    const int t = i / r4, r = i % r4 * 4;
-    const float* from = p.part + (size_t)(tile.y + t) * R + r;
-    f32x4 w[kMaxParts], s{};
+  each_sum(
+      count * r4, p.parts, (size_t)p.T * R,
+      [&](int i) { return p.part + (size_t)(tile.y + i / r4) * R + i % r4 * 4; },
+      [&](int i, const f32x4& s) {
+        const int t = i / r4, r = i % r4 * 4;
+        if (p.v && n0 == 0) *reinterpret_cast<f32x4*>(p.v + (size_t)all_tokens[t] * R + r) = s;
+        u32x2 hi, lo;
 #pragma unroll
-    for (int q = 0; q < kMaxParts; ++q)
-      w[q] = *reinterpret_cast<const f32x4*>(from + (size_t)min(q, p.parts - 1) * p.T * R);
-#pragma unroll
-    for (int q = 0; q < kMaxParts; ++q)
-      if (q < p.parts) s += w[q];
-    if (p.v && n0 == 0) *reinterpret_cast<f32x4*>(p.v + (size_t)all_tokens[t] * R + r) = s;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t hi, lo;
-      split(s[q] * f, hi, lo);
-      vs[t * PITCH + r + q] = (uint16_t)hi;
-      vs[t * PITCH + R + r + q] = (uint16_t)lo;
-    }
-  }
+        for (int q = 0; q < 2; ++q) {
+          uint32_t h0, h1, l0, l1;
+          split(s[2 * q] * f, h0, l0);
+          split(s[2 * q + 1] * f, h1, l1);
+          hi[q] = h0 | h1 << 16;
+          lo[q] = l0 | l1 << 16;
+        }
+        *reinterpret_cast<u32x2*>(vs + t * PITCH + r) = hi;
+        *reinterpret_cast<u32x2*>(vs + t * PITCH + R + r) = lo;
+      });
   const int rest = RB * 32 - 2 * R;  // of a token's row
   for (int i = tid; i < count * rest; i += 256) vs[i / rest * PITCH + 2 * R + i % rest] = 0;
   __syncthreads();
@@ -437,32 +463,28 @@ __global__ __launch_bounds__(256) void lora_operands_kernel(const float* part, i
   const int count = tile.z, padded = (count + 31) & ~31;
   const float f = scale ? scale[tile.x] : 1.f;
   const int which = blockIdx.y;  // 0: dv, 1: v
-  for (int i = threadIdx.x; i < 64 * (R / 4); i += 256) {
-    const int t = i / (R / 4), r = i % (R / 4) * 4;
-    f32x4 s{};
-    if (t < count) {
-      const int pos = tile.y + t;
-      if (which == 0) {
-        f32x4 w[kMaxParts];
-#pragma unroll
-        for (int p = 0; p < kMaxParts; ++p)
-          w[p] = *reinterpret_cast<const f32x4*>(part + ((size_t)min(p, parts - 1) * T + pos) * R + r);
-#pragma unroll
-        for (int p = 0; p < kMaxParts; ++p)
-          if (p < parts) s += w[p];
-        s *= f;
-        *reinterpret_cast<f32x4*>(dv + (size_t)pos * R + r) = s;
-      } else {
-        s = *reinterpret_cast<const f32x4*>(v + (size_t)plan[at.o_order + pos] * R + r) * f;
-      }
-    }
+  const int r4 = R / 4;
+  auto pair = [&](int t, int r, const f32x4& s) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t hi, lo;
       split(s[q], hi, lo);
       pairs[(r + q) * 66 + t] = hi | lo << 16;
     }
-  }
+  };
+  if (which == 0)
+    each_sum(
+        count * r4, parts, (size_t)T * R, [&](int i) { return part + (size_t)(tile.y + i / r4) * R + i % r4 * 4; },
+        [&](int i, const f32x4& s) {
+          *reinterpret_cast<f32x4*>(dv + (size_t)(tile.y + i / r4) * R + i % r4 * 4) = s * f;
+          pair(i / r4, i % r4 * 4, s * f);
+        });
+  else
+    for (int i = threadIdx.x; i < count * r4; i += 256)
+      pair(i / r4, i % r4 * 4,
+           f * *reinterpret_cast<const f32x4*>(
+                   v + (size_t)plan[at.o_tokens + (size_t)blockIdx.x * kLoraTile + i / r4] * R + i % r4 * 4));
+  for (int i = count * R + threadIdx.x; i < padded * R; i += 256) pairs[i % R * 66 + i / R] = 0;
   __syncthreads();
   uint16_t* to = which == 0 ? dvt : vt;
   if (!to) return;
@@ -503,7 +525,10 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
   const LoraPlanLayout at(p.T, p.E);
   const int wgs0 = (p.C[0] + 127) / 128;
   int number, block;
-  place(wgs0 + (p.C[1] + 127) / 128, number, block);
+  const int ranks = (p.R + RB * 16 - 1) / (RB * 16);
+  place((wgs0 + (p.C[1] + 127) / 128) * ranks, number, block);
+  const int r0 = block % ranks * (RB * 16);
+  block /= ranks;
   const int which = block >= wgs0;
   if (number >= at.chunks || number >= p.plan[1]) return;
   const int4 chunk = chunk_at(p.plan, at, number);
@@ -512,7 +537,6 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
   const uint16_t* op = which ? p.op[1] : p.op[0];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
   const int c0 = (block - (which ? wgs0 : 0)) * 128 + l * 8, c = min(c0, C - 8);
-  const int r0 = blockIdx.y * (RB * 16);
   const size_t lo = (size_t)R * at.padded;
   const uint16_t* ops[RB];
 #pragma unroll
@@ -525,39 +549,49 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
       tokens[i] = p.plan[at.o_order + chunk.y + min(p0 + i, chunk.z - 1)];
     __syncthreads();
     const int n = min(512, chunk.z - p0);
-    u32x4 ahead[8];  // the wave's next rows are in flight while these are multiplied
-    auto load = [&](int s) {
+    // the next rows are loaded while these are multiplied, the next operands behind the
+    // last product that reads these
+    u32x4 x[8], a[RB][2];
+    auto load_x = [&](int s) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ahead[i] = ld16(rows + (size_t)tokens[s + g * 8 + i] * C + c);
+      for (int i = 0; i < 8; ++i) x[i] = ld16(rows + (size_t)tokens[s + g * 8 + i] * C + c);
     };
-    if (wave * 32 < n) load(wave * 32);
-    for (int s = wave * 32; s < n; s += 128) {
-      u32x4 x[8], a[RB][2];
+    auto load_a = [&](int s) {
 #pragma unroll
       for (int q = 0; q < RB; ++q) {
         a[q][0] = ld16(ops[q] + p0 + s);
         a[q][1] = ld16(ops[q] + lo + p0 + s);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = ahead[i];
-      if (s + 128 < n) load(s + 128);
+    };
+    if (wave * 32 < n) {
+      load_x(wave * 32);
+      load_a(wave * 32);
+    }
+    for (int s = wave * 32; s < n; s += 128) {
       if (s + 32 > n) {  // tokens past the chunk's last one: zeros on both sides
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (s + g * 8 + i >= n) x[i] = u32x4{0, 0, 0, 0};
       }
+      u32x4 f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        u32x4 f;
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          f[i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+          f[j][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+      __builtin_amdgcn_sched_barrier(0);
+      if (s + 128 < n) load_x(s + 128);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int q = 0; q < RB; ++q) {
-          acc[q][j] = mfma_bf16(as_bf16x8(a[q][0]), as_bf16x8(f), acc[q][j]);
-          acc[q][j] = mfma_bf16(as_bf16x8(a[q][1]), as_bf16x8(f), acc[q][j]);
+          acc[q][j] = mfma_bf16(as_bf16x8(a[q][0]), as_bf16x8(f[j]), acc[q][j]);
+          acc[q][j] = mfma_bf16(as_bf16x8(a[q][1]), as_bf16x8(f[j]), acc[q][j]);
         }
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (s + 128 < n) load_a(s + 128);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   // waves 2 and 3 onto 0 and 1, then 1 onto 0
@@ -745,10 +779,8 @@ hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
     const int wgs = (p.K + 127) / 128 + (p.N + 127) / 128;
     if (p.R <= 16)
       lora_grad_kernel<1><<<grid_of(l.chunks, wgs), 256, 0, st>>>(a);
-    else if (p.R <= 32)
-      lora_grad_kernel<2><<<grid_of(l.chunks, wgs), 256, 0, st>>>(a);
     else
-      lora_grad_kernel<4><<<dim3(grid_of(l.chunks, wgs), (p.R + 63) / 64), 256, 0, st>>>(a);
+      lora_grad_kernel<2><<<grid_of(l.chunks, wgs * ((p.R + 31) / 32)), 256, 0, st>>>(a);
     lora_grad_sum_kernel<<<dim3((p.R * (p.K + p.N) / 8 + 255) / 256, p.E), 256, 0, st>>>(a);
   }
   return hipGetLastError();
