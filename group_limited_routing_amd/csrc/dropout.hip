@@ -75,7 +75,10 @@ __device__ __forceinline__ void store1(T* p, float v) {
 }
 
 // 8 elements a thread and step, one call of the generator. A lane's random words, and so
-// the mask, depend on the place in the tensor alone, not on the launch.
+// the mask, depend on the place in the tensor alone, not on the launch. Bound by memory:
+// 16384 x 5120 in bf16 58 us (x to out), 87 us with the stream, 86 us with its gradient, in fp32
+// 119, 168 and 185: 5.7 to 6 TB/s, so the ten rounds of the generator cost nothing. 16 bits an
+// element halve them as against 32, and put p within 2^-17.
 enum Rest { kNothing, kStream, kGrad };  // what stands beside x: nothing, stream_in, keep * x
 
 template <typename T, Rest REST>

@@ -65,6 +65,12 @@ __device__ __forceinline__ float activation(float g, float& d) {
 //             product are its epilogue.
 //   kInput    d_gate along and w_gate across, then d_up and w_up: one sum over 2 F.
 //   kWeights  d_gate (or d_up) across, x across: a sum over the tokens.
+//
+// Large products are bound by the matrix cores under the chip's power limit: 8192 x 5120 x
+// 10240 (kGated, 1.72e12 operations) takes 1.27 to 1.29 ms, 1.34 PF/s, with the matrix cores
+// busy 76% of the time at 1.5 to 1.65 GHz. The same loop without its loads from memory takes
+// 1.14 ms, without reads of LDS 1.19, without both 0.85 (the instructions alone). The
+// gradient's two products at 4096 tokens: 1.31 to 1.38 ms.
 enum Mode { kGated, kInput, kWeights };
 
 struct TileArgs {
@@ -118,11 +124,12 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
 
 // Waves as WM x WN, each FM x FN fragments of 32 x 32 on 32x32x16 MFMAs (w first, so
 // that a lane ends with runs of 4 consecutive output columns). Operands go from memory
-// straight into LDS (16 bytes a lane) through a ring of NS stages of 32 values of k. A
+// straight into LDS (16 bytes a lane) through a ring of NS stages of 64 values of k (four
+// stages of 32, twice the barriers: 1386 us where two of 64 take 1290; 8192 x 5120 x 10240). A
 // workgroup stays for many items of work, and its loads run ahead into the next one, so
 // that neither the first loads of an item nor its output stop the ring.
 //
-// LDS of a stage. Along: 64 bytes a row, swizzled as tile.h says. Across: a row of the
+// LDS of a stage. Along: 128 bytes a row, swizzled as tile.h says. Across: a row of the
 // tile's width for each k; the 64-byte chunk c (32 columns, one fragment) of row k
 // stands at c ^ (k & 3), so that the 4 rows of a transposing read cover all banks.
 template <Mode MODE, int FM, int FN, int WM, int WN>
@@ -242,7 +249,7 @@ __device__ __forceinline__ void tile_work(const TileArgs& p, int block, int bloc
     }
   };
 
-  // Operand offsets in a stage. Along: fragment i is 32 rows on, chunk 2 j + h of half j.
+  // Operand offsets in a stage. Along: fragment i is 32 rows on, chunk 2 j + h in step j.
   // Across: fragment i is 64-byte chunk (first + i) of rows 16 j + 8 h + 4 e + kk.
   const int kk = lane % 16 / 4, ac = (lane / 16 % 2) * 32 + lane % 4 * 8;
   int xo[XA ? FM : HALVES], wo[WA ? FN : HALVES];
@@ -277,12 +284,12 @@ __device__ __forceinline__ void tile_work(const TileArgs& p, int block, int bloc
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
   };
 
-  // A stage is two halves of 16 values of k, each FM x FN instructions. Beside every
+  // A stage is HALVES steps of 16 values of k, each FM x FN instructions. Beside every
   // instruction goes at most a read or two of LDS and a load, so that neither queue
-  // holds the wave back: the fragments of half 1 are read during half 0, those of the next
-  // stage's half 0 during half 1. The barrier between the halves says that every wave has
-  // read all of stage s, whose slot stage s + NS refills from then on, and that stage s + 1
-  // has landed.
+  // holds the wave back: the fragments of step j + 1 are read during step j, those of the
+  // next stage's step 0 during the last one. The barrier before the last step says that
+  // every wave has read all of stage s, whose slot stage s + NS refills from then on, and
+  // that stage s + 1 has landed.
   constexpr int SLOTS = FM * FN, READS = FM + FN, WITHIN = SLOTS > 4 ? SLOTS * 3 / 4 : SLOTS;
   u32x4 xr[2][FM], wr[2][FN];
   auto read_one = [&](const uint8_t* st, auto jc, auto qc) {  // x fragment 0, w's, the other x's
@@ -301,8 +308,8 @@ __device__ __forceinline__ void tile_work(const TileArgs& p, int block, int bloc
         xr[J % 2][I] = ld16(st + xo[J] + I * 32 * ROW);
     }
   };
-  // loads of a stage that go beside half 1 of the stage NS before it; the others beside
-  // half 0 of the next one
+  // loads of a stage that go beside the last step of the stage NS before it; the others
+  // beside the first steps of the next one
   constexpr int TURN = (HALVES - 1) * SLOTS, WINDOW = HALVES * SLOTS * (MODE == kGated ? 3 : 4) / 8;
   constexpr int FIRST = (SLOTS * PER + WINDOW - 1) / WINDOW < PER ? (SLOTS * PER + WINDOW - 1) / WINDOW : PER;
   auto issue_some = [&](int slot, auto from, auto to) {
@@ -467,8 +474,9 @@ void tile_kernel(TileArgs p) {
 }
 
 // Both products of the gradient in one launch, which do not wait for each other: the first
-// `first` workgroups have dx, the others the weights' gradients. FM x FN of dx, 2 FN x FN or
-// as much of the others' waves.
+// `first` workgroups have dx, by waves of FM x FN fragments, the others the weights'
+// gradients, by waves of GM x FN. (777 x 1288 x 1000: 28 us, so 18 and 13 one after the other;
+// 4096 x 5120 x 10240: the second product's tiles fill the end of the first's last round.)
 template <int FM, int FN, int GM, int WM, int WN, bool RAGGED>
 __global__ __launch_bounds__(64 * WM * WN)
     __attribute__((amdgpu_waves_per_eu(Tile<kWeights, GM, FN, WM, WN>::PER_CU * WM * WN / 4)))
@@ -483,7 +491,8 @@ void gradients_kernel(TileArgs in, TileArgs weights, int first) {
 }
 
 // The tiles that were cut along k: the sum of a tile's parts, in their order, and what
-// tile_kernel does with a sum. 8 columns a thread.
+// tile_kernel does with a sum. 8 columns a thread. Bound by the latency of its loads and its
+// start: 4 to 5 us at a few MB of parts, 18 us for 67 MB.
 template <Mode MODE, int BM, int BN, bool GELU>
 __global__ __launch_bounds__(64) void finish_kernel(TileArgs p) {
   constexpr int TN = MODE == kGated ? BN / 2 : BN, PROBLEMS = MODE == kWeights ? 2 : 1;
@@ -549,8 +558,10 @@ __global__ __launch_bounds__(64) void finish_kernel(TileArgs p) {
 
 // How a product is cut. Rounds of 256 PER_CU workgroups take whole tiles; what is left
 // would keep a part of the chip busy for a whole round, so it is cut along k into as many
-// parts as make it cheapest. Costs in ns: a stage of a full round, the parts' way through memory, and
-// the second kernel.
+// parts as make it cheapest. Costs in ns: a stage of a full round, the parts' way through
+// memory at 2 TB/s, and 5 us for the second kernel. (64 tokens, 5120 x 10240: 160 tiles of
+// the 512 that run at once, cut in 3, 48 us and 5 us for the sums; the weights alone are
+// 42 us at a large copy's rate.)
 struct Cut {
   int whole, items, splits;
   int64_t cost;
@@ -617,8 +628,8 @@ void tile_launch(const TileArgs& a, const Cut& c, int gelu, hipStream_t st) {
 }
 
 // Tiles of 256 x 256, 128 x 128 and 64 x 128 (columns of w): the one whose cut costs least.
-// A stage of a full round takes 1.6, 1.1 and 0.75 us (8192 x 5120 x 10240 by one tile alone:
-// 1.29, 1.76 and 2.37 ms).
+// A stage of a full round (256, 512 and 512 tiles) takes 1.6, 1.1 and 0.75 us (8192 x 5120 x
+// 10240 by one tile alone: 1.29, 1.76 and 2.37 ms).
 constexpr size_t kTileFloats[3] = {256 * 256, 128 * 128, 64 * 128};
 struct Choice {
   int tile;
@@ -749,7 +760,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void gated_few_kernel(GatedArgs p) 
 }
 
 // d_up = dh act(gate), d_gate = dh up act'(gate), 8 values a thread. Rounded to bf16,
-// which is their type as outputs and as operands of the products.
+// which is their type as outputs and as operands of the products. Bound by memory: 4096 x
+// 10240 65 to 75 us, 420 MB at 5.6 to 6.4 TB/s. As the products' own operands,
+// each of their tiles would compute its part again: 20 times with 5120 columns of x.
 template <bool GELU>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedBwdArgs p) {
   const int64_t n8 = (int64_t)p.T * p.F / 8, stride = (int64_t)gridDim.x * 256;
