@@ -998,7 +998,7 @@ def lora(x, a, b, plan, *, scale=None, base=None, out=None, return_v=False, work
 
     x [T, K], a [E, R, K], b [E, N, R] bf16, R (8 to 128), K and N multiples of 8;
     scale [E] fp32 (None: 1); base [T, N] bf16, such as mx4_linear()'s result (None:
-    0); ``out`` may be given, also base itself. Returns dict(out: [T, N] bf16, v: [T, R]
+    0); ``out`` may be given, also base or x itself. Returns dict(out: [T, N] bf16, v: [T, R]
     fp32 for lora_backward(), None without ``return_v``)."""
     T, K = x.shape
     dev = x.device
@@ -1026,7 +1026,7 @@ def lora_backward(dy, x, v, a, b, plan, *, scale=None, base=None, dx=None, input
     """Gradients of lora() from its stored ``v`` and the gradient ``dy`` of out (which
     is also base's): dv = scale[i] b[i]^T dy, dx = base + a[i]^T dv (base [T, K] bf16: the
     gradient that reaches x through the shared projection, None: 0; ``dx`` may be
-    given, also base itself), d_a[i] and d_b[i] summed over the tokens of adapter i.
+    given, also base, dy or x itself), d_a[i] and d_b[i] summed over the tokens of adapter i.
     Returns dict(dx: [T, K] bf16, None without ``input_grad``; d_a, d_b: bf16, shapes
     of a and b, None without ``weight_grad``)."""
     T, K = x.shape

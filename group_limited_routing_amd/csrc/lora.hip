@@ -779,7 +779,6 @@ hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
   into_rank(p.dy, bt, p.plan, p.T, p.E, p.R, p.N, part, st);
   lora_operands_kernel<<<dim3(l.tiles, p.da ? 2 : 1), 256, p.R * 66 * 4, st>>>(
       part, parts_of(l.tiles, p.N), p.v, p.scale, p.plan, p.T, p.E, p.R, dv, p.da ? dvt : nullptr, vt);
-  if (p.dx) out_of_rank({dv, at, nullptr, p.plan, p.base, p.dx, nullptr, 1, p.T, p.E, p.R, p.K, 0}, st);
   if (p.da) {
     const LoraGradArgs a{{dvt, vt}, {p.x, p.dy}, {p.da, p.db},
                          {(float*)(ws + w.part_a), (float*)(ws + w.part_b)}, p.plan, p.T, p.E, p.R, {p.K, p.N}};
@@ -790,6 +789,8 @@ hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
       lora_grad_kernel<2><<<grid_of(l.chunks, wgs * ((p.R + 31) / 32)), 256, 0, st>>>(a);
     lora_grad_sum_kernel<<<dim3((p.R * (p.K + p.N) / 8 + 255) / 256, p.E), 256, 0, st>>>(a);
   }
+  // last: dx may be the memory of dy or x
+  if (p.dx) out_of_rank({dv, at, nullptr, p.plan, p.base, p.dx, nullptr, 1, p.T, p.E, p.R, p.K, 0}, st);
   return hipGetLastError();
 }
 

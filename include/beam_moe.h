@@ -663,7 +663,8 @@ beam_status beam_moe_lora_plan(const int32_t* index, int32_t T, int32_t n_adapte
  *   x      [T, k] bf16;  a [n_adapters, rank, k] bf16;  b [n_adapters, n, rank] bf16.
  *   scale  [n_adapters] fp32 or NULL (1).
  *   plan   of beam_moe_lora_plan.
- *   base   [T, n] bf16 or NULL (0);  out [T, n] bf16. May be the same memory.
+ *   base   [T, n] bf16 or NULL (0);  out [T, n] bf16. out may be the same memory as base or
+ *          (n == k) x.
  *   v      out [T, rank] fp32 or NULL (the gradient needs it).
  *   workspace  beam_moe_lora_workspace_bytes(cfg, T).
  * Supported: rank in [8, 128], k in [8, 65536], n in [8, 262144], multiples of 8; dtype
@@ -692,7 +693,7 @@ beam_status beam_moe_lora(const beam_moe_lora_config* cfg, int32_t T, const void
  *   dy   [T, n] bf16;  x, a, b, scale, plan as above;  v [T, rank] fp32 (x and v only
  *        for the adapters' gradients).
  *   base [T, k] bf16 or NULL: gradient that reaches x on another way;  dx out [T, k]
- *        bf16 or NULL. May be the same memory.
+ *        bf16 or NULL. dx may be the same memory as base, x or (n == k) dy.
  *   d_a, d_b  out, shapes of a and b, bf16, or both NULL. With T == 0 they are left as
  *        they were.
  *   workspace  beam_moe_lora_backward_workspace_bytes(cfg, T).

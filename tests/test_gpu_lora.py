@@ -299,3 +299,28 @@ def test_no_tokens():
     assert fw["out"].shape == (0, 32) and fw["v"].shape == (0, 8)
     bw = gl.lora_backward(p["dy"], p["x"], fw["v"], p["a"], p["b"], plan)
     assert bw["dx"].shape == (0, 64) and not bw["d_a"].any() and not bw["d_b"].any()
+
+
+@pytest.mark.parametrize("R", [16, 64])
+@pytest.mark.parametrize("T", [70, 2100])
+def test_residual_in_place(T, R):
+    """out = x + s B A x in x's own memory, and its gradient in dy's: base and the result
+    are also the operand."""
+    N, E = 264, 3
+    p, index = _inputs(T, N, N, R, E), _index(T, E, "mixed", T)
+    plan = gl.lora_plan(index, E)
+    x, dy = p["x"], p["dy"]
+    a, b, scale = p["a"], p["b"], p["scale"]
+    want = gl.lora(x, a, b, plan, scale=scale, base=x, return_v=True)
+    x2 = x.clone()
+    got = gl.lora(x2, a, b, plan, scale=scale, base=x2, out=x2, return_v=True)
+    assert torch.equal(x2, want["out"]) and torch.equal(got["v"], want["v"])
+    want = gl.lora_backward(dy, x, got["v"], a, b, plan, scale=scale, base=dy)
+    dy2 = dy.clone()
+    got2 = gl.lora_backward(dy2, x, got["v"], a, b, plan, scale=scale, base=dy2, dx=dy2)
+    assert torch.equal(dy2, want["dx"])
+    x3 = x.clone()
+    got3 = gl.lora_backward(dy, x3, got["v"], a, b, plan, scale=scale, base=dy, dx=x3)
+    assert torch.equal(x3, want["dx"])
+    for g in (got2, got3):
+        assert torch.equal(g["d_a"], want["d_a"]) and torch.equal(g["d_b"], want["d_b"])
