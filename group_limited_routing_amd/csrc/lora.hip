@@ -420,12 +420,19 @@ __global__ __launch_bounds__(256, RB <= 4 ? 2 : 1) void lora_out_kernel(LoraOutA
 }
 
 // ------------------------------------------------------------------ gradients
-// a [E, R, K] -> [E, K, R] and b [E, N, R] -> [E, R, N], 64 x 64 blocks through LDS.
+// a [E, R, K] -> [E, K, R] and b [E, N, R] -> [E, R, N], 64 x 64 blocks through LDS, of
+// the adapters that have tokens; zeros in the gradients of the others.
 __global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __restrict__ a,
-                                                             const uint16_t* __restrict__ b, int E, int R, int K,
-                                                             int N, uint16_t* __restrict__ at,
-                                                             uint16_t* __restrict__ bt) {
+                                                             const uint16_t* __restrict__ b,
+                                                             const int32_t* __restrict__ plan, int T, int E, int R,
+                                                             int K, int N, uint16_t* __restrict__ at,
+                                                             uint16_t* __restrict__ bt, uint16_t* __restrict__ da,
+                                                             uint16_t* __restrict__ db) {
   __shared__ uint16_t tile[64][72];
+  const LoraPlanLayout l(T, E);
+  const int32_t* chunks = plan + l.o_first + blockIdx.y;
+  const bool used = chunks[0] != chunks[1];
+  if (!used && !da) return;
   const int rb = (R + 63) / 64, kb = (K + 63) / 64, nb = (N + 63) / 64;
   int i = blockIdx.x;
   const bool of_a = i < rb * kb;
@@ -434,6 +441,14 @@ __global__ __launch_bounds__(256) void lora_transpose_kernel(const uint16_t* __r
   const uint16_t* src = (of_a ? a : b) + (size_t)blockIdx.y * rows * cols;
   uint16_t* dst = (of_a ? at : bt) + (size_t)blockIdx.y * rows * cols;
   const int r0 = i / cb * 64, c0 = i % cb * 64;
+  if (!used) {
+    uint16_t* grad = (of_a ? da : db) + (size_t)blockIdx.y * rows * cols;
+    for (int q = threadIdx.x; q < 512; q += 256) {
+      const int r = r0 + q / 8, c = c0 + q % 8 * 8;
+      if (r < rows && c < cols) st16(grad + (size_t)r * cols + c, u32x4{0, 0, 0, 0});
+    }
+    return;
+  }
   for (int q = threadIdx.x; q < 512; q += 256) {
     const int r = r0 + q / 8, c = c0 + q % 8 * 8;
     if (r < rows && c < cols) {
@@ -648,13 +663,12 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
   }
 }
 
-// The sums of adapters with several chunks, in their order, and zeros for those without
-// tokens: 8 values a thread. 6 to 7 us for 21 MB (8 chunks of rank 64, 5120 + 5120 columns).
+// The sums of adapters with several chunks, in their order: 8 values a thread. 6 to 7 us for 21 MB (8 chunks of rank 64, 5120 + 5120 columns).
 __global__ __launch_bounds__(256) void lora_grad_sum_kernel(LoraGradArgs p) {
   const LoraPlanLayout at(p.T, p.E);
   const int e = blockIdx.y;
   const int first = p.plan[at.o_first + e], n = p.plan[at.o_first + e + 1] - first;
-  if (n == 1) return;
+  if (n <= 1) return;
   const int slot = p.plan[at.o_slot + e], R = p.R;
   int i = blockIdx.x * 256 + threadIdx.x;
   const int n0 = R * (p.C[0] / 8), n1 = (R / 8) * p.C[1];
@@ -775,7 +789,8 @@ hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
   float *part = (float*)(ws + w.part), *dv = (float*)(ws + w.dv);
   uint16_t *dvt = (uint16_t*)(ws + w.dvt), *vt = (uint16_t*)(ws + w.vt);
   const int blocks = (p.R + 63) / 64 * ((p.K + 63) / 64 + (p.N + 63) / 64);
-  lora_transpose_kernel<<<dim3(blocks, p.E), 256, 0, st>>>(p.a, p.b, p.E, p.R, p.K, p.N, at, bt);
+  lora_transpose_kernel<<<dim3(blocks, p.E), 256, 0, st>>>(p.a, p.b, p.plan, p.T, p.E, p.R, p.K, p.N, at, bt, p.da,
+                                                               p.db);
   into_rank(p.dy, bt, p.plan, p.T, p.E, p.R, p.N, part, st);
   lora_operands_kernel<<<dim3(l.tiles, p.da ? 2 : 1), 256, p.R * 66 * 4, st>>>(
       part, parts_of(l.tiles, p.N), p.v, p.scale, p.plan, p.T, p.E, p.R, dv, p.da ? dvt : nullptr, vt);
@@ -787,7 +802,8 @@ hipError_t launch_lora_backward(const LoraBwdArgs& p, hipStream_t st) {
       lora_grad_kernel<1><<<grid_of(l.chunks, wgs), 256, 0, st>>>(a);
     else
       lora_grad_kernel<2><<<grid_of(l.chunks, wgs * ((p.R + 31) / 32)), 256, 0, st>>>(a);
-    lora_grad_sum_kernel<<<dim3((p.R * (p.K + p.N) / 8 + 255) / 256, p.E), 256, 0, st>>>(a);
+    if (l.slots > 0)
+      lora_grad_sum_kernel<<<dim3((p.R * (p.K + p.N) / 8 + 255) / 256, p.E), 256, 0, st>>>(a);
   }
   // last: dx may be the memory of dy or x
   if (p.dx) out_of_rank({dv, at, nullptr, p.plan, p.base, p.dx, nullptr, 1, p.T, p.E, p.R, p.K, 0}, st);
