@@ -538,7 +538,7 @@ struct LoraGradArgs {
 // are r, columns c, the reduction runs over 32 tokens. Lane (l, g) loads columns 8 l .. + 7
 // of tokens 8 g .. + 7, whole 256-byte runs of a row, and turns them in its registers into
 // fragment j of column 8 l + j, whose reduction values are its 8 tokens. Rank 64, 8191 tokens,
-// 5120 + 5120 columns: 64 us. The rows (168 MB) come twice, for two blocks of 32 ranks (one block
+// 5120 + 5120 columns: 57 us. The rows (168 MB) come twice, for two blocks of 32 ranks (one block
 // of 64 spilled registers); the second time from the XCD's L2 (70% of its reads hit).
 template <int RB>
 __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
@@ -663,7 +663,7 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
   }
 }
 
-// The sums of adapters with several chunks, in their order: 8 values a thread. 6 to 7 us for 21 MB (8 chunks of rank 64, 5120 + 5120 columns).
+// The sums of adapters with several chunks, in their order: 8 values a thread. 6 to 8 us for 21 MB (8 chunks of rank 64, 5120 + 5120 columns).
 __global__ __launch_bounds__(256) void lora_grad_sum_kernel(LoraGradArgs p) {
   const LoraPlanLayout at(p.T, p.E);
   const int e = blockIdx.y;
