@@ -324,3 +324,24 @@ def test_residual_in_place(T, R):
     assert torch.equal(x3, want["dx"])
     for g in (got2, got3):
         assert torch.equal(g["d_a"], want["d_a"]) and torch.equal(g["d_b"], want["d_b"])
+
+
+@pytest.mark.parametrize("T", [5, 1030])
+@pytest.mark.parametrize("K,N,R", [(72, 136, 8), (200, 72, 72)])
+def test_adapters_without_tokens(T, K, N, R):
+    """Their gradients are zeros in memory that held other values, whether an adapter can
+    have several chunks of tokens or not."""
+    E, dev, L = 40, _dev(), gl.lib()
+    p = _inputs(T, K, N, R, E)
+    index = (torch.arange(T) % 3 * 7).to(torch.int32).to(dev)  # adapters 0, 7 and 14
+    plan = gl.lora_plan(index, E)
+    v = gl.lora(p["x"], p["a"], p["b"], plan, return_v=True)["v"]
+    cfg = ctypes.byref(gl.BeamMoeLoraConfig(K, N, R, E, gl.BEAM_BF16))
+    ws = torch.full((L.beam_moe_lora_backward_workspace_bytes(cfg, T),), 255, dtype=torch.uint8, device=dev)
+    da, db = (torch.full_like(p[k], float("nan")) for k in "ab")
+    assert L.beam_moe_lora_backward(cfg, T, p["dy"].data_ptr(), p["x"].data_ptr(), v.data_ptr(), p["a"].data_ptr(),
+                                    p["b"].data_ptr(), None, plan.buffer.data_ptr(), None, None, da.data_ptr(),
+                                    db.data_ptr(), ws.data_ptr(), ws.numel(), None) == gl.BEAM_OK
+    idle = torch.tensor([e not in (0, 7, 14) for e in range(E)], device=dev)
+    for g in (da, db):
+        assert (g[idle] == 0).all() and not g.isnan().any() and (g[~idle] != 0).any()
