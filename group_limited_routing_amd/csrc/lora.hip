@@ -172,10 +172,11 @@ __device__ __forceinline__ void each_sum(int count, int parts, size_t pitch, Fro
     go(std::integral_constant<int, kMaxParts>{});
 }
 
-// v as the sum of two bf16 values, 16 significant bits; beyond the largest bf16 number,
-// and for NaN, the first alone.
+// v as the sum of two bf16 values, 16 significant bits (a finite v that would round beyond the
+// largest bf16 number is that number and the rest); an infinity or a NaN is the first alone.
 __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
   hi = f32_to_bf16_bits(v);
+  if ((hi & 0x7fffu) == 0x7f80u && (__float_as_uint(v) & 0x7fffffffu) != 0x7f800000u) --hi;
   const float rest = v - bf16_bits_to_f32(hi);
   lo = (hi & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_bits(rest);
 }
