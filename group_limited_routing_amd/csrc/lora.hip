@@ -181,6 +181,22 @@ __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
   lo = (hi & 0x7f80u) == 0x7f80u ? 0u : f32_to_bf16_bits(rest);
 }
 
+// Eight bf16 values with zeros for infinities and NaN. The second part of a v is 0 or of either
+// sign, so its product with an infinity would turn the first part's into a NaN: it gets these.
+// lora_out_kernel looks for them among the adapter's values before it multiplies, at 4 RB products
+// with zeros for 64 columns (rank 16: 120 us, so 119; rank 64, gradient: 168, so 165; smallest
+// calls 0.3 us). lora_grad_kernel, which holds no operand for long, makes a sum again that came
+// out as a NaN.
+__device__ __forceinline__ u32x4 finite(u32x4 m) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t low = (m[i] & 0x7f80u) == 0x7f80u ? 0u : m[i] & 0xffffu;
+    const uint32_t high = (m[i] & 0x7f800000u) == 0x7f800000u ? 0u : m[i] & 0xffff0000u;
+    m[i] = low | high;
+  }
+  return m;
+}
+
 // ------------------------------------------------------------------ into the rank
 // part[ks][position][r] = sum over a part of k of x[t, k] m[e][r, k]: a workgroup per
 // tile of tokens and part of k, its waves take 128 values of k in turn, and the four
@@ -345,6 +361,27 @@ __device__ __forceinline__ void rank_out(const LoraOutArgs& p, const int4& tile,
   __syncthreads();
   for (; nb < n1; nb += 256) {
     u32x4 w[TB][2];
+    // products with zeros tell whether an infinity or a NaN is among the adapter's values
+    f32x4 zero[2][2] = {};
+#pragma unroll
+    for (int s = 0; s < RB; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) zero[i][j] = mfma_bf16(as_bf16x8(mf[s][i][j]), as_bf16x8(u32x4{}), zero[i][j]);
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) bad |= __builtin_isunordered(zero[i][0][q], zero[i][1][q]);
+    if (__builtin_expect(__ballot(bad) != 0, 0))
+#pragma unroll
+      for (int s = 0; s < RB; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (s * 32 + g * 8 >= R) mf[s][i][j] = finite(mf[s][i][j]);
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
       f32x4 acc[2][2] = {};
@@ -565,6 +602,13 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
 #pragma unroll
   for (int q = 0; q < RB; ++q)
     ops[q] = op + (size_t)min(r0 + q * 16 + l, R - 1) * at.padded + chunk.w + g * 8;
+  auto turn = [](const u32x4 (&x)[8], u32x4 (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[j][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+  };
   f32x4 acc[RB][8] = {};
   for (int p0 = 0; p0 < chunk.z; p0 += 512) {
     __syncthreads();
@@ -597,11 +641,7 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
           if (s + g * 8 + i >= n) x[i] = u32x4{0, 0, 0, 0};
       }
       u32x4 f[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          f[j][i] = __builtin_amdgcn_perm(x[2 * i + 1][j / 2], x[2 * i][j / 2], j % 2 ? 0x07060302u : 0x05040100u);
+      turn(x, f);
       __builtin_amdgcn_sched_barrier(0);
       if (s + 128 < n) load_x(s + 128);
       __builtin_amdgcn_sched_barrier(0);
@@ -615,6 +655,48 @@ __global__ __launch_bounds__(256, 2) void lora_grad_kernel(LoraGradArgs p) {
       __builtin_amdgcn_sched_barrier(0);
       if (s + 128 < n) load_a(s + 128);
       __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  bool nan = false;
+#pragma unroll
+  for (int q = 0; q < RB; ++q)
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nan |= __builtin_isunordered(acc[q][j][i], acc[q][j + 1][i]);
+  if (__builtin_expect(__ballot(nan) != 0, 0)) {
+    // this wave's sum again, a step after the other, by a lane that no loop knows: the pass
+    // above holds nothing for it in registers
+    int lane = threadIdx.x & 63;
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(lane));
+#endif
+    const int l = lane & 15, g = lane >> 4;
+    const uint16_t* from = rows + min((block - (which ? wgs0 : 0)) * 128 + l * 8, C - 8);
+#pragma unroll
+    for (int q = 0; q < RB; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[q][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int s = wave * 32; s < chunk.z; s += 128) {
+      u32x4 x[8], f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = s + g * 8 + i;
+        const int token = p.plan[at.o_order + chunk.y + min(t, chunk.z - 1)];
+        x[i] = t < chunk.z ? ld16(from + (size_t)token * C) : u32x4{0, 0, 0, 0};
+      }
+      turn(x, f);
+#pragma unroll
+      for (int q = 0; q < RB; ++q) {
+        const uint16_t* o = op + (size_t)min(r0 + q * 16 + l, R - 1) * at.padded + chunk.w + g * 8 + s;
+        const u32x4 first = ld16(o), second = ld16(o + lo);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          acc[q][j] = mfma_bf16(as_bf16x8(first), as_bf16x8(f[j]), acc[q][j]);
+          acc[q][j] = mfma_bf16(as_bf16x8(second), as_bf16x8(finite(f[j])), acc[q][j]);
+        }
+      }
     }
   }
   // waves 2 and 3 onto 0 and 1, then 1 onto 0

@@ -658,8 +658,9 @@ beam_status beam_moe_lora_plan(const int32_t* index, int32_t T, int32_t n_adapte
  * Low-rank adapters of many requests beside a projection that they share, such as
  * beam_moe_mx4_linear's: for a token with adapter i
  *   v = a[i] x;  out = base + scale[i] b[i] v,
- * and for a token without one v = 0, out = base. Sums are fp32; v goes into the second
- * product as a sum of two bf16 values (16 significant bits).
+ * and for a token without one v = 0, out = base. Sums are fp32; scale[i] v (fp32) goes into
+ * the second product as a sum of two bf16 values (16 significant bits), infinities and NaN as
+ * the formula has them.
  *   x      [T, k] bf16;  a [n_adapters, rank, k] bf16;  b [n_adapters, n, rank] bf16.
  *   scale  [n_adapters] fp32 or NULL (1).
  *   plan   of beam_moe_lora_plan.

@@ -1,5 +1,5 @@
 """The adapters at the ends of the number range, against oracle.mlp in float64: a v beyond
-the largest bf16 number."""
+the largest bf16 number, and infinities in the rows and the adapters."""
 
 import numpy as np
 import pytest
@@ -82,3 +82,26 @@ def test_v_beyond_the_largest_bf16(R, sign):
     _, bw = _check(x, a, b, index, dy, v=v)
     assert bw["dx"][0, 0] == sign * np.inf and torch.isfinite(bw["dx"][0, 1:]).all()
     assert bw["d_a"][0, 0, 0] == sign * np.inf and torch.isfinite(bw["d_a"][0, 0, 1:]).all()
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf])
+@pytest.mark.parametrize("where", ["x", "a", "b", "dy"])
+@pytest.mark.parametrize("T,R,whole", [(5, 8, True), (70, 16, False), (1100, 24, True), (1100, 64, False),
+                                       (40, 128, False)])
+def test_infinite_operands(T, R, whole, where, value):
+    """One infinity in a row or an adapter: infinities of the definition's sign, not NaN, in
+    what it reaches, and nothing else changes. v and dv of few bits (``whole``, so that a
+    second part of them is 0) and of many (so that it has either sign)."""
+    K, N, E = 24, 40, 2
+    rng = np.random.default_rng(T + R)
+    # whole numbers from 1 to 3 of either sign: sums below 2^8 of the K products of a v
+    some = lambda *s: (rng.integers(1, 4, s) * rng.choice([-1.0, 1.0], s)) if whole else rng.standard_normal(s)
+    p = dict(x=some(T, K), a=some(E, R, K), b=some(E, N, R), dy=some(T, N))
+    index = rng.integers(-1, E, T)
+    index[T // 2] = 0
+    v = some(T, R)
+    p[where][{"x": (T // 2, 3), "dy": (T // 2, 37), "a": (0, R - 1, 5), "b": (0, 17, 2)}[where]] = value
+    fw, bw = _check(p["x"], p["a"], p["b"], index, p["dy"], v=v)
+    hit = {"x": (bw["d_a"][0, :, 3],), "dy": (bw["d_b"][0, 37],), "a": (fw["out"][T // 2], bw["dx"][T // 2, 5]),
+           "b": (fw["out"][T // 2, 17], bw["dx"][T // 2])}[where]
+    assert any(t.isinf().any() for t in hit)
