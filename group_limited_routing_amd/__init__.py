@@ -132,6 +132,7 @@ class BeamMoeGated(ctypes.Structure):
         ("intermediate", ctypes.c_int32),
         ("activation", ctypes.c_int32),
         ("dtype", ctypes.c_int32),
+        ("pre_f32", ctypes.c_int32),
     ]
 
 
@@ -888,18 +889,19 @@ def mx4_linear(x, x_scale, w, w_scale, *, out_dtype=torch.bfloat16, out=None, st
 
 
 def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=None,
-                 return_pre=False, workspace=None, stream=None):
+                 return_pre=False, pre_dtype=torch.bfloat16, workspace=None, stream=None):
     """The gated product of a dense MLP in one kernel: gate = x w_gate^T + add_gate,
     up = x w_up^T + add_up, h = act(gate) * up, act "silu" or "gelu" (g Phi(g)).
 
     x [T, H], w_gate and w_up [F, H], add_gate and add_up [T, F] (an adapter's share,
     as from lora(); may be None), all bf16, H and F multiples of 8. Returns dict(h:
-    [T, F] bf16, gate, up: [T, F] bf16 for gated_linear_backward(), None without
-    ``return_pre``)."""
+    [T, F] bf16, gate, up: [T, F] for gated_linear_backward(), in ``pre_dtype``, bf16 or
+    fp32, None without ``return_pre``). From bf16 ones d_gate has an absolute error of
+    2^-8 |dh up gate act''(gate)|, all of it near a zero of act' (silu: gate = -1.28)."""
     T, H = x.shape
     F = w_gate.shape[0]
     dev = x.device
-    cfg = _gated_config(x, w_gate, w_up, activation, dev)
+    cfg = _gated_config(x, w_gate, w_up, activation, pre_dtype, dev)
     for t, name in ((add_gate, "add_gate"), (add_up, "add_up")):
         if t is not None:
             _check(t, name, (T, F), _BF16, dev)
@@ -907,7 +909,7 @@ def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=No
     with _on(dev, stream):
         h = torch.empty(T, F, dtype=torch.bfloat16, device=dev)
         if return_pre:
-            gate, up = torch.empty_like(h), torch.empty_like(h)
+            gate, up = (torch.empty_like(h, dtype=pre_dtype) for _ in range(2))
         need = int(lib().beam_moe_gated_linear_workspace_bytes(ctypes.byref(cfg), T))
         workspace = _scratch(workspace, need, dev) if need else None
         _launch("beam_moe_gated_linear", dev, lib().beam_moe_gated_linear, ctypes.byref(cfg), T,
@@ -918,16 +920,17 @@ def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=No
 
 def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", input_grad=True,
                           weight_grad=True, workspace=None, stream=None):
-    """Gradients of gated_linear() from its stored ``gate`` and ``up`` and the gradient
-    ``dh`` of h. Returns dict(d_gate, d_up: [T, F] bf16, also the gradients of add_gate
+    """Gradients of gated_linear() from its stored ``gate`` and ``up`` (both bf16 or both
+    fp32) and the gradient ``dh`` of h. Sums are fp32; d_gate and d_up are rounded to
+    bf16 once, as outputs and as the products' operands. Returns dict(d_gate, d_up: [T, F] bf16, also the gradients of add_gate
     and add_up; dx: [T, H] bf16, None without ``input_grad``; d_w_gate, d_w_up: [F, H]
     bf16, None without ``weight_grad``)."""
     T, H = x.shape
     F = w_gate.shape[0]
     dev = x.device
-    cfg = _gated_config(x, w_gate, w_up, activation, dev)
-    for t, name in ((dh, "dh"), (gate, "gate"), (up, "up")):
-        _check(t, name, (T, F), _BF16, dev)
+    cfg = _gated_config(x, w_gate, w_up, activation, gate.dtype, dev)
+    for t, name, dtype in ((dh, "dh", torch.bfloat16), (gate, "gate", gate.dtype), (up, "up", gate.dtype)):
+        _check(t, name, (T, F), (dtype,), dev)
     dx = dwg = dwu = None
     with _on(dev, stream):
         dg, du = torch.empty_like(dh), torch.empty_like(dh)
@@ -946,9 +949,11 @@ def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", i
     return {"dx": dx, "d_w_gate": dwg, "d_w_up": dwu, "d_gate": dg, "d_up": du}
 
 
-def _gated_config(x, w_gate, w_up, activation, dev):
+def _gated_config(x, w_gate, w_up, activation, pre_dtype, dev):
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation is {activation!r}, expected one of {tuple(_ACTIVATIONS)}")
+    if pre_dtype not in _FLOATS:
+        raise ValueError(f"gate and up have dtype {pre_dtype}, expected one of {_FLOATS}")
     T, H = x.shape
     F = w_gate.shape[0]
     _check(x, "x", (T, H), _BF16, dev)
@@ -958,7 +963,7 @@ def _gated_config(x, w_gate, w_up, activation, dev):
     # before outputs of F columns are allocated; the library checks the rest
     if H % 8 or F % 8:
         raise BeamMoeError(BEAM_ERR_SHAPE, "beam_moe_gated_linear")
-    return BeamMoeGated(H, F, _ACTIVATIONS[activation], BEAM_BF16)
+    return BeamMoeGated(H, F, _ACTIVATIONS[activation], BEAM_BF16, pre_dtype == torch.float32)
 
 
 class LoraPlan:

@@ -80,7 +80,9 @@ struct TileArgs {
   int M, N, K;       // N: columns of the output; K: of one of the two sums of kInput
   const uint16_t* add_gate;
   const uint16_t* add_up;
-  uint16_t* out[3];  // h, gate, up; or the output of each of two products
+  uint16_t* out[2];  // h; or the output of each of two products
+  void* pre[2];      // gate and up, bf16 or fp32, or null
+  bool pre_f32;
   // The first `whole` tiles are one item of work each; the others are cut into `splits`
   // ranges of k, whose sums go to part[item - whole], a tile each.
   int whole, items, splits;
@@ -455,8 +457,24 @@ __device__ __forceinline__ void tile_work(const TileArgs& p, int block, int bloc
         if (p.add_up) add(up_add, j1);
         if constexpr (I + 1 < FM) fetch(I + 1);
         put(p.out[0], [&](int j, int i) { return activation<GELU>(acc[I][2 * j][i]) * acc[I][2 * j + 1][i]; });
-        if (p.out[1]) put(p.out[1], [&](int j, int i) { return acc[I][2 * j][i]; });
-        if (p.out[2]) put(p.out[2], [&](int j, int i) { return acc[I][2 * j + 1][i]; });
+        auto keep = [&](void* out, auto which) {  // gate (0) or up (1)
+          constexpr int W = decltype(which)::value;
+          if (!p.pre_f32) return put((uint16_t*)out, [&](int j, int i) { return acc[I][2 * j + W][i]; });
+          // fp32: 32 bytes of a row from two lanes, straight from the sums
+          if (mb + r < p.M)
+#pragma unroll
+            for (int j = 0; j < COLS / 32; ++j)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int c = c0 + j * 32 + 8 * q + 4 * h;
+                const f32x16& v = acc[I][2 * j + W];
+                if (c < p.N)
+                  *reinterpret_cast<f32x4*>((float*)out + (size_t)(mb + r) * p.N + c) =
+                      f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+              }
+        };
+        if (p.pre[0]) keep(p.pre[0], j0);
+        if (p.pre[1]) keep(p.pre[1], j1);
       } else {
         put(p.out[t.problem], [&](int j, int i) { return acc[I][j][i]; });
       }
@@ -548,8 +566,14 @@ __global__ __launch_bounds__(64) void finish_kernel(TileArgs p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = activation<GELU>(g[i]) * u[i];
     put8(p.out[0] + to, f);
-    if (p.out[1]) put8(p.out[1] + to, g);
-    if (p.out[2]) put8(p.out[2] + to, u);
+    auto keep = [&](void* out, const float (&v)[8]) {
+      if (!p.pre_f32) return put8((uint16_t*)out + to, v);
+      f32x4* at = reinterpret_cast<f32x4*>((float*)out + to);
+      at[0] = f32x4{v[0], v[1], v[2], v[3]};
+      at[1] = f32x4{v[4], v[5], v[6], v[7]};
+    };
+    if (p.pre[0]) keep(p.pre[0], g);
+    if (p.pre[1]) keep(p.pre[1], u);
   } else {
     sum8(c, g);
     put8((problem ? p.out[1] : p.out[0]) + to, g);
@@ -755,19 +779,33 @@ __global__ __launch_bounds__(64 * kFewWaves) void gated_few_kernel(GatedArgs p) 
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = activation<GELU>(gate[e]) * up[e];
   put(p.h, h);
-  if (p.gate) put(p.gate, gate);
-  if (p.up) put(p.up, up);
+  auto keep = [&](void* to, const f32x4& v) {
+    if (p.pre_f32)
+      *reinterpret_cast<f32x4*>((float*)to + at) = v;
+    else
+      put((uint16_t*)to, v);
+  };
+  if (p.gate) keep(p.gate, gate);
+  if (p.up) keep(p.up, up);
 }
 
 // d_up = dh act(gate), d_gate = dh up act'(gate), 8 values a thread. Rounded to bf16,
 // which is their type as outputs and as operands of the products. Bound by memory: 4096 x
 // 10240 65 to 75 us, 420 MB at 5.6 to 6.4 TB/s. As the products' own operands,
 // each of their tiles would compute its part again: 20 times with 5120 columns of x.
-template <bool GELU>
+// F32: gate and up are fp32.
+template <bool GELU, bool F32>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedBwdArgs p) {
   const int64_t n8 = (int64_t)p.T * p.F / 8, stride = (int64_t)gridDim.x * 256;
+  constexpr int B = F32 ? 4 : 2, L = F32 ? 2 : 1;  // bytes of a value, loads of 8 of them
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += stride) {
-    const u32x4 dh = ld16(p.dh + i * 8), g = ld16(p.gate + i * 8), u = ld16(p.up + i * 8);
+    const u32x4 dh = ld16(p.dh + i * 8);
+    u32x4 g[L], u[L];
+#pragma unroll
+    for (int k = 0; k < L; ++k) {
+      g[k] = ld16((const uint8_t*)p.gate + i * (8 * B) + k * 16);
+      u[k] = ld16((const uint8_t*)p.up + i * (8 * B) + k * 16);
+    }
     u32x4 dg, du;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -775,9 +813,12 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedBwdArgs p) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         auto half = [&](uint32_t v) { return __uint_as_float(e ? v & 0xffff0000u : v << 16); };
+        auto pre = [&](const u32x4 (&v)[L]) {
+          return F32 ? __uint_as_float(v[q / 2 * (L - 1)][q % 2 * 2 + e]) : half(v[0][q]);
+        };
         float d;
-        const float f = activation<GELU>(half(g[q]), d), dhv = half(dh[q]);
-        a[e] = dhv * half(u[q]) * d;
+        const float f = activation<GELU>(pre(g), d), dhv = half(dh[q]);
+        a[e] = dhv * pre(u) * d;
         b[e] = dhv * f;
       }
       dg[q] = pack_bf16x2(a[0], a[1]);
@@ -814,8 +855,9 @@ hipError_t launch_gated_linear(const GatedArgs& a, int gelu, hipStream_t st) {
   t.add_gate = a.add_gate;
   t.add_up = a.add_up;
   t.out[0] = a.h;
-  t.out[1] = a.gate;
-  t.out[2] = a.up;
+  t.pre[0] = a.gate;
+  t.pre[1] = a.up;
+  t.pre_f32 = a.pre_f32;
   t.part = a.part;
   product<kGated>(t, gelu, st);
   return hipGetLastError();
@@ -829,10 +871,17 @@ size_t gated_bwd_workspace_bytes(int T, int H, int F) {
 hipError_t launch_gated_linear_backward(const GatedBwdArgs& a, int gelu, hipStream_t st) {
   const int64_t n8 = (int64_t)a.T * a.F / 8;
   const unsigned grid = (unsigned)std::min<int64_t>((n8 + 255) / 256, 1 << 20);
+  auto go = [&](auto gc) {
+    constexpr bool G = decltype(gc)::value;
+    if (a.pre_f32)
+      gated_grad_kernel<G, true><<<grid, 256, 0, st>>>(a);
+    else
+      gated_grad_kernel<G, false><<<grid, 256, 0, st>>>(a);
+  };
   if (gelu)
-    gated_grad_kernel<true><<<grid, 256, 0, st>>>(a);
+    go(std::true_type{});
   else
-    gated_grad_kernel<false><<<grid, 256, 0, st>>>(a);
+    go(std::false_type{});
   TileArgs in{};
   in.x[0] = (const uint8_t*)a.d_gate;
   in.x[1] = (const uint8_t*)a.d_up;

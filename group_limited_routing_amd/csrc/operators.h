@@ -101,10 +101,11 @@ struct GatedArgs {
   const uint16_t* add_gate;  // [T, F] or null
   const uint16_t* add_up;    // [T, F] or null
   uint16_t* h;               // [T, F]
-  uint16_t* gate;            // [T, F] or null
-  uint16_t* up;              // [T, F] or null
+  void* gate;                // [T, F] bf16, or fp32, or null
+  void* up;                  // as gate
   float* part;               // workspace: sums over parts of H
   int T, H, F;
+  bool pre_f32;              // gate and up are fp32
 };
 size_t gated_workspace_bytes(int T, int H, int F);
 // gelu: the activation is gelu (else silu)
@@ -115,8 +116,8 @@ struct GatedBwdArgs {
   const uint16_t* x;     // [T, H]
   const uint16_t* wg;    // [F, H]
   const uint16_t* wu;    // [F, H]
-  const uint16_t* gate;  // [T, F]
-  const uint16_t* up;    // [T, F]
+  const void* gate;      // [T, F] bf16 or fp32
+  const void* up;        // as gate
   uint16_t* d_gate;      // [T, F]
   uint16_t* d_up;        // [T, F]
   uint16_t* dx;          // [T, H] or null
@@ -124,6 +125,7 @@ struct GatedBwdArgs {
   uint16_t* d_wu;        // [F, H]
   float* part;           // workspace: sums over parts of a product's reduction
   int T, H, F;
+  bool pre_f32;          // gate and up are fp32
 };
 size_t gated_bwd_workspace_bytes(int T, int H, int F);
 hipError_t launch_gated_linear_backward(const GatedBwdArgs& a, int gelu, hipStream_t st);

@@ -64,6 +64,7 @@ beam_status check_linear(const beam_moe_linear* c, int32_t T) {
 beam_status check_gated(const beam_moe_gated* c, int32_t T) {
   if (!c) return BEAM_ERR_NULL;
   if (c->activation != BEAM_ACT_SILU && c->activation != BEAM_ACT_GELU) return BEAM_ERR_CONFIG;
+  if (c->pre_f32 != 0 && c->pre_f32 != 1) return BEAM_ERR_CONFIG;
   if (c->dtype != BEAM_BF16) return BEAM_ERR_DTYPE;
   if (c->hidden < 8 || c->hidden > kMlpMaxH || c->hidden % 8 != 0 || c->intermediate < 8 ||
       c->intermediate > kMlpMaxF || c->intermediate % 8 != 0 || T < 0 || T > kMaxT)
@@ -263,10 +264,14 @@ beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const vo
   const size_t need = beam_moe_gated_linear_workspace_bytes(cfg, T);
   if (need && (!workspace || workspace_bytes < need)) return BEAM_ERR_WORKSPACE;
   if (any_misaligned(x, w_gate, w_up, add_gate, add_up, h, gate, up, workspace)) return BEAM_ERR_ALIGN;
+  // rows of twice the bytes: a workgroup would write over another's shares
+  if (cfg->pre_f32 && ((gate && (gate == add_gate || gate == add_up)) || (up && (up == add_gate || up == add_up))))
+    return BEAM_ERR_CONFIG;
   const GatedArgs a{(const uint16_t*)x,        (const uint16_t*)w_gate, (const uint16_t*)w_up,
                     (const uint16_t*)add_gate, (const uint16_t*)add_up, (uint16_t*)h,
-                    (uint16_t*)gate,           (uint16_t*)up,           (float*)workspace,
-                    T,                         cfg->hidden,             cfg->intermediate};
+                    gate,                      up,                      (float*)workspace,
+                    T,                         cfg->hidden,             cfg->intermediate,
+                    cfg->pre_f32 != 0};
   return launched(launch_gated_linear(a, cfg->activation == BEAM_ACT_GELU, (hipStream_t)stream));
 }
 
@@ -290,11 +295,13 @@ beam_status beam_moe_gated_linear_backward(const beam_moe_gated* cfg, int32_t T,
   if (need && (!workspace || workspace_bytes < need)) return BEAM_ERR_WORKSPACE;
   if (any_misaligned(dh, x, w_gate, w_up, gate, up, d_gate, d_up, dx, d_w_gate, d_w_up, workspace))
     return BEAM_ERR_ALIGN;
-  const GatedBwdArgs a{(const uint16_t*)dh,   (const uint16_t*)x,    (const uint16_t*)w_gate,
-                       (const uint16_t*)w_up, (const uint16_t*)gate, (const uint16_t*)up,
-                       (uint16_t*)d_gate,     (uint16_t*)d_up,       (uint16_t*)dx,
-                       (uint16_t*)d_w_gate,   (uint16_t*)d_w_up,     (float*)workspace,
-                       T,                     cfg->hidden,           cfg->intermediate};
+  if (cfg->pre_f32 && (d_gate == gate || d_gate == up || d_up == gate || d_up == up)) return BEAM_ERR_CONFIG;
+  const GatedBwdArgs a{(const uint16_t*)dh,   (const uint16_t*)x,  (const uint16_t*)w_gate,
+                       (const uint16_t*)w_up, gate,                up,
+                       (uint16_t*)d_gate,     (uint16_t*)d_up,     (uint16_t*)dx,
+                       (uint16_t*)d_w_gate,   (uint16_t*)d_w_up,   (float*)workspace,
+                       T,                     cfg->hidden,         cfg->intermediate,
+                       cfg->pre_f32 != 0};
   return launched(launch_gated_linear_backward(a, cfg->activation == BEAM_ACT_GELU, (hipStream_t)stream));
 }
 

@@ -597,18 +597,22 @@ typedef enum beam_activation {
  *   x                [T, hidden] bf16;  w_gate, w_up [intermediate, hidden] bf16.
  *   add_gate, add_up [T, intermediate] bf16 or NULL (the adapters' shares).
  *   h                out [T, intermediate] bf16.
- *   gate, up         out [T, intermediate] bf16 or NULL: what the gradient needs. May be
- *                    the same memory as add_gate and add_up, each as its own.
+ *   gate, up         out [T, intermediate] or NULL: what the gradient needs, bf16, or
+ *                    fp32 with pre_f32 (near a zero of act' only those leave d_gate its
+ *                    relative accuracy). In bf16 they may be the same memory as
+ *                    add_gate and add_up, each as its own.
  *   workspace        beam_moe_gated_linear_workspace_bytes(cfg, T) (0: none).
  * Supported: hidden in [8, 65536] and intermediate in [8, 262144], multiples of 8;
- * dtype BEAM_BF16. Errors: BEAM_ERR_NULL, BEAM_ERR_CONFIG (activation),
- * BEAM_ERR_SHAPE, BEAM_ERR_DTYPE, BEAM_ERR_WORKSPACE, BEAM_ERR_ALIGN, BEAM_ERR_HIP.
+ * dtype BEAM_BF16. Errors: BEAM_ERR_NULL, BEAM_ERR_CONFIG (activation, pre_f32; fp32
+ * gate and up in the memory of a bf16 argument), BEAM_ERR_SHAPE, BEAM_ERR_DTYPE,
+ * BEAM_ERR_WORKSPACE, BEAM_ERR_ALIGN, BEAM_ERR_HIP.
  */
 typedef struct beam_moe_gated {
   int32_t hidden;
   int32_t intermediate;
   int32_t activation; /* beam_activation */
   int32_t dtype;      /* beam_dtype */
+  int32_t pre_f32;    /* gate and up are fp32 (1) or bf16 (0) */
 } beam_moe_gated;
 
 size_t beam_moe_gated_linear_workspace_bytes(const beam_moe_gated* cfg, int32_t T);
@@ -622,10 +626,11 @@ beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const vo
  * Its gradient, from the stored gate and up:
  *   d_up = dh act(gate);  d_gate = dh up act'(gate), both rounded to bf16, then
  *   dx = d_gate w_gate + d_up w_up;  d_w_gate = d_gate^T x;  d_w_up = d_up^T x.
- *   dh, gate, up     [T, intermediate] bf16;  x, w_gate, w_up as above (x only for the
- *                    weights' gradients, the weights only for dx).
+ *   dh, gate, up     [T, intermediate], dh bf16, gate and up as stored (pre_f32);  x,
+ *                    w_gate, w_up as above (x only for the weights' gradients, the
+ *                    weights only for dx).
  *   d_gate, d_up     out [T, intermediate] bf16 (the adapters' gradients start from
- *                    them). May be the same memory as gate and up, or dh.
+ *                    them). May be the same memory as bf16 gate and up, or dh.
  *   dx               out [T, hidden] bf16 or NULL.
  *   d_w_gate, d_w_up out [intermediate, hidden] bf16, or both NULL. With T == 0 they
  *                    are left as they were.
