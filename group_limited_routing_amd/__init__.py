@@ -901,7 +901,7 @@ def gated_linear(x, w_gate, w_up, *, activation="silu", add_gate=None, add_up=No
     T, H = x.shape
     F = w_gate.shape[0]
     dev = x.device
-    cfg = _gated_config(x, w_gate, w_up, activation, pre_dtype, dev)
+    cfg = _gated_config(x, w_gate, w_up, activation, pre_dtype, dev, T)
     for t, name in ((add_gate, "add_gate"), (add_up, "add_up")):
         if t is not None:
             _check(t, name, (T, F), _BF16, dev)
@@ -924,11 +924,13 @@ def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", i
     fp32) and the gradient ``dh`` of h. Sums are fp32; d_gate and d_up are rounded to
     bf16 once, as outputs and as the products' operands. Returns dict(d_gate, d_up: [T, F] bf16, also the gradients of add_gate
     and add_up; dx: [T, H] bf16, None without ``input_grad``; d_w_gate, d_w_up: [F, H]
-    bf16, None without ``weight_grad``)."""
-    T, H = x.shape
-    F = w_gate.shape[0]
-    dev = x.device
-    cfg = _gated_config(x, w_gate, w_up, activation, gate.dtype, dev)
+    bf16, None without ``weight_grad``). x may be None without ``weight_grad``."""
+    if x is None and weight_grad:
+        raise ValueError("x is None, which the weights' gradients need")
+    T = dh.shape[0]
+    F, H = w_gate.shape
+    dev = dh.device
+    cfg = _gated_config(x, w_gate, w_up, activation, gate.dtype, dev, T)
     for t, name, dtype in ((dh, "dh", torch.bfloat16), (gate, "gate", gate.dtype), (up, "up", gate.dtype)):
         _check(t, name, (T, F), (dtype,), dev)
     dx = dwg = dwu = None
@@ -938,7 +940,7 @@ def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", i
         if input_grad or weight_grad:
             need = int(lib().beam_moe_gated_linear_backward_workspace_bytes(ctypes.byref(cfg), T))
         if input_grad:
-            dx = torch.empty_like(x)
+            dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
         if weight_grad:  # no rows: the sums over them are 0
             dwg, dwu = ((torch.empty_like if T else torch.zeros_like)(w) for w in (w_gate, w_up))
         workspace = _scratch(workspace, need, dev) if need else None
@@ -949,14 +951,14 @@ def gated_linear_backward(dh, x, w_gate, w_up, gate, up, *, activation="silu", i
     return {"dx": dx, "d_w_gate": dwg, "d_w_up": dwu, "d_gate": dg, "d_up": du}
 
 
-def _gated_config(x, w_gate, w_up, activation, pre_dtype, dev):
+def _gated_config(x, w_gate, w_up, activation, pre_dtype, dev, T):
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation is {activation!r}, expected one of {tuple(_ACTIVATIONS)}")
     if pre_dtype not in _FLOATS:
         raise ValueError(f"gate and up have dtype {pre_dtype}, expected one of {_FLOATS}")
-    T, H = x.shape
-    F = w_gate.shape[0]
-    _check(x, "x", (T, H), _BF16, dev)
+    F, H = w_gate.shape
+    if x is not None:
+        _check(x, "x", (T, H), _BF16, dev)
     _check(w_gate, "w_gate", (F, H), _BF16, dev)
     _check(w_up, "w_up", (F, H), _BF16, dev)
     _sizes("beam_moe_gated_linear", T, H, F)
@@ -1007,7 +1009,7 @@ def lora(x, a, b, plan, *, scale=None, base=None, out=None, return_v=False, work
     fp32 for lora_backward(), None without ``return_v``)."""
     T, K = x.shape
     dev = x.device
-    cfg = _lora_config("beam_moe_lora", x, a, b, plan, scale, dev)
+    cfg = _lora_config("beam_moe_lora", x, a, b, plan, scale, dev, T)
     N, R = cfg.n, cfg.rank
     for t, name in ((base, "base"), (out, "out")):
         if t is not None:
@@ -1033,10 +1035,13 @@ def lora_backward(dy, x, v, a, b, plan, *, scale=None, base=None, dx=None, input
     gradient that reaches x through the shared projection, None: 0; ``dx`` may be
     given, also base, dy or x itself), d_a[i] and d_b[i] summed over the tokens of adapter i.
     Returns dict(dx: [T, K] bf16, None without ``input_grad``; d_a, d_b: bf16, shapes
-    of a and b, None without ``weight_grad``)."""
-    T, K = x.shape
-    dev = x.device
-    cfg = _lora_config("beam_moe_lora_backward", x, a, b, plan, scale, dev)
+    of a and b, None without ``weight_grad``). x and v may be None without
+    ``weight_grad``."""
+    if x is None and weight_grad:
+        raise ValueError("x is None, which the adapters' gradients need")
+    T, K = dy.shape[0], a.shape[2]
+    dev = dy.device
+    cfg = _lora_config("beam_moe_lora_backward", x, a, b, plan, scale, dev, T)
     _check(dy, "dy", (T, cfg.n), _BF16, dev)
     if weight_grad:
         _check(v, "v", (T, cfg.rank), _F32, dev)
@@ -1048,7 +1053,7 @@ def lora_backward(dy, x, v, a, b, plan, *, scale=None, base=None, dx=None, input
         if not input_grad:
             dx = None
         elif dx is None:
-            dx = torch.empty_like(x)
+            dx = torch.empty(T, K, dtype=torch.bfloat16, device=dev)
         if weight_grad:  # no rows: the sums over them are 0
             da, db = ((torch.empty_like if T else torch.zeros_like)(w) for w in (a, b))
         workspace = _scratch(
@@ -1061,11 +1066,11 @@ def lora_backward(dy, x, v, a, b, plan, *, scale=None, base=None, dx=None, input
     return {"dx": dx, "d_a": da, "d_b": db}
 
 
-def _lora_config(where, x, a, b, plan, scale, dev):
-    T, K = x.shape
-    E, R = a.shape[:2]
+def _lora_config(where, x, a, b, plan, scale, dev, T):
+    E, R, K = a.shape
     N = b.shape[1]
-    _check(x, "x", (T, K), _BF16, dev)
+    if x is not None:
+        _check(x, "x", (T, K), _BF16, dev)
     _check(a, "a", (E, R, K), _BF16, dev)
     _check(b, "b", (E, N, R), _BF16, dev)
     if scale is not None:
