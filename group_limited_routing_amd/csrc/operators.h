@@ -139,7 +139,7 @@ constexpr int kLoraMaxE = 1024;
 // of the adapters, into longer chunks.
 constexpr int kLoraTile = 64;
 struct LoraPlanLayout {
-  int chunk;          // tokens of a chunk: at most 64 chunks of one adapter's tokens, or 1024
+  int chunk;          // tokens of a chunk: 1024, or so many that T tokens make at most 65
   int tiles, chunks;  // at most
   int slots;          // chunks, at most, of adapters that have more than one
   int padded;         // tokens, at most, with every adapter's rounded up to 32
