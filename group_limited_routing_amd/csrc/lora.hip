@@ -17,7 +17,10 @@ constexpr int kPlanWaves = 16;
 constexpr int kMaxParts = 8;  // of a reduction over k
 
 // One workgroup: counts of each wave's part of the tokens, offsets by a scan over
-// the adapters, then each wave places its part in order, so the order is stable.
+// the adapters, then each wave places its part in order, so the order is stable. Bound by latency:
+// a turn for each different adapter among 64 tokens, and the last tile's repeated tokens one by
+// one. 515 tokens in any order of 5 adapters 8 us, 64 of 32 18, 8192 of 8 26 (one after the
+// other 19), 4096 of 64 57, 16384 of 256 265.
 __global__ __launch_bounds__(64 * kPlanWaves) void lora_plan_kernel(const int32_t* __restrict__ index, int T,
                                                                     int E, int32_t* plan) {
   __shared__ int32_t part[kPlanWaves][kLoraMaxE + 1];
@@ -184,8 +187,8 @@ __device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
 // Eight bf16 values with zeros for infinities and NaN. The second part of a v is 0 or of either
 // sign, so its product with an infinity would turn the first part's into a NaN: it gets these.
 // lora_out_kernel looks for them among the adapter's values before it multiplies, at 4 RB products
-// with zeros for 64 columns (rank 16: 120 us, so 119; rank 64, gradient: 168, so 165; smallest
-// calls 0.3 us). lora_grad_kernel, which holds no operand for long, makes a sum again that came
+// with zeros for 64 columns (8192 x 5120 x 10240 of rank 16: 120 us, without 119; gradient of rank
+// 64, 8191 x 5120 x 5120: 167, without 164; smallest calls 0.3 us). lora_grad_kernel, which holds no operand for long, makes a sum again that came
 // out as a NaN.
 __device__ __forceinline__ u32x4 finite(u32x4 m) {
 #pragma unroll
@@ -202,8 +205,8 @@ __device__ __forceinline__ u32x4 finite(u32x4 m) {
 // tile of tokens and part of k, its waves take 128 values of k in turn, and the four
 // sums are added through LDS. MFMA rows are r, columns tokens; both operands go from
 // memory into registers, 64 bytes of a row at a time. Bound by reading x: 8192 x 5120 (84 MB)
-// 23 us warm and 30 to 39 us from memory, of ranks 16 and 64; a kernel that only reads x in this
-// order takes 15.
+// 23 us warm and 30 to 39 us from memory (2.2 to 2.8 TB/s), of ranks 16 and 64; a kernel that only
+// reads x in this order takes 15 us warm.
 template <int RB, int TB>
 __device__ __forceinline__ void rank_sums(const uint16_t* x, const uint16_t* m, const int (&tokens)[4], int R, int K, int first, int step, f32x4 (&acc)[TB][RB]) {
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
@@ -290,8 +293,8 @@ __global__ __launch_bounds__(256, RB <= 2 ? 4 : RB <= 4 ? 2 : 1) void lora_in_ke
 // and then the second parts of f v. Fragments (i, j) of a wave's 64 columns take rows n =
 // 32 i + 8 (m / 4) + 4 j + m % 4, so that a lane ends with two runs of 8 columns of a token,
 // and four lanes have 64 bytes of a row. Bound by base and out: 8192 x 10240 80 us, 335 MB at
-// 4.2 TB/s; a kernel that only copies them in this order takes 70. Of rank 64, 8191 x 5120:
-// 58 us (2.9 TB/s), where every tile also reads b, from L2, as many bytes as base.
+// 4.1 TB/s; a kernel that only copies them in this order takes 70. Of rank 64, 8191 x 5120:
+// 61 us (2.7 TB/s), where every tile also reads b, from L2, as many bytes as base.
 struct LoraOutArgs {
   const float* part;     // [parts, T, R]
   const uint16_t* m;     // [E, N, R]

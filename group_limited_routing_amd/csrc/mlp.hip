@@ -67,10 +67,11 @@ __device__ __forceinline__ float activation(float g, float& d) {
 //   kWeights  d_gate (or d_up) across, x across: a sum over the tokens.
 //
 // Large products are bound by the matrix cores under the chip's power limit: 8192 x 5120 x
-// 10240 (kGated, 1.72e12 operations) takes 1.27 to 1.29 ms, 1.34 PF/s, with the matrix cores
-// busy 76% of the time at 1.5 to 1.65 GHz. The same loop without its loads from memory takes
+// 10240 (kGated, 1.72e12 operations) takes 1.26 to 1.31 ms a call in a row of them (1.3 to 1.4 each
+// under the profiler), 1.31 to 1.36 PF/s, with the matrix cores
+// busy 76% of the time at 1.45 to 1.65 GHz. The same loop without its loads from memory takes
 // 1.14 ms, without reads of LDS 1.19, without both 0.85 (the instructions alone). The
-// gradient's two products at 4096 tokens: 1.31 to 1.38 ms.
+// gradient's two products at 4096 tokens: 1.32 to 1.41 ms, profiled.
 enum Mode { kGated, kInput, kWeights };
 
 struct TileArgs {
@@ -460,7 +461,8 @@ __device__ __forceinline__ void tile_work(const TileArgs& p, int block, int bloc
         auto keep = [&](void* out, auto which) {  // gate (0) or up (1)
           constexpr int W = decltype(which)::value;
           if (!p.pre_f32) return put((uint16_t*)out, [&](int j, int i) { return acc[I][2 * j + W][i]; });
-          // fp32: 32 bytes of a row from two lanes, straight from the sums
+          // fp32: 32 bytes of a row from two lanes, straight from the sums (4096 x 5120 x 10240:
+          // 760 us, with a bf16 pair 690, without 653)
           if (mb + r < p.M)
 #pragma unroll
             for (int j = 0; j < COLS / 32; ++j)
@@ -583,9 +585,11 @@ __global__ __launch_bounds__(64) void finish_kernel(TileArgs p) {
 // How a product is cut. Rounds of 256 PER_CU workgroups take whole tiles; what is left
 // would keep a part of the chip busy for a whole round, so it is cut along k into as many
 // parts as make it cheapest. Costs in ns: a stage of a full round, the parts' way through
-// memory at 2 TB/s, and 5 us for the second kernel. (64 tokens, 5120 x 10240: 160 tiles of
+// memory at 2 TB/s, and 5 us for the second kernel. It is a model: a stage of a partial round is
+// taken to cost as much as a full round's, and each product to have the chip to itself, also where
+// two are launched together. (64 tokens, 5120 x 10240: 160 tiles of
 // the 512 that run at once, cut in 3, 48 us and 5 us for the sums; the weights alone are
-// 42 us at a large copy's rate.)
+// 31 us at 6.9 TB/s.)
 struct Cut {
   int whole, items, splits;
   int64_t cost;
@@ -653,7 +657,7 @@ void tile_launch(const TileArgs& a, const Cut& c, int gelu, hipStream_t st) {
 
 // Tiles of 256 x 256, 128 x 128 and 64 x 128 (columns of w): the one whose cut costs least.
 // A stage of a full round (256, 512 and 512 tiles) takes 1.6, 1.1 and 0.75 us (8192 x 5120 x
-// 10240 by one tile alone: 1.29, 1.76 and 2.37 ms).
+// 10240 by one tile alone: 1.29, 1.76 and 2.37 ms; the gradient's products are given the same).
 constexpr size_t kTileFloats[3] = {256 * 256, 128 * 128, 64 * 128};
 struct Choice {
   int tile;
@@ -790,10 +794,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void gated_few_kernel(GatedArgs p) 
 }
 
 // d_up = dh act(gate), d_gate = dh up act'(gate), 8 values a thread. Rounded to bf16,
-// which is their type as outputs and as operands of the products. Bound by memory: 4096 x
-// 10240 65 to 75 us, 420 MB at 5.6 to 6.4 TB/s. As the products' own operands,
+// which is their type as outputs and as operands of the products: dx and the weights' gradients
+// are then 0.0023 of their norm off, 0.0017 of it by their own rounding. (Two bf16 parts of each
+// would double the products' 1.3 ms.) Bound by memory: 4096 x 10240 64 to 78 us, 420 MB at 5.4 to
+// 6.5 TB/s; from fp32 gate and up 104 us, 587 MB. As the products' own operands,
 // each of their tiles would compute its part again: 20 times with 5120 columns of x.
-// F32: gate and up are fp32.
+// F32: gate and up are fp32. In bf16 they are 2^-8 off, and with them d by 2^-8 |gate act''|, which near
+// a zero of d is all of it.
 template <bool GELU, bool F32>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedBwdArgs p) {
   const int64_t n8 = (int64_t)p.T * p.F / 8, stride = (int64_t)gridDim.x * 256;

@@ -624,7 +624,8 @@ beam_status beam_moe_gated_linear(const beam_moe_gated* cfg, int32_t T, const vo
 
 /*
  * Its gradient, from the stored gate and up:
- *   d_up = dh act(gate);  d_gate = dh up act'(gate), both rounded to bf16, then
+ *   d_up = dh act(gate);  d_gate = dh up act'(gate), both rounded to bf16 (also as the
+ *   operands of the products), then
  *   dx = d_gate w_gate + d_up w_up;  d_w_gate = d_gate^T x;  d_w_up = d_up^T x.
  *   dh, gate, up     [T, intermediate], dh bf16, gate and up as stored (pre_f32);  x,
  *                    w_gate, w_up as above (x only for the weights' gradients, the
@@ -717,7 +718,7 @@ beam_status beam_moe_lora_backward(const beam_moe_lora_config* cfg, int32_t T, c
  * Dropout with a mask that is never stored, and the stream's update with it:
  *   out[i] = keep * stream_in[i] + add * D(x[i]) (without stream_in: add * D(x[i])),
  *   D(x[i]) = x[i] / (1 - q) where u[i] >= 65536 q, else 0 (also for an infinity or a NaN),
- *   q = p rounded to a multiple of 1 / 65536.
+ *   q = p rounded to a multiple of 1 / 65536, each product and the sum in fp32.
  * u[i] are 16 bits of Philox4x32-10 with the 64-bit key `seed` and the counter
  * (i / 8, offset), each 64 bits, low word first: the low half of word (i % 8) / 2 for
  * even i, the high half for odd i. So the mask depends on the seed, the offset and the
